@@ -18,6 +18,8 @@ LIB_PATH = os.environ.get("MOE_OFFLOAD_LIB") or os.path.join(_HERE, "libmoe_offl
 MOE_OK, MOE_E_INVALID, MOE_E_CAPACITY, MOE_E_BUSY, MOE_E_HIP, MOE_E_NOMEM = 0, -1, -2, -3, -4, -5
 MOE_E_HYBRID, MOE_E_SCRATCH = -6, -7
 MOE_FMT_BF16, MOE_FMT_FP8_E4M3_K128, MOE_FMT_MXFP4_K32 = 0, 1, 2
+MOE_T_BF16, MOE_T_FP16, MOE_T_FP32, MOE_T_I8 = 0, 1, 2, 3
+MOE_EPI_NONE, MOE_EPI_SWIGLU = 0, 1
 
 # PyTorch ships its own HIP runtime with the same soname (libamdhip64.so.7).  Loading torch
 # first makes the library's HIP dependency resolve to that already-loaded runtime, so device
@@ -114,6 +116,18 @@ _SIGS = {
     "moe_cpu_expert_rate": (_i32, [ctypes.POINTER(MoeShape), _vp, _i32, _i32, _i32,
                                    ctypes.POINTER(ctypes.c_double)]),
     "moe_profile_read": (_i32, [_vp, ctypes.POINTER(MoeProfile)]),
+    "moe_sort_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_sort_tokens": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp,
+                               _i64, _i32, _vp, _vp, _sz, _vp]),
+    "moe_sort_tokens_grad": (_i32, [_vp, _i64, _i32, _i32, _vp, _i32, _i32, _i32, _vp, _i64,
+                                    _vp]),
+    "moe_combine_tokens": (_i32, [_vp, _i64, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i64,
+                                  _vp]),
+    "moe_combine_tokens_grad": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _i32, _i32,
+                                       _i32, _vp, _i64, _vp, _vp]),
+    "moe_quantise_rows": (_i32, [_vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]),
+    "moe_product_i8": (_i32, [_vp, _i64, _vp, _i32, _i32, _vp, _i64, _vp, _i32, _i32, _vp, _i32,
+                              _vp, _i64, _i32, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_i32]),
     "moe_last_hip_error": (_i32, [_vp]),
 }
@@ -404,6 +418,62 @@ def moe_profile_read(handle: int) -> dict:
     out["gate_up_timed_bytes"] = int(p.gate_up_timed_bytes)
     out["fused_timed_bytes"] = int(p.fused_timed_bytes)
     return out
+
+
+def moe_sort_workspace_bytes(T: int, top_k: int, experts: int) -> int:
+    return int(_lib.moe_sort_workspace_bytes(T, top_k, experts))
+
+
+def moe_sort_tokens(topk_idx, T: int, top_k: int, experts: int, offsets, order, place, x=None,
+                    x_stride: int = 0, hidden: int = 0, x_type: int = MOE_T_BF16, rows=None,
+                    rows_stride: int = 0, rows_type: int = MOE_T_BF16, row_scale=None,
+                    workspace=None, workspace_bytes: int = 0, stream: int = 0) -> None:
+    """Tokens sorted by expert, their rows copied or quantised (see the header)."""
+    _check(_lib.moe_sort_tokens(_p(topk_idx), T, top_k, experts, _p(offsets), _p(order),
+                                _p(place), _p(x), x_stride, hidden, x_type, _p(rows),
+                                rows_stride, rows_type, _p(row_scale), _p(workspace),
+                                workspace_bytes, stream), "moe_sort_tokens")
+
+
+def moe_sort_tokens_grad(drows, drows_stride: int, n_rows: int, type: int, place, T: int,
+                         top_k: int, hidden: int, dx, dx_stride: int, stream: int = 0) -> None:
+    """dx[t] = sum of drows at the token's places (see the header)."""
+    _check(_lib.moe_sort_tokens_grad(_p(drows), drows_stride, n_rows, type, _p(place), T, top_k,
+                                     hidden, _p(dx), dx_stride, stream), "moe_sort_tokens_grad")
+
+
+def moe_combine_tokens(rows, rows_stride: int, n_rows: int, type: int, place, weights, T: int,
+                       top_k: int, hidden: int, out, out_stride: int, stream: int = 0) -> None:
+    """Sorted rows back to tokens with the routing weights applied (see the header)."""
+    _check(_lib.moe_combine_tokens(_p(rows), rows_stride, n_rows, type, _p(place), _p(weights),
+                                   T, top_k, hidden, _p(out), out_stride, stream),
+           "moe_combine_tokens")
+
+
+def moe_combine_tokens_grad(dout, dout_stride: int, rows, rows_stride: int, n_rows: int,
+                            type: int, place, weights, T: int, top_k: int, hidden: int, drows,
+                            drows_stride: int, dweights, stream: int = 0) -> None:
+    """Gradients of moe_combine_tokens for the rows and the weights (see the header)."""
+    _check(_lib.moe_combine_tokens_grad(_p(dout), dout_stride, _p(rows), rows_stride, n_rows,
+                                        type, _p(place), _p(weights), T, top_k, hidden,
+                                        _p(drows), drows_stride, _p(dweights), stream),
+           "moe_combine_tokens_grad")
+
+
+def moe_quantise_rows(x, x_stride: int, type: int, M: int, K: int, codes, codes_stride: int,
+                      scale, rows_end=None, stream: int = 0) -> None:
+    """8-bit codes and one scale for each row (see the header)."""
+    _check(_lib.moe_quantise_rows(_p(x), x_stride, type, M, K, _p(codes), codes_stride,
+                                  _p(scale), _p(rows_end), stream), "moe_quantise_rows")
+
+
+def moe_product_i8(a, a_stride: int, a_scale, M: int, K: int, w, w_stride: int, w_scale, N: int,
+                   groups: int, offsets, epilogue: int, out, out_stride: int, out_type: int,
+                   stream: int = 0) -> None:
+    """Product of 8-bit integers with scales per row and channel (see the header)."""
+    _check(_lib.moe_product_i8(_p(a), a_stride, _p(a_scale), M, K, _p(w), w_stride, _p(w_scale),
+                               N, groups, _p(offsets), epilogue, _p(out), out_stride, out_type,
+                               stream), "moe_product_i8")
 
 
 def moe_status_string(status: int) -> str:

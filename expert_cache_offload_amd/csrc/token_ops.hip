@@ -1,0 +1,609 @@
+// Tokens sorted by expert and back, with routing weights, their gradients, and the 8-bit
+// quantisation of rows.
+//
+// With id[a] the expert of assignment a = t * k + j (choice j of token t), the sort is stable by
+// expert: place[a] = #{b : id[b] < id[a]} + #{b < a : id[b] = id[a]} over the assignments whose
+// id is in [0, E); the others are dropped (place -1).  Row place[a] of the sorted matrix is
+// token t's row.  Back: y[t] = sum_j w[t][j] * rows[place[t][j]].  Gradients: of the sort, the same
+// sum with w = 1; of the sum, drows[place[a]] = w[a] dy[t] and dw[a] = <dy[t], rows[place[a]]>.
+//
+// All of it is movement: every kernel is bound by the bytes of the rows it reads and writes.
+// Every count is an integer from ballots, so nothing depends on the order of execution.
+#include "row_ops.h"
+
+namespace moe {
+namespace {
+
+constexpr int TOK_T = 256;          // threads of every kernel here but the scan
+constexpr int kSmallIds = 4096;     // assignments that one kernel sorts (each workgroup counts
+                                    // all of them for the ids of its own token)
+constexpr int kMaxTopK = 16;
+constexpr int kMaxExperts = 1024;
+constexpr int kChunkIds = 1024;     // assignments of a counted chunk (whole tokens)
+constexpr int kChunkWaves = kChunkIds / 64;
+constexpr int kSubTokens = 16;      // tokens a workgroup of the move kernel sorts and moves
+constexpr int kMaxT = 1 << 20;
+constexpr int SCAN_T = 1024;
+
+struct SortArgs {
+  const int* ids;
+  int T, k, E, N;
+  const void* x;  // null: integers only
+  int64_t xs;
+  int H;
+  int* offsets;
+  int* order;  // may be null
+  int* place;
+  void* rows;
+  int64_t rs;
+  float* row_scale;
+  int* base;    // [nblk][E] counts of each chunk, then the first place of each (chunk, expert)
+  int tok_blk;  // tokens of a chunk
+  int nblk;
+};
+
+// Dropped assignments get a key above every expert's.
+__device__ __forceinline__ int key_of_id(int id, int E) {
+  return (unsigned)id < (unsigned)E ? id : 0x7fffffff;
+}
+
+// Copies one row of H elements to k rows of the sorted matrix, threads [tid, nthr) of it over
+// columns [c0, c1) in chunks.
+template <class E>
+__device__ __forceinline__ void copy_row(const E* x, int H, const int* place, int k, E* rows,
+                                         int64_t rs, int c0, int c1, int tid, int nthr) {
+  constexpr int V = Chunk<E>::V;
+  for (int c = c0 + tid; c < c1; c += nthr) {
+    const int n = H - c * V;
+    const Chunk<E> v = load_chunk(x + (int64_t)c * V, n);
+    for (int j = 0; j < k; ++j) {
+      const int p = place[j];
+      if (p >= 0) store_chunk(rows + (int64_t)p * rs + (int64_t)c * V, n, v);
+    }
+  }
+}
+
+// The same with the row's 8-bit codes.
+template <class E>
+__device__ __forceinline__ void quant_row_to(const E* x, int H, const RowQuant& r,
+                                             const int* place, int k, int8_t* rows, int64_t rs,
+                                             float* row_scale, int tid, int nthr) {
+  constexpr int V = Chunk<E>::V;
+  const int nc = (H + V - 1) / V;
+  for (int c = tid; c < nc; c += nthr) {
+    const int n = H - c * V;
+    const Chunk<E> v = load_chunk(x + (int64_t)c * V, n);
+    for (int j = 0; j < k; ++j) {
+      const int p = place[j];
+      if (p >= 0) store_codes(rows + (int64_t)p * rs + (int64_t)c * V, n, v, r);
+    }
+  }
+  if (tid < k && place[tid] >= 0) row_scale[place[tid]] = r.scale;
+}
+
+template <class E>
+__device__ __forceinline__ uint32_t row_max_bits(const E* x, int H, int tid, int nthr) {
+  constexpr int V = Chunk<E>::V;
+  const int nc = (H + V - 1) / V;
+  uint32_t m = 0;
+  for (int c = tid; c < nc; c += nthr)
+    m = chunk_max_bits(load_chunk(x + (int64_t)c * V, H - c * V), m);
+  return m;
+}
+
+// offsets[0..E] from per-expert totals in LDS, one workgroup of nthr threads.
+__device__ void write_offsets(const int* total, int E, int* offsets, int* s_wave, int tid,
+                              int nthr) {
+  const int per = (E + nthr - 1) / nthr;
+  int sum = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < E) sum += total[e];
+  }
+  int inc = sum;  // inclusive over the lanes of the wave
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const int o = __shfl_up(inc, s);
+    if ((tid & 63) >= s) inc += o;
+  }
+  if ((tid & 63) == 63) s_wave[tid >> 6] = inc;
+  __syncthreads();
+  int first = inc - sum;
+  for (int w = 0; w < (tid >> 6); ++w) first += s_wave[w];
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < E) {
+      offsets[e] = first;
+      first += total[e];
+      if (e == E - 1) offsets[E] = first;
+    }
+  }
+}
+
+// Few assignments: one launch.  Workgroup (t, y) counts, over all N ids, those before each of
+// token t's k assignments (a wave takes 64 ids at a time and adds up ballots), and moves column
+// slice y of the token's row; workgroup (T, 0) writes the offsets.  Latency is what it costs: one
+// read of the ids (L2), one barrier, one read and k writes of the row.
+template <class E, bool I8>
+__global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
+  __shared__ int s_cnt[TOK_T / 64][kMaxTopK];
+  __shared__ int s_place[kMaxTopK];
+  __shared__ int s_hist[kMaxExperts];
+  __shared__ int s_wave[TOK_T / 64];
+  __shared__ uint32_t s_max[TOK_T / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int t = blockIdx.x;
+  if (t == a.T) {
+    if (blockIdx.y != 0) return;
+    for (int e = tid; e < a.E; e += TOK_T) s_hist[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.N; i += TOK_T) {
+      const int id = a.ids[i];
+      if ((unsigned)id < (unsigned)a.E) atomicAdd(&s_hist[id], 1);
+    }
+    __syncthreads();
+    write_offsets(s_hist, a.E, a.offsets, s_wave, tid, TOK_T);
+    return;
+  }
+  const E* x = (const E*)a.x + (int64_t)t * a.xs;
+  uint32_t mb = 0;
+  if constexpr (I8) mb = wave_max_u32(row_max_bits(x, a.H, tid, TOK_T));
+  int own[kMaxTopK], cnt[kMaxTopK];
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    own[j] = j < a.k ? key_of_id(a.ids[t * a.k + j], a.E) : 0;
+    cnt[j] = 0;
+  }
+  for (int i0 = wave * 64; i0 < a.N; i0 += TOK_T) {
+    const int i = i0 + lane;
+    const int key = i < a.N ? key_of_id(a.ids[i], a.E) : 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j)
+      if (j < a.k)
+        cnt[j] += __popcll(__ballot(key < own[j] || (key == own[j] && i < t * a.k + j)));
+  }
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j)
+    if (j < a.k && lane == 0) s_cnt[wave][j] = cnt[j];
+  if (lane == 0) s_max[wave] = mb;
+  __syncthreads();
+  if (tid < a.k) {
+    int p = 0;
+#pragma unroll
+    for (int w = 0; w < TOK_T / 64; ++w) p += s_cnt[w][tid];
+    const int at = t * a.k + tid;
+    if ((unsigned)a.ids[at] >= (unsigned)a.E) p = -1;
+    s_place[tid] = p;
+    if (blockIdx.y == 0) {
+      a.place[at] = p;
+      if (a.order && p >= 0) a.order[p] = at;
+    }
+  }
+  __syncthreads();
+  if (!a.x) return;
+  if constexpr (I8) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < TOK_T / 64; ++w) m = m > s_max[w] ? m : s_max[w];
+    quant_row_to(x, a.H, row_quant(m), s_place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, tid,
+                 TOK_T);
+  } else {
+    const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
+    const int per = (nc + gridDim.y - 1) / gridDim.y;
+    const int c0 = blockIdx.y * per, c1 = min(nc, c0 + per);
+    copy_row(x, a.H, s_place, a.k, (E*)a.rows, a.rs, c0, c1, tid, TOK_T);
+  }
+}
+
+// Many assignments, first of three launches: the ids of each chunk counted by expert.
+__global__ __launch_bounds__(TOK_T) void sort_count_kernel(SortArgs a) {
+  __shared__ int s_hist[kMaxExperts];
+  const int b = blockIdx.x;
+  for (int e = threadIdx.x; e < a.E; e += TOK_T) s_hist[e] = 0;
+  __syncthreads();
+  const int i1 = min(a.N, (b + 1) * a.tok_blk * a.k);
+  for (int i = b * a.tok_blk * a.k + threadIdx.x; i < i1; i += TOK_T) {
+    const int id = a.ids[i];
+    if ((unsigned)id < (unsigned)a.E) atomicAdd(&s_hist[id], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += TOK_T) a.base[(int64_t)b * a.E + e] = s_hist[e];
+}
+
+// Second: one workgroup turns the counts into first places.  Thread (g, e) adds up a segment g of
+// the chunks of expert e, the segments and then the experts are scanned, and a second pass over
+// the counts writes the running place.
+__global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
+  __shared__ int s_seg[SCAN_T];
+  __shared__ int s_total[kMaxExperts];
+  __shared__ int s_off[kMaxExperts + 1];
+  __shared__ int s_wave[SCAN_T / 64];
+  int ep = 1;  // experts rounded up to a power of two
+  while (ep < a.E) ep <<= 1;
+  const int nseg = SCAN_T / ep, e = threadIdx.x & (ep - 1), g = threadIdx.x / ep;
+  const int per = (a.nblk + nseg - 1) / nseg;
+  const int b0 = min(a.nblk, g * per), b1 = min(a.nblk, b0 + per);
+  int sum = 0;
+  if (e < a.E)
+    for (int b = b0; b < b1; ++b) sum += a.base[(int64_t)b * a.E + e];
+  s_seg[threadIdx.x] = sum;
+  __syncthreads();
+  if (g == 0 && e < a.E) {
+    int run = 0;
+    for (int s = 0; s < nseg; ++s) {
+      const int v = s_seg[s * ep + e];
+      s_seg[s * ep + e] = run;
+      run += v;
+    }
+    s_total[e] = run;
+  }
+  __syncthreads();
+  write_offsets(s_total, a.E, s_off, s_wave, threadIdx.x, SCAN_T);
+  __syncthreads();
+  for (int i = threadIdx.x; i <= a.E; i += SCAN_T) a.offsets[i] = s_off[i];
+  if (e < a.E) {
+    int run = s_off[e] + s_seg[threadIdx.x];
+    for (int b = b0; b < b1; ++b) {
+      const int64_t i = (int64_t)b * a.E + e;
+      const int v = a.base[i];
+      a.base[i] = run;
+      run += v;
+    }
+  }
+}
+
+// Third: a workgroup takes kSubTokens tokens of a chunk, ranks the chunk's ids up to its own last
+// one (a wave finds the lanes that hold its id by ballots over the id's bits; counts per wave and
+// expert in LDS), writes their places and moves their rows, a wave per token.
+template <class E, bool I8>
+__global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int subs) {
+  extern __shared__ __align__(16) uint16_t s_cnt[];  // [kChunkWaves][E]
+  __shared__ int s_id[kSubTokens * kMaxTopK], s_rank[kSubTokens * kMaxTopK];
+  __shared__ int s_place[kSubTokens * kMaxTopK];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int b = blockIdx.x / subs, sub = blockIdx.x % subs;
+  const int t_blk = b * a.tok_blk;
+  const int t0 = t_blk + sub * kSubTokens;
+  const int t1 = min(min(a.T, t_blk + a.tok_blk), t0 + kSubTokens);
+  if (t0 >= t1) return;
+  const int first = t_blk * a.k, own0 = (t0 - t_blk) * a.k, own1 = (t1 - t_blk) * a.k;
+  const int waves = (own1 + 63) / 64;
+  for (int i = tid; i < waves * a.E; i += TOK_T) s_cnt[i] = 0;
+  __syncthreads();
+  for (int it = wave; it < waves; it += TOK_T / 64) {
+    const int i = it * 64 + lane;
+    const int id = i < own1 ? a.ids[first + i] : -1;
+    const bool ok = (unsigned)id < (unsigned)a.E;
+    uint64_t same = __ballot(ok);
+    for (int bit = 0; (a.E - 1) >> bit; ++bit) {
+      const uint64_t set = __ballot((id >> bit) & 1);
+      same &= (id >> bit) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & lanemask_lt());
+    if (ok && rank == 0) s_cnt[it * a.E + id] = (uint16_t)__popcll(same);
+    if (i >= own0 && i < own1) {
+      s_id[i - own0] = ok ? id : -1;
+      s_rank[i - own0] = rank;
+    }
+  }
+  __syncthreads();
+  if (tid < own1 - own0) {
+    const int i = own0 + tid, id = s_id[tid];
+    int p = -1;
+    if (id >= 0) {
+      p = a.base[(int64_t)b * a.E + id] + s_rank[tid];
+      for (int it = 0; it < i / 64; ++it) p += s_cnt[it * a.E + id];
+      if (a.order) a.order[p] = first + i;
+    }
+    a.place[first + i] = p;
+    s_place[tid] = p;
+  }
+  __syncthreads();
+  if (!a.x) return;
+  for (int t = t0 + wave; t < t1; t += TOK_T / 64) {
+    const E* x = (const E*)a.x + (int64_t)t * a.xs;
+    const int* place = s_place + (t - t0) * a.k;
+    if constexpr (I8) {
+      const RowQuant r = row_quant(wave_max_u32(row_max_bits(x, a.H, lane, 64)));
+      quant_row_to(x, a.H, r, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, lane, 64);
+    } else {
+      const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
+      copy_row(x, a.H, place, a.k, (E*)a.rows, a.rs, 0, nc, lane, 64);
+    }
+  }
+}
+
+struct CombineArgs {
+  const void* rows;
+  int64_t rs;
+  int n_rows;
+  const int* place;
+  const float* w;  // null: 1
+  int T, k, H;
+  void* out;
+  int64_t os;
+  int tpt_log;  // log2 of the threads per token
+};
+
+// y[t] = sum_j w[t][j] rows[place[t][j]], fp32, j ascending, rounded once.  A thread holds one
+// 16-byte chunk of one token's row; 2^tpt_log threads share a token.
+template <class E, bool W>
+__global__ __launch_bounds__(TOK_T) void combine_kernel(CombineArgs a) {
+  constexpr int V = Chunk<E>::V;
+  const int64_t g = (int64_t)blockIdx.x * TOK_T + threadIdx.x;
+  const int t = (int)(g >> a.tpt_log);
+  const int c = (int)(g & ((1 << a.tpt_log) - 1)) + ((int)blockIdx.y << a.tpt_log);
+  const int n = a.H - c * V;
+  if (t >= a.T || n <= 0) return;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  const int* place = a.place + (int64_t)t * a.k;
+  const float* w = W ? a.w + (int64_t)t * a.k : nullptr;
+  const E* rows = (const E*)a.rows + (int64_t)c * V;
+  for (int j = 0; j < a.k; ++j) {
+    const int p = place[j];
+    if ((unsigned)p >= (unsigned)a.n_rows) continue;
+    const Chunk<E> v = load_chunk(rows + (int64_t)p * a.rs, n);
+    const float wj = W ? w[j] : 1.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = W ? fmaf(wj, to_f32(v.e[i]), acc[i])
+                                           : acc[i] + to_f32(v.e[i]);
+  }
+  Chunk<E> o;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o.e[i] = from_f32<E>(acc[i]);
+  store_chunk((E*)a.out + (int64_t)t * a.os + (int64_t)c * V, n, o);
+}
+
+struct CombineGradArgs {
+  const void* dout;
+  int64_t ds;
+  const void* rows;  // null without dw
+  int64_t rs;
+  int n_rows;
+  const int* place;
+  const float* w;  // null: 1
+  int T, k, H;
+  void* drows;  // may be null
+  int64_t drs;
+  float* dw;  // may be null
+};
+
+// A wave per assignment: drows[p] = w dy, dw = <dy, rows[p]> (fp32 products, per-lane partial
+// sums joined by shuffles in a fixed order).  The waves of a token read its dy row together.
+template <class E>
+__global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) {
+  constexpr int V = Chunk<E>::V;
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * (TOK_T / 64) + (threadIdx.x >> 6);
+  if (at >= (int64_t)a.T * a.k) return;
+  const int p = a.place[at];
+  if ((unsigned)p >= (unsigned)a.n_rows) {
+    if (a.dw && lane == 0) a.dw[at] = 0.f;
+    return;
+  }
+  const float w = a.w ? a.w[at] : 1.f;
+  const E* dy = (const E*)a.dout + at / a.k * a.ds;
+  const E* r = (const E*)a.rows + (int64_t)p * a.rs;
+  E* dr = (E*)a.drows + (int64_t)p * a.drs;
+  const int nc = (a.H + V - 1) / V;
+  float sum = 0.f;
+  for (int c = lane; c < nc; c += 64) {
+    const int n = a.H - c * V;
+    const Chunk<E> g = load_chunk(dy + (int64_t)c * V, n);
+    if (a.dw) {
+      const Chunk<E> v = load_chunk(r + (int64_t)c * V, n);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum = fmaf(to_f32(g.e[i]), to_f32(v.e[i]), sum);
+    }
+    if (a.drows) {
+      Chunk<E> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o.e[i] = from_f32<E>(w * to_f32(g.e[i]));
+      store_chunk(dr + (int64_t)c * V, n, o);
+    }
+  }
+  if (a.dw) {
+    sum = wave_sum(sum);
+    if (lane == 0) a.dw[at] = sum;
+  }
+}
+
+struct QuantArgs {
+  const void* x;
+  int64_t xs;
+  int M, K;
+  int8_t* codes;
+  int64_t cs;
+  float* scale;
+  const int* rows_end;  // may be null
+};
+
+// A wave per row: the maximum, then the codes (the second read of the row hits the cache).
+template <class E>
+__global__ __launch_bounds__(TOK_T) void quantise_kernel(QuantArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int row = blockIdx.x * (TOK_T / 64) + (threadIdx.x >> 6);
+  if (row >= a.M || (a.rows_end && row >= *a.rows_end)) return;
+  const E* x = (const E*)a.x + (int64_t)row * a.xs;
+  const RowQuant r = row_quant(wave_max_u32(row_max_bits(x, a.K, lane, 64)));
+  constexpr int V = Chunk<E>::V;
+  const int nc = (a.K + V - 1) / V;
+  int8_t* codes = a.codes + (int64_t)row * a.cs;
+  for (int c = lane; c < nc; c += 64) {
+    const int n = a.K - c * V;
+    store_codes(codes + (int64_t)c * V, n, load_chunk(x + (int64_t)c * V, n), r);
+  }
+  if (lane == 0) a.scale[row] = r.scale;
+}
+
+// ------------------------------------------------------------------ host side
+
+bool tokens_ok(int T, int k, int E) {
+  return T >= 0 && T <= kMaxT && k >= 1 && k <= kMaxTopK && E >= 1 && E <= kMaxExperts;
+}
+bool float_type(int type) { return type >= MOE_T_BF16 && type <= MOE_T_FP32; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
+constexpr int kMaxCols = 1 << 20;
+
+int chunk_tokens(int k) { return kChunkIds / k; }
+int chunk_count(int T, int k) { return (T + chunk_tokens(k) - 1) / chunk_tokens(k); }
+
+template <class E, bool I8>
+void launch_sort(SortArgs& a, hipStream_t s) {
+  if (a.N <= kSmallIds) {
+    const int slices = I8 || !a.x ? 1 : (a.H + 64 * Chunk<E>::V * 4 - 1) / (64 * Chunk<E>::V * 4);
+    hipLaunchKernelGGL((sort_small_kernel<E, I8>), dim3(a.T + 1, min(slices, 64)), dim3(TOK_T), 0,
+                       s, a);
+    return;
+  }
+  hipLaunchKernelGGL(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
+  hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
+  const int subs = (a.tok_blk + kSubTokens - 1) / kSubTokens;
+  hipLaunchKernelGGL((sort_move_kernel<E, I8>), dim3(a.nblk * subs), dim3(TOK_T),
+                     (size_t)kChunkWaves * a.E * 2, s, a, subs);
+}
+
+template <class E>
+void launch_combine(CombineArgs& a, hipStream_t s) {
+  constexpr int V = Chunk<E>::V;
+  const int nc = (a.H + V - 1) / V;
+  a.tpt_log = 0;
+  while (a.tpt_log < 8 && (1 << a.tpt_log) < nc) ++a.tpt_log;
+  const int64_t thr = (int64_t)a.T << a.tpt_log;
+  const dim3 grid((unsigned)((thr + TOK_T - 1) / TOK_T),
+                  (unsigned)((nc + (1 << a.tpt_log) - 1) >> a.tpt_log));
+  if (a.w)
+    hipLaunchKernelGGL((combine_kernel<E, true>), grid, dim3(TOK_T), 0, s, a);
+  else
+    hipLaunchKernelGGL((combine_kernel<E, false>), grid, dim3(TOK_T), 0, s, a);
+}
+
+moe_status combine(const void* rows, int64_t rs, int n_rows, int type, const int* place,
+                   const float* w, int T, int k, int H, void* out, int64_t os, hipStream_t s) {
+  if (!float_type(type) || !tokens_ok(T, k, 1) || H < 1 || H > kMaxCols || n_rows < 0 || !place ||
+      !aligned4(place) || !aligned4(w) || !rows_ok(out, os, H, type) ||
+      (n_rows > 0 && !rows_ok(rows, rs, H, type)) || !on_current_device(out))
+    return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;
+  CombineArgs a{rows, rs, n_rows, place, w, T, k, H, out, os, 0};
+  if (type == MOE_T_BF16)
+    launch_combine<bf16_t>(a, s);
+  else if (type == MOE_T_FP16)
+    launch_combine<fp16_t>(a, s);
+  else
+    launch_combine<float>(a, s);
+  return launched();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_sort_workspace_bytes(int32_t T, int32_t top_k, int32_t experts) {
+  if (!tokens_ok(T, top_k, experts) || T * top_k <= kSmallIds) return 0;
+  return sizeof(int) * (size_t)chunk_count(T, top_k) * (size_t)experts;
+}
+
+moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, int32_t experts,
+                           int32_t* offsets, int32_t* order, int32_t* place, const void* x,
+                           int64_t x_stride, int32_t hidden, int32_t x_type, void* rows,
+                           int64_t rows_stride, int32_t rows_type, float* row_scale,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (!tokens_ok(T, top_k, experts) || !offsets || !aligned4(offsets) || !aligned4(order))
+    return MOE_E_INVALID;
+  if (T > 0 && (!topk_idx || !place || !aligned4(topk_idx) || !aligned4(place)))
+    return MOE_E_INVALID;
+  if ((x == nullptr) != (rows == nullptr)) return MOE_E_INVALID;
+  const bool i8 = x && rows_type == MOE_T_I8;
+  if (x) {
+    if (!float_type(x_type) || (rows_type != x_type && !i8) || hidden < 1 || hidden > kMaxCols ||
+        !rows_ok(x, x_stride, hidden, x_type) || !rows_ok(rows, rows_stride, hidden, rows_type))
+      return MOE_E_INVALID;
+    if (i8 && (!row_scale || !aligned4(row_scale))) return MOE_E_INVALID;
+  }
+  const size_t need = moe_sort_workspace_bytes(T, top_k, experts);
+  if (need && (!workspace || !aligned4(workspace))) return MOE_E_INVALID;
+  if (workspace_bytes < need) return MOE_E_SCRATCH;
+  if (!on_current_device(offsets)) return MOE_E_INVALID;
+  SortArgs a{topk_idx, T,       top_k, experts, T * top_k, x,
+             x_stride, hidden,  offsets, order, place,     rows,
+             rows_stride, row_scale, (int*)workspace, chunk_tokens(top_k), chunk_count(T, top_k)};
+  const hipStream_t s = (hipStream_t)stream;
+  const int type = x ? x_type : MOE_T_FP32;
+  if (type == MOE_T_BF16)
+    i8 ? launch_sort<bf16_t, true>(a, s) : launch_sort<bf16_t, false>(a, s);
+  else if (type == MOE_T_FP16)
+    i8 ? launch_sort<fp16_t, true>(a, s) : launch_sort<fp16_t, false>(a, s);
+  else
+    i8 ? launch_sort<float, true>(a, s) : launch_sort<float, false>(a, s);
+  return launched();
+}
+
+moe_status moe_sort_tokens_grad(const void* drows, int64_t drows_stride, int32_t n_rows,
+                                int32_t type, const int32_t* place, int32_t T, int32_t top_k,
+                                int32_t hidden, void* dx, int64_t dx_stride, void* stream) {
+  return combine(drows, drows_stride, n_rows, type, place, nullptr, T, top_k, hidden, dx,
+                 dx_stride, (hipStream_t)stream);
+}
+
+moe_status moe_combine_tokens(const void* rows, int64_t rows_stride, int32_t n_rows, int32_t type,
+                              const int32_t* place, const float* weights, int32_t T,
+                              int32_t top_k, int32_t hidden, void* out, int64_t out_stride,
+                              void* stream) {
+  if (!weights) return MOE_E_INVALID;
+  return combine(rows, rows_stride, n_rows, type, place, weights, T, top_k, hidden, out,
+                 out_stride, (hipStream_t)stream);
+}
+
+moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const void* rows,
+                                   int64_t rows_stride, int32_t n_rows, int32_t type,
+                                   const int32_t* place, const float* weights, int32_t T,
+                                   int32_t top_k, int32_t hidden, void* drows,
+                                   int64_t drows_stride, float* dweights, void* stream) {
+  if (!float_type(type) || !tokens_ok(T, top_k, 1) || hidden < 1 || hidden > kMaxCols ||
+      n_rows < 0 || !place || !weights || !aligned4(place) || !aligned4(weights) ||
+      !aligned4(dweights) || (!drows && !dweights) || !rows_ok(dout, dout_stride, hidden, type) ||
+      (drows && !rows_ok(drows, drows_stride, hidden, type)) ||
+      (dweights && n_rows > 0 && !rows_ok(rows, rows_stride, hidden, type)) ||
+      !on_current_device(dout))
+    return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;
+  CombineGradArgs a{dout, dout_stride, rows, rows_stride, n_rows, place, weights, T,
+                    top_k, hidden, drows, drows_stride, dweights};
+  const hipStream_t s = (hipStream_t)stream;
+  const dim3 grid((unsigned)((T * top_k + TOK_T / 64 - 1) / (TOK_T / 64)));
+  if (type == MOE_T_BF16)
+    hipLaunchKernelGGL(combine_grad_kernel<bf16_t>, grid, dim3(TOK_T), 0, s, a);
+  else if (type == MOE_T_FP16)
+    hipLaunchKernelGGL(combine_grad_kernel<fp16_t>, grid, dim3(TOK_T), 0, s, a);
+  else
+    hipLaunchKernelGGL(combine_grad_kernel<float>, grid, dim3(TOK_T), 0, s, a);
+  return launched();
+}
+
+moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
+                             int8_t* codes, int64_t codes_stride, float* scale,
+                             const int32_t* rows_end, void* stream) {
+  if (!float_type(type) || M < 0 || K < 1 || K > kMaxCols || !rows_ok(x, x_stride, K, type) ||
+      !rows_ok(codes, codes_stride, K, MOE_T_I8) || !scale || !aligned4(scale) ||
+      !aligned4(rows_end) || !on_current_device(codes))
+    return MOE_E_INVALID;
+  if (M == 0) return MOE_OK;
+  QuantArgs a{x, x_stride, M, K, codes, codes_stride, scale, rows_end};
+  const hipStream_t s = (hipStream_t)stream;
+  const dim3 grid((unsigned)(((int64_t)M + TOK_T / 64 - 1) / (TOK_T / 64)));
+  if (type == MOE_T_BF16)
+    hipLaunchKernelGGL(quantise_kernel<bf16_t>, grid, dim3(TOK_T), 0, s, a);
+  else if (type == MOE_T_FP16)
+    hipLaunchKernelGGL(quantise_kernel<fp16_t>, grid, dim3(TOK_T), 0, s, a);
+  else
+    hipLaunchKernelGGL(quantise_kernel<float>, grid, dim3(TOK_T), 0, s, a);
+  return launched();
+}
+
+}  // extern "C"

@@ -385,6 +385,101 @@ moe_status moe_probe_empty_launch(int32_t grid, int32_t reps, void* stream, doub
 moe_status moe_probe_copy(const void* src, void* dst, uint64_t bytes, int32_t reps, void* stream,
                           double* avg_us);
 
+/* ---------------------------------------------------------------- operators on device buffers
+ *
+ * The expert layer's token movement and an 8-bit integer product, as calls of their own: for
+ * experts that live outside a handle (kept resident, in 8-bit integers, or in training).  They
+ * need no handle and keep nothing between calls.  Conventions as above, and:
+ *  - a matrix is a pointer to its first element and the distance of its rows in elements (at
+ *    least its width); rows may start at any element: no alignment beyond the element's own is
+ *    asked for, 16-byte aligned rows are the fast ones;
+ *  - element types MOE_T_*; sums are held in fp32 (32-bit integers in the 8-bit product) and a
+ *    16-bit output is rounded once, to nearest even;
+ *  - buffers live on the current device and `stream` is one of its streams; outputs do not
+ *    overlap inputs or each other (not checked); a buffer is free for other use once the
+ *    stream has passed the call;
+ *  - every argument check is made before anything is enqueued; MOE_E_HIP when a launch fails;
+ *  - results do not depend on timing: the same inputs give the same bits. */
+#define MOE_T_BF16 0
+#define MOE_T_FP16 1
+#define MOE_T_FP32 2
+#define MOE_T_I8 3 /* 8-bit codes; the scales are an array of their own */
+
+/* Workspace bytes of moe_sort_tokens (0: none needed, or unsupported sizes).  The workspace is in use
+ * until the stream has passed the call and holds nothing afterwards: calls that may run at
+ * the same time (two streams, two graphs replayed side by side) need one each. */
+size_t moe_sort_workspace_bytes(int32_t T, int32_t top_k, int32_t experts);
+
+/* Tokens sorted by expert.  topk_idx: [T][top_k] expert ids as a route step writes them; an id
+ * outside [0, experts) - an expert of another rank, a masked choice - drops its assignment.
+ * The sort is stable: by expert, then by token, then by choice; an expert may appear twice in a
+ * token.  Writes
+ *   offsets [experts + 1]: first sorted row of each expert, offsets[experts] = n rows in all;
+ *   order [n of T*top_k]: assignment t*top_k + j of each sorted row (may be NULL);
+ *   place [T][top_k]: sorted row of each assignment, -1 where dropped;
+ *   rows [n of T*top_k][hidden]: token t's row of x at each of its places (x and rows NULL: the
+ *     integers only).  rows_type: x_type (copied) or MOE_T_I8 (codes as moe_quantise_rows
+ *     gives them, scales in row_scale [n of T*top_k], else ignored).
+ * Entries of order, rows and row_scale from n on are left as they were.
+ * T 0..1048576, top_k 1..16, experts 1..1024, hidden 1..1048576, x_type bf16, fp16 or fp32.
+ * MOE_E_SCRATCH when workspace_bytes is below moe_sort_workspace_bytes. */
+moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, int32_t experts,
+                           int32_t* offsets, int32_t* order, int32_t* place, const void* x,
+                           int64_t x_stride, int32_t hidden, int32_t x_type, void* rows,
+                           int64_t rows_stride, int32_t rows_type, float* row_scale,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the sort for x: dx[t] = sum over j of drows[place[t][j]], j ascending, for the
+ * n_rows rows of drows; a place outside [0, n_rows) adds nothing (a token without any: zeros). */
+moe_status moe_sort_tokens_grad(const void* drows, int64_t drows_stride, int32_t n_rows,
+                                int32_t type, const int32_t* place, int32_t T, int32_t top_k,
+                                int32_t hidden, void* dx, int64_t dx_stride, void* stream);
+
+/* Sorted rows back to tokens: out[t] = sum over j of weights[t][j] * rows[place[t][j]], j
+ * ascending.  A place outside [0, n_rows) adds nothing, whatever its weight holds; a token
+ * without any gets zeros.  weights: [T][top_k] fp32.  Sizes as moe_sort_tokens. */
+moe_status moe_combine_tokens(const void* rows, int64_t rows_stride, int32_t n_rows, int32_t type,
+                              const int32_t* place, const float* weights, int32_t T,
+                              int32_t top_k, int32_t hidden, void* out, int64_t out_stride,
+                              void* stream);
+
+/* Gradients of moe_combine_tokens: drows[place[t][j]] = weights[t][j] * dout[t] (rows that no
+ * assignment has are left as they were) and dweights[t][j] = <dout[t], rows[place[t][j]]>, 0
+ * where dropped.  drows or dweights may be NULL, rows too where dweights is.  The places in
+ * [0, n_rows) have to be distinct, as moe_sort_tokens writes them. */
+moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const void* rows,
+                                   int64_t rows_stride, int32_t n_rows, int32_t type,
+                                   const int32_t* place, const float* weights, int32_t T,
+                                   int32_t top_k, int32_t hidden, void* drows,
+                                   int64_t drows_stride, float* dweights, void* stream);
+
+/* 8-bit quantisation of the M rows of x [M][K] (bf16, fp16 or fp32): with m the row's largest
+ * magnitude, scale = m / 127 (fp32) and code = 127 x / m to the nearest integer, ties to even,
+ * exactly.  A row of zeros has scale 0; a row that holds a NaN or an infinity has scale NaN and
+ * codes 0.  rows_end: NULL, or a device word: rows from *rows_end on are not read and their
+ * outputs left as they were (offsets + experts of a sort).  K 1..1048576. */
+moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
+                             int8_t* codes, int64_t codes_stride, float* scale,
+                             const int32_t* rows_end, void* stream);
+
+/* Product of 8-bit integers with a scale per row and per channel:
+ *   c[m][n] = (sum over k of a[m][k] * w[g][n][k]) * a_scale[m] * w_scale[g][n]
+ * a: [M][K] codes; w: [groups][N][K] codes, w_stride from channel to channel (group g at
+ * w + g * N * w_stride); w_scale: [groups][N].  offsets NULL: one group (groups = 1) and all
+ * M rows; else device words [groups + 1], rows offsets[g] .. offsets[g + 1] - 1 belong to group
+ * g (ascending, within [0, M]; what lies outside is cut off), and the rows of out that belong
+ * to no group are left as they were.  The integer sum is exact.
+ * epilogue MOE_EPI_NONE: out [M][N] = c.  MOE_EPI_SWIGLU (N even): channels 2i and 2i + 1 are
+ * gate and up (the order of an expert blob's rows), out [M][N/2] = silu(c[2i]) * c[2i + 1].
+ * out_type bf16, fp16 or fp32.  M 0..16777216, N 1..1048576, K 1..131071 (a longer sum could
+ * leave 32 bits), groups 1..1024. */
+#define MOE_EPI_NONE 0
+#define MOE_EPI_SWIGLU 1
+moe_status moe_product_i8(const int8_t* a, int64_t a_stride, const float* a_scale, int32_t M,
+                          int32_t K, const int8_t* w, int64_t w_stride, const float* w_scale,
+                          int32_t N, int32_t groups, const int32_t* offsets, int32_t epilogue,
+                          void* out, int64_t out_stride, int32_t out_type, void* stream);
+
 const char* moe_status_string(moe_status s);
 
 /* The hipError_t of the last MOE_E_HIP returned on this handle (0 if none). */

@@ -1,0 +1,708 @@
+"""The token operators (sort by expert, back with weights, their gradients), the 8-bit
+quantisation of rows and the 8-bit product against plain implementations in 64 bits.
+
+Integers and codes are compared exactly.  Tolerances count roundings: a value rounded to type t is
+off by at most eps_t / 2 relative to it, and a sum of products held in fp32 by at most
+(additions in sequence + 1) * 2^-24 times the sum of the magnitudes."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+KINDS = ["bf16", "fp16", "fp32"]
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    import expert_cache_offload_amd as m
+    types = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32,
+             "i8": torch.int8}
+    ids = {"bf16": m.MOE_T_BF16, "fp16": m.MOE_T_FP16, "fp32": m.MOE_T_FP32, "i8": m.MOE_T_I8}
+    return torch, m, types, ids
+
+
+def _gen(torch, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _matrix(torch, g, rows, cols, dtype, pad=0, at=0):
+    """Rows of a wider buffer, starting `at` elements into it."""
+    wide = torch.randn(rows, cols + pad + at, generator=g, device="cuda")
+    wide *= torch.exp(torch.randn(rows, 1, generator=g, device="cuda"))
+    return wide.to(dtype)[:, at:at + cols]
+
+
+def _half_ulp(torch, kind):
+    return torch.finfo(kind).eps / 2
+
+
+def _quantised(torch, x):
+    x = x.double()
+    m = x.abs().amax(1, keepdim=True)
+    codes = torch.round(127 * x / torch.where(m > 0, m, 1.0))
+    scale = m / 127
+    bad = ~torch.isfinite(m)
+    return torch.where(bad, 0.0, codes).to(torch.int8), torch.where(bad, torch.nan, scale)[:, 0]
+
+
+def _sorted(torch, ids, experts):
+    """offsets, order, place of a stable sort by expert, on the host."""
+    flat = ids.reshape(-1).tolist()
+    order = [a for e in range(experts) for a in range(len(flat)) if flat[a] == e] \
+        if experts <= 8 else sorted((a for a in range(len(flat)) if 0 <= flat[a] < experts),
+                                    key=lambda a: (flat[a], a))
+    count = [0] * (experts + 1)
+    for a in order:
+        count[flat[a] + 1] += 1
+    for e in range(experts):
+        count[e + 1] += count[e]
+    place = [-1] * len(flat)
+    for p, a in enumerate(order):
+        place[a] = p
+    return count, order, place
+
+
+def _run_sort(env, ids, experts, x=None, rows_kind=None, x_kind=None, stream=0, out=None):
+    """All outputs of one sort, in buffers filled with marks beforehand."""
+    torch, m, types, tid = env
+    T, k = ids.shape
+    A = T * k
+    o = out or {}
+    if not o:
+        o["offsets"] = torch.full((experts + 1,), -7, dtype=torch.int32, device="cuda")
+        o["order"] = torch.full((A + 1,), -7, dtype=torch.int32, device="cuda")
+        o["place"] = torch.full((A + 1,), -7, dtype=torch.int32, device="cuda")
+        o["ws"] = torch.empty(max(16, m.moe_sort_workspace_bytes(T, k, experts)),
+                              dtype=torch.uint8, device="cuda")
+        if x is not None:
+            o["wide"] = torch.full((A + 1, x.shape[1] + 5), 77, dtype=types[rows_kind],
+                                   device="cuda")
+            o["rows"] = o["wide"][:, 2:2 + x.shape[1]]
+            o["scale"] = torch.full((A + 1,), 77.0, device="cuda")
+    if x is None:
+        m.moe_sort_tokens(ids, T, k, experts, o["offsets"], o["order"], o["place"],
+                          workspace=o["ws"], workspace_bytes=o["ws"].numel(), stream=stream)
+    else:
+        m.moe_sort_tokens(ids, T, k, experts, o["offsets"], o["order"], o["place"], x,
+                          x.stride(0), x.shape[1], tid[x_kind], o["rows"], o["rows"].stride(0),
+                          tid[rows_kind], o["scale"], o["ws"], o["ws"].numel(), stream)
+    return o
+
+
+def _check_sort(env, ids, experts, o, x=None, rows_kind=None):
+    torch = env[0]
+    k, A = ids.shape[1], ids.numel()
+    offsets, order, place = _sorted(torch, ids, experts)
+    n = offsets[-1]
+    assert o["offsets"].tolist() == offsets
+    assert o["place"].tolist() == place + [-7]
+    assert o["order"].tolist() == order + [-7] * (A + 1 - n)
+    if x is None:
+        return
+    token = torch.tensor(order, dtype=torch.int64, device="cuda") // k
+    wide = o["wide"].double()
+    H = x.shape[1]
+    assert bool((wide[:, :2] == 77).all()) and bool((wide[:, 2 + H:] == 77).all())
+    assert bool((wide[n:] == 77).all()) and bool((o["scale"][n:] == 77).all())
+    if rows_kind == "i8":
+        codes, scale = _quantised(torch, x)
+        assert torch.equal(o["rows"][:n], codes[token])
+        torch.testing.assert_close(o["scale"][:n].double(), scale[token], rtol=U32, atol=2e-45,
+                                   equal_nan=True)
+    else:
+        assert torch.equal(o["rows"][:n], x[token])
+
+
+def _ids(torch, g, T, k, experts, drop):
+    """k distinct experts per token, some dropped (also by ids beyond the range)."""
+    ids = torch.rand(T, experts, generator=g, device="cuda").argsort(1)[:, :k]
+    if k > experts:
+        ids = torch.randint(0, experts, (T, k), generator=g, device="cuda")
+    if drop:
+        r = torch.rand(ids.shape, generator=g, device="cuda")
+        ids = torch.where(r < drop / 2, -1, torch.where(r < drop, experts + 3, ids))
+    return ids.to(torch.int32).contiguous()
+
+
+SORTS = [  # T, k, experts, share dropped, H, padding, start
+    (1, 1, 1, 0, 1, 0, 0), (1, 8, 128, 0, 2048, 0, 0), (4, 8, 256, 0, 6144, 0, 0),
+    (3, 16, 7, 0.3, 257, 3, 1), (512, 8, 128, 0, 96, 0, 0), (513, 8, 128, 0.5, 96, 8, 0),
+    (1000, 6, 60, 0.1, 130, 1, 3), (2049, 2, 1024, 0, 40, 0, 0), (5000, 1, 3, 0.9, 64, 0, 0),
+    (300, 16, 16, 1.0, 33, 0, 0), (4100, 1, 1, 0, 17, 0, 5)]
+
+
+@pytest.mark.parametrize("T,k,experts,drop,H,pad,at", SORTS)
+@pytest.mark.parametrize("kind,rows", [("bf16", "bf16"), ("bf16", "i8"), ("fp16", "i8"),
+                                       ("fp32", "fp32"), ("fp32", "i8")])
+def test_sort(env, T, k, experts, drop, H, pad, at, kind, rows):
+    torch, m, types, tid = env
+    g = _gen(torch, T + H)
+    ids = _ids(torch, g, T, k, experts, drop)
+    x = _matrix(torch, g, T, H, types[kind], pad, at)
+    _check_sort(env, ids, experts, _run_sort(env, ids, experts, x, rows, kind), x, rows)
+
+
+def test_sort_integers_only_same_expert_twice_and_no_tokens(env):
+    torch = env[0]
+    g = _gen(torch, 3)
+    for T, k, experts in [(7, 4, 3), (2000, 5, 2), (0, 8, 128), (0, 1, 1)]:
+        ids = torch.randint(-1, experts + 1, (T, k), generator=g, device="cuda",
+                            dtype=torch.int32)
+        _check_sort(env, ids, experts, _run_sort(env, ids, experts))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_quantise_values(env, kind):
+    """Ties, zeros, tiny and huge rows, infinities and NaN, against the exact definition."""
+    torch, m, types, tid = env
+    g = _gen(torch, 5)
+    K = 300
+    x = torch.randn(64, K, generator=g, device="cuda").double()
+    x[1] = 0
+    x[2] *= 1e-30
+    x[3] = torch.arange(K, device="cuda") / 2.0 - 63.5  # code ties: with 127 the largest
+    x[3, 0] = 127
+    x[4] = torch.arange(K, device="cuda") * 0.5 - 75
+    x[5, 17] = float("inf")
+    x[6, K - 1] = float("nan")
+    x[7, 3] = -float("inf")
+    x[8] = 0
+    x[8, K - 1] = -torch.finfo(types[kind]).smallest_normal / 8  # a subnormal alone
+    x[9] = torch.finfo(types[kind]).max
+    x[10] = torch.linspace(-1, 1, K, device="cuda") * torch.finfo(types[kind]).max
+    x[11] *= 1e-6
+    x[12:40] = torch.round(x[12:40] * 16) / 16  # few distinct values: many ties
+    x = x.to(types[kind])
+    codes = torch.full((64, K), 99, dtype=torch.int8, device="cuda")
+    scale = torch.full((64,), 99.0, device="cuda")
+    m.moe_quantise_rows(x, K, tid[kind], 64, K, codes, K, scale)
+    ref, ref_scale = _quantised(torch, x)
+    assert torch.equal(codes, ref)
+    # m / 127 rounded once; below the normal range by half the smallest subnormal instead
+    torch.testing.assert_close(scale.double(), ref_scale, rtol=U32, atol=2.0 ** -150,
+                               equal_nan=True)
+
+
+@pytest.mark.parametrize("M,K,pad,at", [(1, 1, 0, 0), (8, 768, 0, 0), (1, 20001, 0, 0),
+                                        (1000, 129, 3, 1), (5, 8191, 8, 0), (70000, 72, 0, 0),
+                                        (3, 131072, 0, 0)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_quantise(env, M, K, pad, at, kind):
+    torch, m, types, tid = env
+    x = _matrix(torch, _gen(torch, M + K), M, K, types[kind], pad, at)
+    wide = torch.full((M, K + 3), 99, dtype=torch.int8, device="cuda")
+    codes = wide[:, 1:1 + K]
+    scale = torch.full((M,), 99.0, device="cuda")
+    end = torch.tensor([M - M // 3], dtype=torch.int32, device="cuda")
+    m.moe_quantise_rows(x, x.stride(0), tid[kind], M, K, codes, K + 3, scale, end)
+    n = int(end)
+    ref, ref_scale = _quantised(torch, x[:n])
+    assert torch.equal(codes[:n], ref)
+    torch.testing.assert_close(scale[:n].double(), ref_scale, rtol=U32, atol=0)
+    assert bool((wide[:, 0] == 99).all()) and bool((wide[:, K + 1:] == 99).all())
+    assert bool((wide[n:] == 99).all()) and bool((scale[n:] == 99).all())
+
+
+def _places(torch, g, T, k, drop):
+    """Distinct places of the assignments that are kept, a random order of them."""
+    keep = torch.rand(T * k, generator=g, device="cuda") >= drop
+    n = int(keep.sum())
+    place = torch.full((T * k,), -1, dtype=torch.int32, device="cuda")
+    place[keep] = torch.randperm(n, generator=g, device="cuda").to(torch.int32)
+    place[~keep] = torch.where(torch.arange(T * k, device="cuda")[~keep] % 2 == 0, -1,
+                               n + 5).to(torch.int32)
+    return place.reshape(T, k).contiguous(), n
+
+
+COMBINES = [(1, 8, 2048, 0, 0, 0), (8, 8, 2048, 0, 0, 0), (1, 1, 1, 0, 0, 0),
+            (777, 6, 1000, 0, 0, 0), (300, 16, 257, 0.3, 3, 1), (100, 3, 63, 1.0, 0, 0),
+            (2, 5, 20001, 0.2, 1, 0), (3000, 2, 40, 0.5, 8, 0), (64, 8, 6144, 0.1, 0, 0)]
+
+
+def _wide_out(torch, rows, cols, kind):
+    wide = torch.full((rows, cols + 4), 77.0, dtype=kind, device="cuda")
+    return wide, wide[:, 1:1 + cols]
+
+
+@pytest.mark.parametrize("T,k,H,drop,pad,at", COMBINES)
+@pytest.mark.parametrize("kind", KINDS)
+def test_combine_and_sort_grad(env, T, k, H, drop, pad, at, kind):
+    torch, m, types, tid = env
+    g = _gen(torch, T + H)
+    place, n = _places(torch, g, T, k, drop)
+    rows = _matrix(torch, g, n, H, types[kind], pad, at)
+    w = torch.rand(T, k, generator=g, device="cuda") * 2 - 0.5
+    kept = (place >= 0) & (place < n)
+    w_in = torch.where(kept, w, torch.nan)  # whatever a dropped choice's weight holds
+    u = _half_ulp(torch, types[kind])
+    r = rows.double()[torch.where(kept, place, 0).reshape(-1)].reshape(T, k, H) if n else \
+        torch.zeros(T, k, H, dtype=torch.float64, device="cuda")
+    for weights in (w_in, None):
+        f = torch.where(kept, 1.0 if weights is None else w.double(), 0.0)[:, :, None]
+        ref, mag = (r * f).sum(1), (r * f).abs().sum(1)
+        wide, out = _wide_out(torch, T, H, types[kind])
+        args = (rows if n else None, rows.stride(0) if n else H, n, tid[kind], place)
+        if weights is None:
+            m.moe_sort_tokens_grad(*args, T, k, H, out, H + 4)
+        else:
+            m.moe_combine_tokens(*args, weights, T, k, H, out, H + 4)
+        # k additions in sequence and their products, then the output's own rounding (in the
+        # range below fp16's normal numbers half its spacing there)
+        tol = ((k + 1) * U32 * mag) * (1 + u) + u * ref.abs() + (2.0 ** -25 if kind == "fp16"
+                                                               else 0)
+        assert bool(((out.double() - ref).abs() <= tol).all())
+        assert bool((wide[:, 0] == 77).all()) and bool((wide[:, 1 + H:] == 77).all())
+
+
+@pytest.mark.parametrize("T,k,H,drop,pad,at", COMBINES)
+@pytest.mark.parametrize("kind", KINDS)
+def test_combine_grad(env, T, k, H, drop, pad, at, kind):
+    torch, m, types, tid = env
+    g = _gen(torch, T + H + 1)
+    place, n = _places(torch, g, T, k, drop)
+    rows = _matrix(torch, g, n, H, types[kind], pad, at)
+    dout = _matrix(torch, g, T, H, types[kind], pad, at)
+    w = torch.rand(T, k, generator=g, device="cuda") * 2 - 0.5
+    kept = (place >= 0) & (place < n)
+    w_in = torch.where(kept, w, torch.nan)
+    u = _half_ulp(torch, types[kind])
+    for which in ("both", "drows", "dweights"):
+        wide, drows = _wide_out(torch, n + 1, H, types[kind])
+        dw = torch.full((T, k), 77.0, device="cuda")
+        need_rows = which != "drows" and n > 0
+        m.moe_combine_tokens_grad(
+            dout, dout.stride(0), rows if need_rows else None, rows.stride(0) if n else H, n,
+            tid[kind], place, w_in, T, k, H, None if which == "dweights" else drows, H + 4,
+            None if which == "drows" else dw)
+        if which != "dweights":
+            ref = torch.zeros(n, H, dtype=torch.float64, device="cuda")
+            t, j = torch.nonzero(kept, as_tuple=True)
+            ref[place[t, j].long()] = dout.double()[t] * w.double()[t, j][:, None]
+            tol = (u + 2 * U32) * ref.abs() + (2.0 ** -25 if kind == "fp16" else 0)
+            assert bool(((drows[:n].double() - ref).abs() <= tol).all())
+            assert bool((wide[n] == 77).all()) and bool((wide[:, 0] == 77).all())
+            assert bool((wide[:, 1 + H:] == 77).all())
+        else:
+            assert bool((wide == 77).all())
+        if which != "drows":
+            ref = torch.zeros(T, k, dtype=torch.float64, device="cuda")
+            mag = torch.zeros_like(ref)
+            t, j = torch.nonzero(kept, as_tuple=True)
+            prod = dout.double()[t] * rows.double()[place[t, j].long()]
+            ref[t, j], mag[t, j] = prod.sum(1), prod.abs().sum(1)
+            # a lane adds up every 64th chunk of 16 bytes, then six joins of lanes, then of waves
+            tol = (H // 64 + 32) * U32 * mag
+            assert bool(((dw.double() - ref).abs() <= tol).all())
+        else:
+            assert bool((dw == 77).all())
+
+
+def test_gradients_against_differences(env):
+    """The gradients of L = <dout, combine(rows, w)> and of <drows, sort(x)> against central
+    differences of the forward kernels; both are linear in each argument, so the difference is
+    exact but for the roundings of the two forward passes."""
+    torch, m, types, tid = env
+    g = _gen(torch, 11)
+    T, k, H, experts = 37, 4, 129, 8
+    ids = _ids(torch, g, T, k, experts, 0.2)
+    x = torch.randn(T, H, generator=g, device="cuda")
+    o = _run_sort(env, ids, experts, x, "fp32", "fp32")
+    n = int(o["offsets"][-1])
+    place = o["place"][:-1].reshape(T, k)
+    rows = torch.randn(n, H, generator=g, device="cuda")
+    w = torch.rand(T, k, generator=g, device="cuda")
+    dout = torch.randn(T, H, generator=g, device="cuda")
+
+    def forward(r, v):
+        out = torch.zeros(T, H, device="cuda")
+        m.moe_combine_tokens(r, H, n, tid["fp32"], place, v, T, k, H, out, H)
+        return out.double()
+
+    drows = torch.zeros(n, H, device="cuda")
+    dw = torch.zeros(T, k, device="cuda")
+    m.moe_combine_tokens_grad(dout, H, rows, H, n, tid["fp32"], place, w, T, k, H, drows, H, dw)
+    d_rows, d_w = torch.randn_like(rows), torch.randn_like(w)
+    mag = float((dout.double().abs() * forward(rows.abs() + d_rows.abs(),
+                                               w.abs() + d_w.abs())).sum())
+    for got, plus, minus in [
+            ((drows.double() * d_rows.double()).sum(), (rows + d_rows, w), (rows - d_rows, w)),
+            ((dw.double() * d_w.double()).sum(), (rows, w + d_w), (rows, w - d_w))]:
+        diff = (dout.double() * (forward(*plus) - forward(*minus))).sum() / 2
+        # k + 2 roundings per forward element (arguments included), H / 64 + 32 in dw
+        assert abs(float(got - diff)) <= (k + 2 + H // 64 + 32) * U32 * mag
+    dx = torch.zeros(T, H, device="cuda")
+    m.moe_sort_tokens_grad(rows, H, n, tid["fp32"], place, T, k, H, dx, H)
+    d_x = torch.randn_like(x)
+    moved = _run_sort(env, ids, experts, d_x, "fp32", "fp32")["rows"][:n]
+    lhs, rhs = (dx.double() * d_x.double()).sum(), (rows.double() * moved.double()).sum()
+    mag = float((rows.abs() * moved.abs()).double().sum())
+    assert abs(float(lhs - rhs)) <= (k + 1) * U32 * mag
+
+
+# ------------------------------------------------------------------ 8-bit product
+
+
+def _codes(torch, g, rows, cols, pad=0, at=0, low=-128):
+    wide = torch.randint(low, 128, (rows, cols + pad + at), generator=g, device="cuda",
+                         dtype=torch.int8)
+    return wide[:, at:at + cols]
+
+
+def _product_ref(torch, a, a_scale, w, w_scale, N, offsets, swiglu):
+    """Values and their error bounds relative to 2^-24, rows of no group as NaN."""
+    M = a.shape[0]
+    n_out = N // 2 if swiglu else N
+    ref = torch.full((M, n_out), torch.nan, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(ref)
+    ends = [0, M] if offsets is None else [min(max(v, 0), M) for v in offsets.tolist()]
+    for g, (lo, hi) in enumerate(zip(ends, ends[1:])):
+        if lo >= hi:
+            continue
+        c = a[lo:hi].double() @ w[g * N:(g + 1) * N].double().t()
+        c = c * a_scale[lo:hi, None].double() * w_scale[g * N:(g + 1) * N].double()
+        if swiglu:
+            gate, up = c[:, 0::2], c[:, 1::2]
+            ref[lo:hi] = gate * torch.sigmoid(gate) * up
+            # gate and up: the sum's conversion and two scales (3 roundings each), an error of
+            # the gate acts on silu 1 + |gate| times at most; exp, 1 + exp, reciprocal (1 ulp
+            # each, the exponent's own remainder) and three products
+            tol[lo:hi] = ref[lo:hi].abs() * (16 + 3 * gate.abs()) + 1e-30 * up.abs()
+        else:
+            ref[lo:hi] = c
+            tol[lo:hi] = 3 * c.abs()
+    return ref, tol * U32
+
+
+def _run_product(env, a, a_scale, w, w_scale, N, groups, offsets, swiglu, kind, stream=0):
+    torch, m, types, tid = env
+    M, K = a.shape
+    n_out = N // 2 if swiglu else N
+    wide, out = _wide_out(torch, M, n_out, types[kind])
+    m.moe_product_i8(a, a.stride(0), a_scale, M, K, w, w.stride(0), w_scale, N, groups, offsets,
+                     int(swiglu), out, n_out + 4, tid[kind], stream)
+    return wide, out
+
+
+def _check_product(env, a, a_scale, w, w_scale, N, groups, offsets, swiglu, kind):
+    torch, m, types, tid = env
+    wide, out = _run_product(env, a, a_scale, w, w_scale, N, groups, offsets, swiglu, kind)
+    ref, tol = _product_ref(torch, a, a_scale, w, w_scale, N, offsets, swiglu)
+    u = _half_ulp(torch, types[kind])
+    left = torch.isnan(ref)
+    assert bool((out[left] == 77).all())
+    tol = tol * (1 + u) + u * ref.abs() + (2.0 ** -25 if kind == "fp16" else 0)
+    err = (out.double() - ref).abs()
+    assert bool((err[~left] <= tol[~left]).all()), float((err / tol)[~left].max())
+    assert bool((wide[:, 0] == 77).all()) and bool((wide[:, 1 + out.shape[1]:] == 77).all())
+
+
+def _scales(torch, g, M, C):
+    """Scales that keep sums of the largest codes within fp16."""
+    return (torch.rand(M, generator=g, device="cuda") * 2e-3 + 1e-4,
+            torch.rand(C, generator=g, device="cuda") * 2e-3 + 1e-4)
+
+
+DENSE = [(1, 1, 1, 0, 0), (1, 64, 2048, 0, 0), (7, 130, 96, 0, 0), (16, 1536, 768, 0, 0),
+         (17, 34, 4096, 0, 0), (128, 128, 64, 0, 0), (129, 258, 200, 3, 1), (33, 500, 31, 0, 0),
+         (300, 1000, 1024, 16, 0), (513, 768, 1040, 0, 0), (64, 66, 70000, 0, 0),
+         (1000, 514, 513, 0, 3), (257, 255, 272, 0, 16)]
+
+
+@pytest.mark.parametrize("M,N,K,pad,at", DENSE)
+@pytest.mark.parametrize("kind,swiglu", [("bf16", False), ("bf16", True), ("fp16", False),
+                                         ("fp32", False), ("fp32", True)])
+def test_product_one_weight(env, M, N, K, pad, at, kind, swiglu):
+    torch = env[0]
+    if swiglu and N % 2:
+        N += 1
+    g = _gen(torch, M + N + K)
+    a, w = _codes(torch, g, M, K, pad, at), _codes(torch, g, N, K, pad, at)
+    a_scale, w_scale = _scales(torch, g, M, N)
+    _check_product(env, a, a_scale, w, w_scale, N, 1, None, swiglu, kind)
+
+
+def _offsets(torch, counts, first=0):
+    v = [first]
+    for c in counts:
+        v.append(v[-1] + c)
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+GROUPS = {  # rows of each group; rows before the first and after the last
+    "one_row_each": ([1] * 8, 0, 0), "few": ([0, 3, 0, 1, 16, 17, 0], 0, 5),
+    "ragged": ([130, 0, 1, 257, 64, 5], 2, 3), "empty": ([0, 0, 0], 0, 9),
+    "one_full": ([0, 700, 0, 0], 0, 0), "many": ([i % 5 for i in range(256)], 0, 1),
+    "most": ([1] + [0] * 1022 + [2], 0, 0)}
+
+
+@pytest.mark.parametrize("name", GROUPS)
+@pytest.mark.parametrize("N,K,pad", [(96, 256, 0), (130, 72, 0), (34, 1029, 3)])
+@pytest.mark.parametrize("kind,swiglu", [("bf16", True), ("fp32", False)])
+def test_product_by_group(env, name, N, K, pad, kind, swiglu):
+    torch = env[0]
+    counts, before, behind = GROUPS[name]
+    G, M = len(counts), before + sum(counts) + behind
+    g = _gen(torch, M + N)
+    a, w = _codes(torch, g, M, K, pad), _codes(torch, g, G * N, K, pad)
+    a_scale, w_scale = _scales(torch, g, M, G * N)
+    _check_product(env, a, a_scale, w, w_scale, N, G, _offsets(torch, counts, before), swiglu,
+                   kind)
+
+
+def test_product_extremes(env):
+    """The longest sum of the largest codes, scales that are zero, infinite or NaN, and offsets
+    that leave the rows."""
+    torch, m, types, tid = env
+    K = 131071
+    a = torch.full((5, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((40, K), -128, dtype=torch.int8, device="cuda")
+    w[1] = 127
+    one = torch.ones(40, device="cuda")
+    _, out = _run_product(env, a, one[:5].clone(), w, one, 40, 1, None, False, "fp32")
+    assert bool((out[:, 0].double() == float(128 * 128 * K)).all())  # 2^14 times 17 bits: exact
+    assert bool((out[:, 1].double() + 128 * 127 * K).abs().max() <= 128 * 127 * K * U32)
+    a, w = _codes(torch, _gen(torch, 2), 4, 64), _codes(torch, _gen(torch, 3), 20, 64)
+    sa = torch.tensor([0.0, float("nan"), float("inf"), 1e-3], device="cuda")
+    for kind in KINDS:
+        _, out = _run_product(env, a, sa, w, torch.full((20,), 1e-3, device="cuda"), 20, 1, None,
+                              False, kind)
+        assert bool((out[0] == 0).all()) and bool(out[1].isnan().all())
+        assert bool((~out[2].isfinite()).all()) and bool(out[3].isfinite().all())
+    # offsets beyond the rows are cut off, descending ones are empty groups
+    a, w = _codes(torch, _gen(torch, 4), 50, 64), _codes(torch, _gen(torch, 5), 3 * 20, 64)
+    sa, sw = _scales(torch, _gen(torch, 6), 50, 60)
+    off = torch.tensor([-4, 30, 20, 90], dtype=torch.int32, device="cuda")
+    _, out = _run_product(env, a, sa, w, sw, 20, 3, off, False, "fp32")
+    ref = torch.empty(50, 20, dtype=torch.float64, device="cuda")
+    for g, lo, hi in ((0, 0, 20), (2, 20, 50)):
+        s = slice(g * 20, g * 20 + 20)
+        ref[lo:hi] = (a[lo:hi].double() @ w[s].double().t()) * sa[lo:hi, None] * sw[s]
+    ref0 = (a[20:30].double() @ w[:20].double().t()) * sa[20:30, None] * sw[:20]
+    err = (out.double() - ref).abs() <= 3 * U32 * ref.abs()
+    err[20:30] |= (out[20:30].double() - ref0).abs() <= 3 * U32 * ref0.abs()  # groups 0 and 2
+    assert bool(err.all())
+
+
+def test_offsets_beyond_32_bits(env):
+    """Rows more than 2^31 elements apart in every operand that can be that large."""
+    torch, m, types, tid = env
+    g = _gen(torch, 9)
+    wide = 1 << 20
+    T, k, experts, H = 2100, 1, 4, 24
+    ids = _ids(torch, g, T, k, experts, 0)
+    x = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")[:, :H]
+    x.copy_(torch.randn(T, H, generator=g, device="cuda"))
+    rows = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")[:, :H]
+    ints = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (experts + 1, T, T)]
+    ws = torch.empty(max(16, m.moe_sort_workspace_bytes(T, k, experts)), dtype=torch.uint8,
+                     device="cuda")
+    m.moe_sort_tokens(ids, T, k, experts, *ints, x, wide, H, 0, rows, wide, 0, None, ws,
+                      ws.numel())
+    _, order, _ = _sorted(torch, ids, experts)
+    assert torch.equal(rows, x[torch.tensor(order, device="cuda")])
+    place = ints[2].reshape(T, 1)
+    one = torch.ones(T, 1, device="cuda")
+    back = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")[:, :H]
+    m.moe_combine_tokens(rows, wide, T, 0, place, one, T, k, H, back, wide)
+    assert torch.equal(back, x)
+    dw = torch.empty(T, 1, device="cuda")
+    m.moe_combine_tokens_grad(x, wide, rows, wide, T, 0, place, one, T, k, H, back, wide, dw)
+    assert torch.equal(back, rows)
+    ref = (x.double() ** 2).sum(1, keepdim=True)
+    assert bool(((dw.double() - ref).abs() <= 32 * U32 * ref).all())
+    codes = torch.empty(T, wide, dtype=torch.int8, device="cuda")[:, :H]
+    scale = torch.empty(T, device="cuda")
+    m.moe_quantise_rows(x, wide, 0, T, H, codes, wide, scale)
+    assert torch.equal(codes, _quantised(torch, x)[0])
+    del rows, back
+    # the product: 2100 channels 2^20 bytes apart, twice, and rows as far apart
+    G, N = 2, T // 2
+    sw = torch.rand(T, generator=g, device="cuda")
+    off = _offsets(torch, [1000, 1100])
+    out = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")[:, :N]
+    m.moe_product_i8(codes, wide, scale, T, H, codes, wide, sw, N, G, off, 0, out, wide, 0)
+    ref, tol = _product_ref(torch, codes, scale, codes, sw, N, off, False)
+    assert bool(((out.double() - ref).abs() <= tol * 2 + 2.0 ** -8 * ref.abs()).all())
+
+
+# ------------------------------------------------------------------ together
+
+
+def _expert_layer(env, b, stream=0):
+    """An 8-bit expert layer as a program runs it, into the buffers of b."""
+    torch, m, types, tid = env
+    T, k, E, H, I = b["T"], b["k"], b["E"], b["H"], b["I"]
+    A = T * k
+    end = b["offsets"][E:]
+    m.moe_sort_tokens(b["ids"], T, k, E, b["offsets"], None, b["place"], b["x"], H, H, 0,
+                      b["xq"], H, 3, b["xs"], b["ws"], b["ws"].numel(), stream)
+    m.moe_product_i8(b["xq"], H, b["xs"], A, H, b["wgu"], H, b["sgu"], 2 * I, E, b["offsets"], 1,
+                     b["act"], I, 0, stream)
+    m.moe_quantise_rows(b["act"], I, 0, A, I, b["aq"], I, b["as"], end, stream)
+    m.moe_product_i8(b["aq"], I, b["as"], A, I, b["wd"], I, b["sd"], H, E, b["offsets"], 0,
+                     b["y_rows"], H, 0, stream)
+    m.moe_combine_tokens(b["y_rows"], H, A, 0, b["place"], b["weights"], T, k, H, b["y"], H,
+                         stream)
+
+
+def _layer_buffers(env, T, k, E, H, I, wgu, wd):
+    """wgu [E][2I][H], wd [E][H][I] in float64: quantised per channel, with room for a call."""
+    torch, m, types, tid = env
+    dev = dict(device="cuda")
+    b = dict(T=T, k=k, E=E, H=H, I=I)
+    b["wgu"], b["sgu"] = _quantised(torch, wgu.reshape(-1, H))
+    b["wd"], b["sd"] = _quantised(torch, wd.reshape(-1, I))
+    b["sgu"], b["sd"] = b["sgu"].float(), b["sd"].float()
+    A = T * k
+    b["offsets"] = torch.zeros(E + 1, dtype=torch.int32, **dev)
+    b["place"] = torch.zeros(T, k, dtype=torch.int32, **dev)
+    b["xq"], b["xs"] = torch.zeros(A, H, dtype=torch.int8, **dev), torch.zeros(A, **dev)
+    b["act"] = torch.zeros(A, I, dtype=torch.bfloat16, **dev)
+    b["aq"], b["as"] = torch.zeros(A, I, dtype=torch.int8, **dev), torch.zeros(A, **dev)
+    b["y_rows"] = torch.zeros(A, H, dtype=torch.bfloat16, **dev)
+    b["y"] = torch.zeros(T, H, dtype=torch.bfloat16, **dev)
+    b["ws"] = torch.empty(max(16, m.moe_sort_workspace_bytes(T, k, E)), dtype=torch.uint8, **dev)
+    return b
+
+
+def _layer_ref(torch, x, ids, weights, wgu, wd):
+    """The expert layer in 64 bits without any quantisation."""
+    y = torch.zeros(x.shape, dtype=torch.float64, device="cuda")
+    for e in range(wgu.shape[0]):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        if len(t):
+            c = x[t].double() @ wgu[e].t()
+            h = c[:, 0::2] * torch.sigmoid(c[:, 0::2]) * c[:, 1::2]
+            y.index_add_(0, t, weights[t, j].double()[:, None] * (h @ wd[e].t()))
+    return y
+
+
+# Each of the four quantised factors of a token's output (x, gate/up weights, activations, down
+# weights) is off by at most half a step, m / 254, uniformly: m / (127 sqrt 12) rms, and with m
+# at most 6 times the rms of normal values 1.4% of it.  Gate and up both carry the first two;
+# silu at most doubles the gate's: sqrt(2) * 1.4% * sqrt(1 + 4) + sqrt(2) * 1.4% < 7%.
+LAYER_TOL = 7e-2
+
+
+def _rel(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+def test_expert_layer_beside_the_handle(env):
+    """The route of a layer step of the handle, its experts in 8-bit integers through the
+    operators: the result is the layer's own, within the quantisation's error."""
+    import dataclasses
+    import numpy as np
+    import moe_inputs as mi
+    from expert_cache_offload_amd.runner import Workbench
+    torch, m, types, tid = env
+    wl = dataclasses.replace(mi.WORKLOADS["tiny"].with_tokens(8).with_steps(3), fixed_capacity=16)
+    E, H, I, k = wl.experts, wl.hidden, wl.inter, wl.top_k
+    with Workbench(wl) as wb:
+        bits = wb.pool.view(np.uint16)[:E * 3 * I * H]
+        blobs = torch.from_numpy((bits.astype(np.uint32) << 16).view(np.float32)).cuda().double()
+        blobs = blobs.reshape(E, 3 * I * H)
+        wgu = blobs[:, :2 * I * H].reshape(E, 2 * I, H)
+        wd = blobs[:, 2 * I * H:].reshape(E, I, H).transpose(1, 2).contiguous()
+        b = _layer_buffers(env, wb.T, k, E, H, I, wgu, wd)
+        for t in range(wl.token_steps):
+            wb.step(t, 0)
+            wb.sync()
+            b["ids"], b["weights"] = wb.topk_idx[0], wb.topk_w[0]
+            b["x"] = wb.acts[t, 0].view(torch.bfloat16).reshape(wb.T, H)
+            _expert_layer(env, b)
+            ref = _layer_ref(torch, b["x"], b["ids"], b["weights"], wgu, wd)
+            assert _rel(b["y"], ref) <= LAYER_TOL
+            step = torch.from_numpy(wb.y_f64(0).reshape(wb.T, H)).cuda()
+            assert _rel(b["y"], step) <= LAYER_TOL
+
+
+def test_expert_layer_captured_and_on_another_stream(env):
+    """The layer of 700 tokens (sort over a workspace) captured once and replayed with new inputs,
+    eager work and synchronisation between the replays; and eagerly on a side stream."""
+    torch, m, types, tid = env
+    T, k, E, H, I = 700, 6, 12, 256, 128
+    g = _gen(torch, 21)
+    wgu = torch.randn(E, 2 * I, H, generator=g, device="cuda").double() * 0.06
+    wd = torch.randn(E, H, I, generator=g, device="cuda").double() * 0.06
+    b = _layer_buffers(env, T, k, E, H, I, wgu, wd)
+    eager = _layer_buffers(env, T, k, E, H, I, wgu, wd)
+    assert m.moe_sort_workspace_bytes(T, k, E) > 0
+    b["ids"] = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    b["weights"] = torch.zeros(T, k, device="cuda")
+    b["x"] = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        _expert_layer(env, b, side.cuda_stream)
+    torch.cuda.synchronize()
+    for r in range(4):
+        eager["ids"] = _ids(torch, g, T, k, E, 0.1 * r)
+        eager["weights"] = torch.softmax(torch.randn(T, k, generator=g, device="cuda"), 1)
+        eager["x"] = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+        for n in ("ids", "weights", "x"):
+            b[n].copy_(eager[n])
+        torch.cuda.synchronize()
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        if r % 2:
+            _expert_layer(env, eager, side.cuda_stream)
+        else:
+            _expert_layer(env, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(b["y"], eager["y"]), r
+        ref = _layer_ref(torch, eager["x"], eager["ids"], eager["weights"], wgu, wd)
+        assert _rel(b["y"], ref) <= LAYER_TOL
+
+
+def test_training_step_captured_beside_live_gradients(env):
+    """Sort, a scaling per expert in torch, combine and every gradient, captured and replayed
+    while an eager autograd graph over the same leaves is alive; gradients against autograd's of
+    the plain form in 64 bits."""
+    torch, m, types, tid = env
+    T, k, E, H = 90, 3, 5, 72
+    g = _gen(torch, 31)
+    ids = _ids(torch, g, T, k, E, 0.2)
+    x = torch.randn(T, H, generator=g, device="cuda").requires_grad_()
+    w = torch.rand(T, k, generator=g, device="cuda").requires_grad_()
+    dout = torch.randn(T, H, generator=g, device="cuda")
+    o = _run_sort(env, ids, E, x.detach(), "fp32", "fp32")
+    place = o["place"][:-1].reshape(T, k)
+    n = int(o["offsets"][-1])
+    kept = ids.long().clamp(0, E - 1) == ids
+    live = (torch.where(kept, w, 0.0).double()[:, :, None] * (2 * x.double())[:, None]).sum(1)
+    rows, out, dx = (torch.zeros(s, H, device="cuda") for s in (T * k, T, T))
+    y_rows, drows = torch.zeros(T * k, H, device="cuda"), torch.zeros(T * k, H, device="cuda")
+    dw = torch.zeros(T, k, device="cuda")
+    xd, wd = x.detach(), w.detach()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        s = side.cuda_stream
+        m.moe_sort_tokens(ids, T, k, E, o["offsets"], None, place, xd, H, H, 2, rows, H, 2, None,
+                          o["ws"], o["ws"].numel(), s)
+        torch.mul(rows, 2, out=y_rows)
+        m.moe_combine_tokens(y_rows, H, n, 2, place, wd, T, k, H, out, H, s)
+        m.moe_combine_tokens_grad(dout, H, y_rows, H, n, 2, place, wd, T, k, H, drows, H, dw, s)
+        drows.mul_(2)
+        m.moe_sort_tokens_grad(drows, H, n, 2, place, T, k, H, dx, H, s)
+    torch.cuda.synchronize()
+    live.backward(dout.double())
+    for _ in range(3):
+        for t in (rows, y_rows, drows, out, dx, dw):
+            t.fill_(5)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        tol = (k + 3) * U32 * (k * 2 * w.abs().max() * dout.abs()).double() + 1e-12
+        assert bool(((dx.double() - x.grad.double()).abs() <= tol).all())
+        mag = (dout.double().abs() * 2 * x.detach().double().abs()).sum(1, keepdim=True)
+        assert bool(((dw.double() - w.grad.double()).abs() <= (H // 64 + 34) * U32 * mag).all())
+        ref = live.detach()
+        tol = (k + 3) * U32 * (k * 2 * w.abs().max() * x.detach().abs()).double() + 1e-12
+        assert bool(((out.double() - ref).abs() <= tol).all())

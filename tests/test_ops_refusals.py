@@ -1,0 +1,115 @@
+"""Calls that the token and 8-bit operators refuse, on the host, before any GPU work (no GPU needed:
+the addresses are never dereferenced), and calls of no rows, which return without a launch."""
+import pytest
+
+BF16, FP16, FP32, I8 = 0, 1, 2, 3
+P = 1 << 20  # an address
+
+
+def _m():
+    import expert_cache_offload_amd as m
+    return m
+
+
+def _refused(name, status, **kw):
+    m = _m()
+    with pytest.raises(m.MoeError) as e:
+        getattr(m, name)(**kw)
+    assert e.value.status == status, (name, kw, e.value)
+
+
+SORT = dict(topk_idx=P, T=16, top_k=2, experts=8, offsets=P, order=P, place=P, x=P, x_stride=64,
+            hidden=64, x_type=BF16, rows=P, rows_stride=64, rows_type=BF16, row_scale=None,
+            workspace=None, workspace_bytes=0, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(T=-1), dict(T=(1 << 20) + 1), dict(top_k=0), dict(top_k=17), dict(experts=0),
+    dict(experts=1025), dict(topk_idx=None), dict(offsets=None), dict(place=None),
+    dict(topk_idx=P + 2), dict(offsets=P + 1), dict(place=P + 2), dict(order=P + 2),
+    dict(x=None), dict(rows=None), dict(hidden=0), dict(hidden=(1 << 20) + 1),
+    dict(x_stride=63), dict(rows_stride=63), dict(x_type=I8, rows_type=I8), dict(x_type=4),
+    dict(rows_type=FP16), dict(rows_type=I8), dict(x=P + 1), dict(rows=P + 1),
+    dict(rows_type=I8, row_scale=P + 2), dict(x_stride=(1 << 40) + 1)])
+def test_sort_refuses(bad):
+    _refused("moe_sort_tokens", _m().MOE_E_INVALID, **{**SORT, **bad})
+
+
+def test_sort_workspace():
+    m = _m()
+    assert m.moe_sort_workspace_bytes(1, 8, 128) == 0
+    need = m.moe_sort_workspace_bytes(16384, 8, 128)
+    assert need > 0
+    assert m.moe_sort_workspace_bytes(-1, 8, 128) == 0
+    assert m.moe_sort_workspace_bytes(16384, 17, 128) == 0
+    big = {**SORT, "T": 16384, "top_k": 8, "experts": 128}
+    _refused("moe_sort_tokens", m.MOE_E_SCRATCH,
+             **{**big, "workspace": P, "workspace_bytes": need - 1})
+    _refused("moe_sort_tokens", m.MOE_E_INVALID, **{**big, "workspace_bytes": need})
+    _refused("moe_sort_tokens", m.MOE_E_INVALID,
+             **{**big, "workspace": P + 2, "workspace_bytes": need})
+
+
+COMBINE = dict(rows=P, rows_stride=64, n_rows=32, type=BF16, place=P, weights=P, T=16, top_k=2,
+               hidden=64, out=P, out_stride=64, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=None), dict(rows_stride=63), dict(n_rows=-1), dict(type=I8), dict(type=-1),
+    dict(place=None), dict(place=P + 2), dict(weights=None), dict(weights=P + 2), dict(T=-1),
+    dict(T=(1 << 20) + 1), dict(top_k=0), dict(top_k=17), dict(hidden=0), dict(out=None),
+    dict(out_stride=63), dict(out=P + 1), dict(rows=P + 1)])
+def test_combine_refuses(bad):
+    _refused("moe_combine_tokens", _m().MOE_E_INVALID, **{**COMBINE, **bad})
+
+
+@pytest.mark.parametrize("bad", [
+    dict(drows=None), dict(drows_stride=63), dict(n_rows=-1), dict(type=I8), dict(place=None),
+    dict(T=-1), dict(top_k=0), dict(hidden=0), dict(dx=None), dict(dx_stride=63)])
+def test_sort_grad_refuses(bad):
+    good = dict(drows=P, drows_stride=64, n_rows=32, type=FP16, place=P, T=16, top_k=2,
+                hidden=64, dx=P, dx_stride=64, stream=0)
+    _refused("moe_sort_tokens_grad", _m().MOE_E_INVALID, **{**good, **bad})
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dout=None), dict(dout_stride=63), dict(rows=None), dict(rows_stride=63),
+    dict(n_rows=-1), dict(type=I8), dict(place=None), dict(weights=None), dict(T=-1),
+    dict(top_k=17), dict(hidden=0), dict(drows_stride=63), dict(drows=P + 2),
+    dict(dweights=P + 2), dict(drows=None, dweights=None)])
+def test_combine_grad_refuses(bad):
+    good = dict(dout=P, dout_stride=64, rows=P, rows_stride=64, n_rows=32, type=FP32, place=P,
+                weights=P, T=16, top_k=2, hidden=64, drows=P, drows_stride=64, dweights=P,
+                stream=0)
+    _refused("moe_combine_tokens_grad", _m().MOE_E_INVALID, **{**good, **bad})
+
+
+@pytest.mark.parametrize("bad", [
+    dict(x=None), dict(x_stride=63), dict(type=I8), dict(M=-1), dict(K=0), dict(K=(1 << 20) + 1),
+    dict(codes=None), dict(codes_stride=63), dict(scale=None), dict(scale=P + 2),
+    dict(rows_end=P + 1), dict(x=P + 1)])
+def test_quantise_refuses(bad):
+    good = dict(x=P, x_stride=64, type=BF16, M=16, K=64, codes=P, codes_stride=64, scale=P,
+                rows_end=None, stream=0)
+    _refused("moe_quantise_rows", _m().MOE_E_INVALID, **{**good, **bad})
+
+
+PRODUCT = dict(a=P, a_stride=64, a_scale=P, M=16, K=64, w=P, w_stride=64, w_scale=P, N=32,
+               groups=4, offsets=P, epilogue=0, out=P, out_stride=32, out_type=BF16, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(a=None), dict(a_stride=63), dict(a_scale=None), dict(a_scale=P + 2), dict(M=-1),
+    dict(M=(1 << 24) + 1), dict(K=0), dict(K=131072, a_stride=131072, w_stride=131072),
+    dict(w=None), dict(w_stride=63), dict(w_scale=None), dict(w_scale=P + 2), dict(N=0),
+    dict(N=(1 << 20) + 1), dict(groups=0), dict(groups=1025), dict(offsets=None),
+    dict(offsets=P + 2), dict(epilogue=2), dict(epilogue=-1), dict(epilogue=1, N=31),
+    dict(out=None), dict(out_stride=31), dict(out_type=I8), dict(out_type=-1), dict(out=P + 1)])
+def test_product_refuses(bad):
+    _refused("moe_product_i8", _m().MOE_E_INVALID, **{**PRODUCT, **bad})
+
+
+def test_no_rows_is_no_work():
+    m = _m()
+    m.moe_combine_tokens(**{**COMBINE, "T": 0})
+    m.moe_product_i8(**{**PRODUCT, "M": 0})
