@@ -10,6 +10,7 @@
 // instruction's in the order below, 16 neighbouring channels of it: gate and up meet in a lane
 // and the output is stored in 16-byte pieces.
 #include <algorithm>
+#include <cmath>
 
 #include "row_ops.h"
 
@@ -48,8 +49,12 @@ __device__ __forceinline__ float exp_neg(float z) {
   // |t| beyond exp2's range: e is 0 or infinity already, and the term must not make it a NaN
   return fabsf(t) < 126.f ? fmaf(e, rest * 0.693147181f, e) : e;
 }
-__device__ __forceinline__ float silu_f32(float z) {
-  return z * __builtin_amdgcn_rcpf(1.0f + exp_neg(z));
+// silu(z) for an output of type E.  For 16-bit outputs exp2 of the rounded exponent is enough: its
+// error, below 2^-17 where the result is not negligible, is far inside half a step (2^-12).
+template <class E>
+__device__ __forceinline__ float silu_for(float z) {
+  const float e = sizeof(E) == 2 ? __builtin_amdgcn_exp2f(-1.44269504f * z) : exp_neg(z);
+  return z * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // Channel (row of a 32-row weight tile) that row r of the matrix instruction holds: a lane's 16
@@ -69,15 +74,18 @@ __device__ __forceinline__ int2 group_rows(const ProdArgs& a, int g) {
   return make_int2(lo, min(max(a.offsets[g + 1], lo), a.M));
 }
 
-// s_mt[g] = first row tile (of BM rows) of group g, s_mt[groups] = their number.
+// s_mt[g] = first row tile (of BM rows) of group g, s_mt[groups] = their number; s_rows[g] = the
+// group's rows.
 template <int BM>
-__device__ void tile_prefix(const ProdArgs& a, int* s_mt, int* s_wave, int tid, int nthr) {
+__device__ void tile_prefix(const ProdArgs& a, int* s_mt, int2* s_rows, int* s_wave, int tid,
+                            int nthr) {
   const int per = (a.groups + nthr - 1) / nthr;
   int sum = 0;
   for (int i = 0; i < per; ++i) {
     const int g = tid * per + i;
     if (g < a.groups) {
       const int2 r = group_rows(a, g);
+      s_rows[g] = r;
       sum += (r.y - r.x + BM - 1) / BM;
     }
   }
@@ -95,7 +103,7 @@ __device__ void tile_prefix(const ProdArgs& a, int* s_mt, int* s_wave, int tid, 
     const int g = tid * per + i;
     if (g < a.groups) {
       s_mt[g] = first;
-      const int2 r = group_rows(a, g);
+      const int2 r = s_rows[g];  // this thread's own
       first += (r.y - r.x + BM - 1) / BM;
       if (g == a.groups - 1) s_mt[a.groups] = first;
     }
@@ -103,46 +111,55 @@ __device__ void tile_prefix(const ProdArgs& a, int* s_mt, int* s_wave, int tid, 
   __syncthreads();
 }
 
-__device__ __forceinline__ int find_group(const int* s_mt, int groups, int mt) {
-  int lo = 0, hi = groups - 1;  // last g with s_mt[g] <= mt
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s_mt[mid] <= mt) lo = mid; else hi = mid - 1;
+// The last g with s_mt[g] <= mt, by a whole wave: each lane looks at one group of 64.
+__device__ __forceinline__ int find_group(const int* s_mt, int groups, int mt, int lane) {
+  int n = 0;
+  for (int g0 = 0; g0 < groups; g0 += 64) {
+    const int v = s_mt[min(g0 + lane, groups - 1)];
+    n += __popcll(__ballot(g0 + lane < groups && v <= mt));
   }
-  return lo;
+  return n - 1;
 }
 
-// Stores a lane's 16 channels n .. n + 15 of output row m (sums acc, scaled by sa and the
-// group's channel scales).
+// Stores a lane's 16 channels n .. n + 15 (n a multiple of 16) of output row m: sums acc, scaled
+// by sa and by the channels' scales sw.
 template <class E, bool SWIGLU>
 __device__ __forceinline__ void store_channels(const ProdArgs& a, int64_t m, int n,
-                                               const float* w_scale, float sa,
+                                               const float (&sw)[16], float sa,
                                                const i32x16& acc) {
-  constexpr int V = Chunk<E>::V;
-  const int have = a.N - n;
+  constexpr int V = Chunk<E>::V, NO = SWIGLU ? 8 : 16;
+  const int have = SWIGLU ? (a.N - n) / 2 : a.N - n;
   if (have <= 0) return;
   float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = (float)acc[i] * sa * w_scale[n + min(i, have - 1)];
+  for (int i = 0; i < 16; ++i) v[i] = (float)acc[i] * sa * sw[i];
   if constexpr (SWIGLU) {
-    E* out = (E*)a.out + m * a.os + n / 2;
 #pragma unroll
-    for (int c = 0; c < 8; c += V) {
-      Chunk<E> o;
+    for (int i = 0; i < 8; ++i) v[i] = silu_for<E>(v[2 * i]) * v[2 * i + 1];
+  }
+  E* out = (E*)a.out + m * a.os + (SWIGLU ? n / 2 : n);
+  if (have >= NO) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        o.e[i] = from_f32<E>(silu_f32(v[2 * (c + i)]) * v[2 * (c + i) + 1]);
-      if (have / 2 > c) store_chunk(out + c, have / 2 - c, o);
+    for (int c = 0; c < NO; c += V) store_chunk(out + c, V, round_chunk<E>(v + c));
+  } else {
+#pragma unroll
+    for (int c = 0; c < NO; c += V)
+      if (have > c) store_chunk(out + c, have - c, round_chunk<E>(v + c));
+  }
+}
+
+// The scales of channels n .. n + 15 of a group, those past N repeated.
+__device__ __forceinline__ void load_scales(float (&sw)[16], const float* w_scale, int n, int N) {
+  if (n + 16 <= N) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 q = *(const u32x4_any*)(w_scale + n + 4 * i);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) sw[4 * i + b] = __uint_as_float(q[b]);
     }
   } else {
-    E* out = (E*)a.out + m * a.os + n;
 #pragma unroll
-    for (int c = 0; c < 16; c += V) {
-      Chunk<E> o;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o.e[i] = from_f32<E>(v[c + i]);
-      if (have > c) store_chunk(out + c, have - c, o);
-    }
+    for (int i = 0; i < 16; ++i) sw[i] = w_scale[min(n + i, N - 1)];
   }
 }
 
@@ -160,14 +177,15 @@ template <class E, bool SWIGLU>
 __global__ __launch_bounds__(GT) void product_any_kernel(ProdArgs a) {
   __shared__ __align__(16) int8_t s_t[2][(GM + GN) * GK];  // channels, then rows
   __shared__ int s_mt[kMaxGroups + 1];
+  __shared__ int2 s_rows[kMaxGroups];
   __shared__ int s_wave[GT / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  tile_prefix<GM>(a, s_mt, s_wave, tid, GT);
+  tile_prefix<GM>(a, s_mt, s_rows, s_wave, tid, GT);
   const int NT = (a.N + GN - 1) / GN;
   const int mt = blockIdx.x / NT, nt = blockIdx.x - mt * NT;
   if (mt >= s_mt[a.groups]) return;
-  const int g = find_group(s_mt, a.groups, mt);
-  const int2 rr = group_rows(a, g);
+  const int g = find_group(s_mt, a.groups, mt, lane);
+  const int2 rr = s_rows[g];
   const int m0 = rr.x + (mt - s_mt[g]) * GM, n0 = nt * GN;
   const int8_t* w = a.w + (int64_t)g * a.N * a.ws;
   // thread: chunk tid % 4 of rows tid / 4 + 64 i of the stage
@@ -243,13 +261,15 @@ __global__ __launch_bounds__(GT) void product_any_kernel(ProdArgs a) {
   }
   const float* w_scale = a.w_scale + (int64_t)g * a.N;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int m = m0 + wm + 32 * j + arow;
-    if (m >= rr.y) continue;
-    const float sa = a.a_scale[m];
+  for (int i = 0; i < 2; ++i) {
+    const int n = n0 + wn + 32 * i + 16 * half;
+    float sw[16];
+    load_scales(sw, w_scale, n, a.N);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      store_channels<E, SWIGLU>(a, m, n0 + wn + 32 * i + 16 * half, w_scale, sa, acc[i][j]);
+    for (int j = 0; j < 2; ++j) {
+      const int m = m0 + wm + 32 * j + arow;
+      if (m < rr.y) store_channels<E, SWIGLU>(a, m, n, sw, a.a_scale[m], acc[i][j]);
+    }
   }
 }
 
@@ -349,7 +369,7 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
     E* out = (E*)a.out + (int64_t)(m0 + m) * a.os;
     if constexpr (SWIGLU) {
       if (n0 + 2 * c < a.N)
-        out[n0 / 2 + c] = from_f32<E>(silu_f32(value(2 * c)) * value(2 * c + 1));
+        out[n0 / 2 + c] = from_f32<E>(silu_for<E>(value(2 * c)) * value(2 * c + 1));
     } else {
       if (n0 + c < a.N) out[n0 + c] = from_f32<E>(value(c));
     }
@@ -357,17 +377,19 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
 }
 
 // ------------------------------------------------------------------ large tiles
-// 64 MI rows x 64 NI channels, four waves in a 2 x 2 arrangement of 32 MI rows x 32 NI channels
-// each.  Stages of 128 contraction bytes go from memory straight into LDS (16-byte
-// global-to-LDS loads), double buffered: the loads of stage s + 2 are issued when every wave has
-// read stage s.  Rows are 128 bytes unpadded; 16-byte chunk c of a row sits at chunk
-// c ^ ((r / 2) % 8), r the row's place in its matrix instruction: the 16 lanes that LDS serves
-// at once then read 16 distinct 16-byte bank slots.  Fragments of a 32-deep step are read while
-// the previous step's matrix instructions run, also across a stage's end.
+// 32 WM MI rows x 32 WN NI channels per tile, WM x WN waves of 32 MI rows x 32 NI channels,
+// workgroups persistent over the tiles.  Stages of 128 contraction bytes go from memory straight
+// into LDS (16-byte global-to-LDS loads), double buffered: the loads of stage s + 2 are issued
+// when every wave has read stage s, and a tile's first two stages while the previous tile's
+// epilogue runs.  Rows are 128 bytes unpadded; 16-byte chunk c of a row sits at chunk
+// c ^ ((r / 2) % 8), r the row's place in its matrix instruction: the 16 lanes that LDS serves at
+// once then read 16 distinct 16-byte bank slots.  Fragments of a 32-deep step are read while the
+// previous step's matrix instructions run, also across a stage's end.  A wave whose rows (or
+// channels) lie past the group's end loads and waits with the others but multiplies nothing.
 // The loads are asm so that the compiler does not hold LDS reads back for them; they return
 // nothing to registers, and the waits for them are the stage's own.
 // Needs 16-byte aligned operands and strides and K a multiple of 16.
-constexpr int LT = 256, LK = 128;
+constexpr int LK = 128;
 
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, const int8_t* base) {
   asm volatile(
@@ -379,95 +401,140 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, const in
       : "memory");
 }
 
+// The same with 4 bytes per lane.
+__device__ __forceinline__ void load4_to_lds(uint32_t lds, uint32_t off, const float* base) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory");
+}
+
 // Every LDS access of this wave done, its loads to LDS landed, and the same for the others.
 __device__ __forceinline__ void stage_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 typedef __attribute__((address_space(3))) int8_t lds_i8_t;
+typedef __attribute__((address_space(3))) float lds_f32_t;
 
 __device__ __forceinline__ int xcd_order() {
   return (int)(blockIdx.x % 8) * (int)(gridDim.x / 8) + (int)(blockIdx.x / 8);
 }
 
-template <class E, bool SWIGLU, int MI, int NI>
-__global__ __launch_bounds__(LT, MI * NI >= 16 ? 1 : 2) void product_tile_kernel(ProdArgs a) {
-  constexpr int BM = 64 * MI, BN = 64 * NI, ROWS = BM + BN, STAGE = ROWS * LK;
-  constexpr int LPW = ROWS / 8 / (LT / 64);  // loads of a wave per stage, 8 rows each
-  extern __shared__ __align__(16) int8_t l_smem[];  // 2 stages: channels, then rows
-  __shared__ int s_mt[kMaxGroups + 1];
+// Tiles in blocks of four row tiles, channel tiles ascending inside: the 32 tiles that an XCD's
+// CUs work on at once then share 4 row and 8 channel operands in its L2.
+__device__ __forceinline__ void tile_of(int tile, int MT, int NT, int& mt, int& nt) {
+  const int block = tile / (4 * NT), in = tile - block * 4 * NT;
+  const int rows = min(4, MT - block * 4);
+  nt = in / rows;
+  mt = block * 4 + in - nt * rows;
+}
+
+template <class E, bool SWIGLU, int WM, int WN, int MI, int NI, int KS, int PER_CU>
+__global__ __launch_bounds__(64 * WM * WN * KS, WM * WN * KS * PER_CU / 4)
+void product_tile_kernel(ProdArgs a) {
+  constexpr int TW = WM * WN, LT = 64 * TW * KS;  // waves of a tile; threads
+  constexpr int BM = 32 * WM * MI, BN = 32 * WN * NI, ROWS = BM + BN, STAGE = ROWS * LK;
+  constexpr int LPW = ROWS / 8 / TW;  // loads of a wave per stage, 8 rows each
+  static_assert(LPW * 8 * TW == ROWS && BN % 64 == 0 && BM % 64 == 0);
+  // KS times 2 stages (channels, then rows), the groups' rows and first tiles
+  extern __shared__ __align__(16) int8_t l_smem[];
+  int2* const s_rows = (int2*)(l_smem + 2 * KS * STAGE);
+  int* const s_mt = (int*)(s_rows + a.groups);
+  __shared__ __align__(16) float s_scale[2][ROWS];  // of the tile's channels, then of its rows
   __shared__ int s_wave[LT / 64];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  tile_prefix<BM>(a, s_mt, s_wave, tid, LT);
-  const int NT = (a.N + BN - 1) / BN, MT = s_mt[a.groups];
+  const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ks = KS == 1 ? 0 : wave_all / TW, wave = KS == 1 ? wave_all : wave_all % TW;
+  tile_prefix<BM>(a, s_mt, s_rows, s_wave, tid, LT);
+  const int NT = (a.N + BN - 1) / BN, MT = __builtin_amdgcn_readfirstlane(s_mt[a.groups]);
   const int ntiles = MT * NT;
-  const int nst = (a.K + LK - 1) / LK;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_i8_t*)l_smem;
-  const int wn = (wave & 1) * 32 * NI, wm = (wave >> 1) * 32 * MI;
+  // stages of K; rounds of KS stages, stage KS * round + ks is this wave's
+  const int nst = (a.K + LK - 1) / LK, nfull = a.K / LK, rounds = (nst + KS - 1) / KS;
+  int8_t* const stages = l_smem + ks * 2 * STAGE;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_i8_t*)stages;
+  const int wn = (wave % WN) * 32 * NI, wm = (wave / WN) * 32 * MI;
   const int r32 = lane & 31, half = lane >> 5;
-  for (int tile = xcd_order(); tile < ntiles; tile += gridDim.x) {
-    const int mt = tile / NT, nt = tile - mt * NT;
-    const int g = __builtin_amdgcn_readfirstlane(find_group(s_mt, a.groups, mt));
-    const int2 gr = group_rows(a, g);
-    const int2 rr = make_int2(__builtin_amdgcn_readfirstlane(gr.x),
-                              __builtin_amdgcn_readfirstlane(gr.y));
-    const int m0 = __builtin_amdgcn_readfirstlane(rr.x + (mt - s_mt[g]) * BM), n0 = nt * BN;
-    const int8_t* wbase = a.w + ((int64_t)g * a.N + n0) * a.ws;
-    const int8_t* abase = a.a + (int64_t)m0 * a.as;
-    // load i of this wave: stage rows 8 (wave * LPW + i) .. + 7, lane l brings row + l / 8, chunk
-    // l % 8 in LDS; rows past the group or past N load the last valid one
-    auto chunk_of = [&](int i) {
-      const int row = (wave * LPW + i) * 8 + (lane >> 3);
-      const int r = row < BN ? row_of_channel(row & 31) : row & 31;
-      return (lane & 7) ^ ((r >> 1) & 7);
-    };
-    uint32_t off[LPW];
+
+  int tile = xcd_order();
+  if (tile >= ntiles) return;
+  int m0, n0, end;  // the tile's first row and channel, its group's last row + 1
+  const int8_t *wbase, *abase;
+  uint32_t off[LPW];
+  // load i of this wave: stage rows 8 (wave * LPW + i) .. + 7, lane l brings row + l / 8, chunk
+  // l % 8 in LDS; rows past the group or past N load the last valid one
+  auto chunk_of = [&](int i) {
+    const int row = (wave * LPW + i) * 8 + (lane >> 3);
+    const int r = row < BN ? row_of_channel(row & 31) : row & 31;
+    return (lane & 7) ^ ((r >> 1) & 7);
+  };
+  auto load_stage = [&](int round, int buf) {
+    const int st = round * KS + ks;
+    const uint32_t dst = lds0 + buf * STAGE + wave * LPW * 1024;
+    const int8_t* wk = wbase + st * LK;
+    const int8_t* ak = abase + st * LK;
+    if (st < nfull) {
+#pragma unroll
+      for (int i = 0; i < LPW; ++i)
+        load_to_lds(dst + i * 1024, off[i], (wave * LPW + i) * 8 < BN ? wk : ak);
+    } else if (st < nst) {
+      const int left = (a.K - st * LK) / 16;  // chunks of the row in this stage
+#pragma unroll 1
+      for (int i = 0; i < LPW; ++i) {
+        const int row = (wave * LPW + i) * 8 + (lane >> 3), c = chunk_of(i);
+        const int8_t* src = row < BN ? wk + (int64_t)min(row, a.N - 1 - n0) * a.ws
+                                     : ak + (int64_t)min(row - BN, end - 1 - m0) * a.as;
+        i32x4 v = i32x4{0, 0, 0, 0};  // past K
+        if (c < left) v = *(const i32x4*)(src + 16 * c);
+        *(i32x4*)(stages + buf * STAGE + (wave * LPW + i) * 1024 + lane * 16) = v;
+      }
+    }
+  };
+  // Takes up a tile: its first two stages and its scales (into half sb of their arrays).
+  auto begin = [&](int t, int sb) {
+    int mt, nt;
+    tile_of(t, MT, NT, mt, nt);
+    const int g = find_group(s_mt, a.groups, mt, lane);
+    const int2 gr = s_rows[g];
+    end = __builtin_amdgcn_readfirstlane(gr.y);
+    m0 = __builtin_amdgcn_readfirstlane(gr.x + (mt - s_mt[g]) * BM);
+    n0 = nt * BN;
+    wbase = a.w + ((int64_t)g * a.N + n0) * a.ws;
+    abase = a.a + (int64_t)m0 * a.as;
+    const uint32_t dst = (uint32_t)(uintptr_t)(lds_f32_t*)s_scale[sb];
+    for (int i = wave_all; i < ROWS / 64; i += LT / 64) {
+      const int r = i * 64 + lane;
+      if (i * 64 < BN)
+        load4_to_lds(dst + i * 256, 4 * min(r, a.N - 1 - n0),
+                     a.w_scale + (int64_t)g * a.N + n0);
+      else
+        load4_to_lds(dst + i * 256, 4 * min(r - BN, end - 1 - m0), a.a_scale + m0);
+    }
 #pragma unroll
     for (int i = 0; i < LPW; ++i) {
       const int row = (wave * LPW + i) * 8 + (lane >> 3);
       off[i] = (row < BN ? (uint32_t)min(row, a.N - 1 - n0) * (uint32_t)a.ws
-                         : (uint32_t)min(row - BN, rr.y - 1 - m0) * (uint32_t)a.as) +
+                         : (uint32_t)min(row - BN, end - 1 - m0) * (uint32_t)a.as) +
                16 * chunk_of(i);
     }
-    auto load_stage = [&](int st) {
-      const uint32_t dst = lds0 + (st & 1) * STAGE + wave * LPW * 1024;
-      const int8_t* wk = wbase + st * LK;
-      const int8_t* ak = abase + st * LK;
-      const int left = (a.K - st * LK) / 16;  // chunks of the row in this stage
-      if (left >= LK / 16) {
+    load_stage(0, 0);
+    load_stage(1, 1);
+  };
+  begin(tile, 0);
+  const int8_t* rw = stages + (wn + channel_of_row(r32)) * LK;
+  const int8_t* ra = stages + (BN + wm + r32) * LK;
+  auto read = [&](i32x4 (&fw)[NI], i32x4 (&fa)[MI], int buf, int kk) {
+    const int o = buf * STAGE + (((2 * kk + half) ^ ((r32 >> 1) & 7)) << 4);
 #pragma unroll
-        for (int i = 0; i < LPW; ++i)
-          load_to_lds(dst + i * 1024, off[i], (wave * LPW + i) * 8 < BN ? wk : ak);
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < LPW; ++i) {
-          const int row = (wave * LPW + i) * 8 + (lane >> 3), c = chunk_of(i);
-          const int8_t* src =
-              row < BN ? wk + (int64_t)min(row, a.N - 1 - n0) * a.ws
-                       : ak + (int64_t)min(row - BN, rr.y - 1 - m0) * a.as;
-          i32x4 v = i32x4{0, 0, 0, 0};  // past K
-          if (c < left) v = *(const i32x4*)(src + 16 * c);
-          *(i32x4*)(l_smem + (st & 1) * STAGE + (wave * LPW + i) * 1024 + lane * 16) = v;
-        }
-      }
-    };
+    for (int i = 0; i < NI; ++i) fw[i] = *(const i32x4*)(rw + o + i * 32 * LK);
+#pragma unroll
+    for (int j = 0; j < MI; ++j) fa[j] = *(const i32x4*)(ra + o + j * 32 * LK);
+  };
+  for (int sb = 0;; sb ^= 1) {
     i32x16 acc[NI][MI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < MI; ++j)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-    const int8_t* rw = l_smem + (wn + channel_of_row(r32)) * LK;
-    const int8_t* ra = l_smem + (BN + wm + r32) * LK;
-    auto read = [&](i32x4 (&fw)[NI], i32x4 (&fa)[MI], int buf, int kk) {
-      const int o = buf * STAGE + (((2 * kk + half) ^ ((r32 >> 1) & 7)) << 4);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) fw[i] = *(const i32x4*)(rw + o + i * 32 * LK);
-#pragma unroll
-      for (int j = 0; j < MI; ++j) fa[j] = *(const i32x4*)(ra + o + j * 32 * LK);
-    };
     auto multiply = [&](const i32x4 (&fw)[NI], const i32x4 (&fa)[MI]) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -475,77 +542,162 @@ __global__ __launch_bounds__(LT, MI * NI >= 16 ? 1 : 2) void product_tile_kernel
         for (int j = 0; j < MI; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
     };
-    i32x4 fw0[NI], fa0[MI], fw1[NI], fa1[MI];
-    load_stage(0);
+    const int m1 = m0 + wm, n1 = n0 + wn, end1 = end;
+    const bool active = m1 < end && n1 < a.N;
+    const int mine = active ? (nst - ks + KS - 1) / KS : 0;  // rounds this wave multiplies in
     stage_barrier();
-    if (nst > 1) load_stage(1);
-    read(fw0, fa0, 0, 0);
-    for (int st = 0; st < nst; ++st) {
-      const int b = st & 1;
-      read(fw1, fa1, b, 1);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < MI; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+    i32x4 fw0[NI], fa0[MI], fw1[NI], fa1[MI];
+    if (mine > 0) read(fw0, fa0, 0, 0);
+    int rd = 0;
+    for (; rd < mine; ++rd) {
+      const int buf = rd & 1;
+      read(fw1, fa1, buf, 1);
       multiply(fw0, fa0);
-      read(fw0, fa0, b, 2);
+      read(fw0, fa0, buf, 2);
       multiply(fw1, fa1);
-      read(fw1, fa1, b, 3);
+      read(fw1, fa1, buf, 3);
       multiply(fw0, fa0);
       stage_barrier();
-      if (st + 2 < nst) load_stage(st + 2);
-      if (st + 1 < nst) read(fw0, fa0, b ^ 1, 0);
+      if (rd + 2 < rounds) load_stage(rd + 2, buf);
+      if (rd + 1 < mine) read(fw0, fa0, buf ^ 1, 0);
       multiply(fw1, fa1);
     }
-    const float* w_scale = a.w_scale + (int64_t)g * a.N;
-#pragma unroll
-    for (int j = 0; j < MI; ++j) {
-      const int m = m0 + wm + 32 * j + r32;
-      if (m >= rr.y) continue;
-      const float sa = a.a_scale[m];
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        store_channels<E, SWIGLU>(a, m, n0 + wn + 32 * i + 16 * half, w_scale, sa, acc[i][j]);
+    for (; rd < rounds; ++rd) {
+      stage_barrier();
+      if (rd + 2 < rounds) load_stage(rd + 2, rd & 1);
     }
+    if constexpr (KS > 1) {  // the parts of K added up by the first (integers: exact)
+      static_assert(NI == 1 && MI == 1 && (KS - 1) * TW * 4096 <= 2 * KS * STAGE);
+      i32x4* part = (i32x4*)(l_smem + ((ks - 1) * TW + wave) * 4096) + lane;
+      if (ks > 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          part[64 * q] = i32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2],
+                               acc[0][0][4 * q + 3]};
+      }
+      stage_barrier();
+      if (ks == 0) {
+#pragma unroll
+        for (int p = 1; p < KS; ++p)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const i32x4 v = *((const i32x4*)(l_smem + ((p - 1) * TW + wave) * 4096) + lane +
+                              64 * q);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) acc[0][0][4 * q + b] += v[b];
+          }
+      }
+      stage_barrier();
+    }
+    tile += gridDim.x;
+    const bool more = tile < ntiles;
+    if (more) begin(tile, sb ^ 1);  // both stages are free, and the other half of the scales
+    if (active && ks == 0) {
+      const float* psw = s_scale[sb] + wn + 16 * half;
+      const float* psa = s_scale[sb] + BN + wm + r32;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        float sw[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) sw[q] = psw[32 * i + q];
+#pragma unroll
+        for (int j = 0; j < MI; ++j) {
+          const int m = m1 + 32 * j + r32;
+          if (m < end1)
+            store_channels<E, SWIGLU>(a, m, n1 + 32 * i + 16 * half, sw, psa[32 * j], acc[i][j]);
+        }
+      }
+    }
+    if (!more) return;
   }
 }
 
-template <class E, bool SWIGLU, int MI, int NI>
+template <class E, bool SWIGLU, int WM, int WN, int MI, int NI, int KS, int PER_CU>
 void launch_tile(const ProdArgs& a, hipStream_t s) {
-  constexpr int BM = 64 * MI, BN = 64 * NI;
-  const int64_t mt = a.M / BM + (a.offsets ? min(a.groups, a.M) : 1);
+  constexpr int BM = 32 * WM * MI, BN = 32 * WN * NI, LT = 64 * WM * WN * KS;
+  const int lds = 2 * KS * (BM + BN) * LK + 12 * a.groups + 4;
+  const auto kernel = product_tile_kernel<E, SWIGLU, WM, WN, MI, NI, KS, PER_CU>;
+  if (lds > 64 * 1024)
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                              lds);
+  const int64_t mt = a.M / BM + (a.offsets ? std::min(a.groups, a.M) : 1);
   const int64_t tiles = mt * ((a.N + BN - 1) / BN);
-  constexpr int lds = 2 * (BM + BN) * LK;
-  constexpr int per_cu = lds > 80 * 1024 ? 1 : 2;
-  static const bool big_lds = hipFuncSetAttribute(
-      (const void*)product_tile_kernel<E, SWIGLU, MI, NI>,
-      hipFuncAttributeMaxDynamicSharedMemorySize, lds) == hipSuccess;
-  (void)big_lds;
-  const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, 256 * per_cu);
-  hipLaunchKernelGGL((product_tile_kernel<E, SWIGLU, MI, NI>), dim3(grid), dim3(LT), lds, s, a);
+  const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, 256 * PER_CU);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(LT), lds, s, a);
+}
+
+// The tile shapes, and what the choice among them goes by: microseconds of one round of KS
+// stages with one tile on a CU (low) and what each further tile there adds (more), or with a
+// tile on most CUs, where the chip's power limit lowers the clock (full); microseconds a tile
+// spends outside its stages (rest).  Measured with K = 1024 .. 8192; the sum
+// over the launch's rounds came within 15% of the measured time of launches of 64 to 131072
+// rows, and its order of the shapes was the measured one but for near ties.
+struct TileShape {
+  int bm, bn, ks, per_cu;
+  float low, more, full, rest;
+};
+constexpr TileShape kShapes[] = {
+    {256, 256, 1, 1, 1.3f, 0.f, 1.8f, 5.f},  {256, 320, 1, 1, 1.6f, 0.f, 2.2f, 6.f},
+    {128, 128, 1, 2, 0.63f, 0.46f, 0.f, 2.5f}, {64, 64, 1, 4, 0.45f, 0.16f, 0.f, 1.5f},
+    {64, 64, 2, 2, 0.62f, 0.33f, 0.f, 1.5f}, {64, 64, 4, 1, 1.06f, 0.f, 0.f, 1.5f}};
+
+float tile_cost(const TileShape& t, const ProdArgs& a) {
+  // row tiles: the sizes of the groups are only known on the device
+  const float rows = (float)a.M / (float)a.groups;
+  const float mt = a.offsets ? (float)std::min(a.groups, a.M) * std::max(1.08f, rows / t.bm + 0.5f)
+                             : (float)((a.M + t.bm - 1) / t.bm);
+  const float tiles = mt * (float)((a.N + t.bn - 1) / t.bn);
+  const int nst = (a.K + LK - 1) / LK, k_rounds = (nst + t.ks - 1) / t.ks;
+  const auto round_us = [&](float on_gpu) {  // that many tiles at once
+    if (t.full > 0.f && on_gpu > 128.f) return t.full;
+    return t.low + t.more * (std::ceil(on_gpu / 256.f) - 1.f);
+  };
+  const float slots = 256.f * t.per_cu, whole = std::floor(tiles / slots);
+  const float left = tiles - whole * slots;
+  float us = whole * (k_rounds * round_us(slots) + t.rest);
+  if (left > 0.f) us += k_rounds * round_us(left) + t.rest;
+  return us;
 }
 
 template <class E, bool SWIGLU>
 void launch_product(const ProdArgs& a, hipStream_t s) {
-  const int nf = (a.N + FN - 1) / FN;
-  if (a.M <= 64) {
+  const bool aligned = !(((uintptr_t)a.a | (uintptr_t)a.w | (uintptr_t)a.as | (uintptr_t)a.ws |
+                          (uintptr_t)a.K) & 15) &&
+                       a.as < (1 << 23) && a.ws < (1 << 23);
+  // Few rows: the streaming kernel takes 16 of them as fast as one; with more the tiles win
+  // (64 rows x 5000 channels x 4096: 13.5 against 22.8 us) where alignment allows them, and for
+  // 128 rows of 128 groups the two are equal (42.0 and 42.5 us, the weights' bytes).
+  if (a.M <= 16 || (a.M <= 64 && (a.offsets || !aligned))) {
+    const int nf = (a.N + FN - 1) / FN;
     if (a.offsets || a.M <= 16)
       hipLaunchKernelGGL((product_few_kernel<E, SWIGLU, 1>), dim3(nf, a.offsets ? a.M : 1),
                          dim3(FT), 0, s, a);
-    else if (a.M <= 32)
-      hipLaunchKernelGGL((product_few_kernel<E, SWIGLU, 2>), dim3(nf), dim3(FT), 0, s, a);
     else
       hipLaunchKernelGGL((product_few_kernel<E, SWIGLU, 4>), dim3(nf), dim3(FT), 0, s, a);
     return;
   }
-  const bool aligned = !(((uintptr_t)a.a | (uintptr_t)a.w | (uintptr_t)a.as | (uintptr_t)a.ws |
-                          (uintptr_t)a.K) & 15) &&
-                       a.as < (1 << 23) && a.ws < (1 << 23);
   if (aligned) {
-    const int64_t avg = a.M / a.groups;
-    if (avg >= 512)
-      launch_tile<E, SWIGLU, 4, 4>(a, s);
-    else
-      launch_tile<E, SWIGLU, 2, 2>(a, s);
-    return;
+    int best = 0;
+    for (int i = 1; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i)
+      if (!(kShapes[i].bn == 320 && a.groups > 512) &&  // LDS
+          tile_cost(kShapes[i], a) < tile_cost(kShapes[best], a))
+        best = i;
+    switch (best) {
+      case 0: return launch_tile<E, SWIGLU, 4, 2, 2, 4, 1, 1>(a, s);
+      case 1: return launch_tile<E, SWIGLU, 4, 2, 2, 5, 1, 1>(a, s);
+      case 2: return launch_tile<E, SWIGLU, 4, 2, 1, 2, 1, 2>(a, s);
+      case 3: return launch_tile<E, SWIGLU, 2, 2, 1, 1, 1, 4>(a, s);
+      case 4: return launch_tile<E, SWIGLU, 2, 2, 1, 1, 2, 2>(a, s);
+      default: return launch_tile<E, SWIGLU, 2, 2, 1, 1, 4, 1>(a, s);
+    }
   }
-  const int64_t mt = a.M / GM + (a.offsets ? min(a.groups, a.M) : 1);
+  const int64_t mt = a.M / GM + (a.offsets ? std::min(a.groups, a.M) : 1);
   const int64_t nt = (a.N + GN - 1) / GN;
   hipLaunchKernelGGL((product_any_kernel<E, SWIGLU>), dim3((unsigned)(mt * nt)), dim3(GT), 0, s,
                      a);

@@ -28,7 +28,7 @@ template <class E>
 __device__ __forceinline__ E from_f32(float f);
 template <>
 __device__ __forceinline__ bf16_t from_f32<bf16_t>(float f) {
-  return bf16_t{f32_to_bf16_rne(f)};
+  return bf16_t{__builtin_bit_cast(uint16_t, (__bf16)f)};  // v_cvt_pk_bf16_f32: to nearest even
 }
 template <>
 __device__ __forceinline__ fp16_t from_f32<fp16_t>(float f) {
@@ -46,6 +46,29 @@ union Chunk {
   u32x4 q;
   E e[V];
 };
+
+// V values rounded to a chunk (two at a time: one instruction converts a pair).
+template <class E>
+__device__ __forceinline__ Chunk<E> round_chunk(const float* v) {
+  Chunk<E> c;
+  if constexpr (sizeof(E) == 2) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 p = {v[2 * i], v[2 * i + 1]};
+      if constexpr (__is_same(E, bf16_t))
+        c.q[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+      else
+        c.q[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, fp16x2));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.e[i] = v[i];
+  }
+  return c;
+}
 
 // The chunk at p, of which the first n elements belong to the row (n >= V: all); elements past
 // the row are not touched and read as zero.

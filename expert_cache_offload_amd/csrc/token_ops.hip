@@ -350,10 +350,7 @@ __global__ __launch_bounds__(TOK_T) void combine_kernel(CombineArgs a) {
     for (int i = 0; i < V; ++i) acc[i] = W ? fmaf(wj, to_f32(v.e[i]), acc[i])
                                            : acc[i] + to_f32(v.e[i]);
   }
-  Chunk<E> o;
-#pragma unroll
-  for (int i = 0; i < V; ++i) o.e[i] = from_f32<E>(acc[i]);
-  store_chunk((E*)a.out + (int64_t)t * a.os + (int64_t)c * V, n, o);
+  store_chunk((E*)a.out + (int64_t)t * a.os + (int64_t)c * V, n, round_chunk<E>(acc));
 }
 
 struct CombineGradArgs {
@@ -398,10 +395,10 @@ __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) 
       for (int i = 0; i < V; ++i) sum = fmaf(to_f32(g.e[i]), to_f32(v.e[i]), sum);
     }
     if (a.drows) {
-      Chunk<E> o;
+      float v[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) o.e[i] = from_f32<E>(w * to_f32(g.e[i]));
-      store_chunk(dr + (int64_t)c * V, n, o);
+      for (int i = 0; i < V; ++i) v[i] = w * to_f32(g.e[i]);
+      store_chunk(dr + (int64_t)c * V, n, round_chunk<E>(v));
     }
   }
   if (a.dw) {
