@@ -11,6 +11,7 @@
 // and the output is stored in 16-byte pieces.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "row_ops.h"
 
@@ -121,8 +122,20 @@ __device__ __forceinline__ int find_group(const int* s_mt, int groups, int mt, i
   return n - 1;
 }
 
-// Stores a lane's 16 channels n .. n + 15 (n a multiple of 16) of output row m: sums acc, scaled
-// by sa and by the channels' scales sw.
+// The values of a lane's 16 channels (8 outputs with SwiGLU): sums acc, scaled by the row's sa and
+// the channels' sw.
+template <class E, bool SWIGLU>
+__device__ __forceinline__ void channel_values(float (&v)[16], const float (&sw)[16], float sa,
+                                               const i32x16& acc) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = (float)acc[i] * sa * sw[i];
+  if constexpr (SWIGLU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = silu_for<E>(v[2 * i]) * v[2 * i + 1];
+  }
+}
+
+// Stores a lane's 16 channels n .. n + 15 (n a multiple of 16) of output row m.
 template <class E, bool SWIGLU>
 __device__ __forceinline__ void store_channels(const ProdArgs& a, int64_t m, int n,
                                                const float (&sw)[16], float sa,
@@ -131,20 +144,38 @@ __device__ __forceinline__ void store_channels(const ProdArgs& a, int64_t m, int
   const int have = SWIGLU ? (a.N - n) / 2 : a.N - n;
   if (have <= 0) return;
   float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = (float)acc[i] * sa * sw[i];
-  if constexpr (SWIGLU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = silu_for<E>(v[2 * i]) * v[2 * i + 1];
-  }
+  channel_values<E, SWIGLU>(v, sw, sa, acc);
   E* out = (E*)a.out + m * a.os + (SWIGLU ? n / 2 : n);
-  if (have >= NO) {
 #pragma unroll
-    for (int c = 0; c < NO; c += V) store_chunk(out + c, V, round_chunk<E>(v + c));
-  } else {
+  for (int c = 0; c < NO; c += V)
+    if (have > c) store_chunk(out + c, have - c, round_chunk<E>(v + c));
+}
+
+// 32 output rows of RB bytes each that a wave has put into its LDS (row r's 16-byte chunk c at
+// chunk c ^ swz(r)) go to memory with neighbouring lanes on neighbouring chunks: a request per 64
+// bytes instead of one per 16, which is what the stores of a tile cost otherwise (a launch
+// that writes 403 MB: 165 us with a lane per row, 126 so).
+// A wave's LDS accesses execute in order; this keeps the compiler, which sees one lane's only, from
+// reordering or merging them where lanes read what others wrote.
+__device__ __forceinline__ void wave_lds_order() { asm volatile("" ::: "memory"); }
+
+template <int RB>
+__device__ __forceinline__ int out_swz(int row) {
+  return RB == 64 ? (row >> 2) & 3 : (row >> 3) & 1;
+}
+template <class E, int RB>
+__device__ __forceinline__ void store_rows(const int8_t* stage, int lane, E* out, int64_t os,
+                                           int rows, int cols) {
+  constexpr int CPR = RB / 16, V = Chunk<E>::V;
+  Chunk<E> v[CPR / 2];
+  wave_lds_order();
 #pragma unroll
-    for (int c = 0; c < NO; c += V)
-      if (have > c) store_chunk(out + c, have - c, round_chunk<E>(v + c));
+  for (int t = 0; t < CPR / 2; ++t) v[t].q = *(const u32x4*)(stage + t * 1024 + lane * 16);
+  wave_lds_order();
+#pragma unroll
+  for (int t = 0; t < CPR / 2; ++t) {
+    const int row = t * (64 / CPR) + lane / CPR, c = (lane % CPR) ^ out_swz<RB>(row);
+    if (row < rows && c * V < cols) store_chunk(out + row * os + c * V, cols - c * V, v[t]);
   }
 }
 
@@ -493,7 +524,7 @@ void product_tile_kernel(ProdArgs a) {
       }
     }
   };
-  // Takes up a tile: its first two stages and its scales (into half sb of their arrays).
+  // Takes up a tile: its first stage and its scales (into half sb of their arrays).
   auto begin = [&](int t, int sb) {
     int mt, nt;
     tile_of(t, MT, NT, mt, nt);
@@ -521,7 +552,6 @@ void product_tile_kernel(ProdArgs a) {
                16 * chunk_of(i);
     }
     load_stage(0, 0);
-    load_stage(1, 1);
   };
   begin(tile, 0);
   const int8_t* rw = stages + (wn + channel_of_row(r32)) * LK;
@@ -546,6 +576,7 @@ void product_tile_kernel(ProdArgs a) {
     const bool active = m1 < end && n1 < a.N;
     const int mine = active ? (nst - ks + KS - 1) / KS : 0;  // rounds this wave multiplies in
     stage_barrier();
+    if (rounds > 1) load_stage(1, 1);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -597,20 +628,56 @@ void product_tile_kernel(ProdArgs a) {
     }
     tile += gridDim.x;
     const bool more = tile < ntiles;
-    if (more) begin(tile, sb ^ 1);  // both stages are free, and the other half of the scales
+    if (more) begin(tile, sb ^ 1);  // the first half of the stages, the other half of the scales
     if (active && ks == 0) {
+      // the second half of the stages is free until the next tile's first barrier: 2 KiB a wave
+      constexpr int V = Chunk<E>::V, OB = 16 * (int)sizeof(E) / (SWIGLU ? 2 : 1);
+      static_assert(TW * 2048 <= STAGE);
+      int8_t* const stage = l_smem + STAGE + wave * 2048;
       const float* psw = s_scale[sb] + wn + 16 * half;
       const float* psa = s_scale[sb] + BN + wm + r32;
+      const auto put = [&](auto rb, int chunk, const float* v) {
+        constexpr int RB = decltype(rb)::value;
+        *(u32x4*)(stage + r32 * RB + ((chunk ^ out_swz<RB>(r32)) << 4)) = round_chunk<E>(v).q;
+      };
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        float sw[16];
+      for (int j = 0; j < MI; ++j) {
+        const int rows = end1 - m1 - 32 * j;  // of the group from this row tile on
+        E* const out = (E*)a.out + (int64_t)(m1 + 32 * j) * a.os;
 #pragma unroll
-        for (int q = 0; q < 16; ++q) sw[q] = psw[32 * i + q];
+        for (int i = 0; i < NI; ++i) {
+          const int n = n1 + 32 * i;
+          float sw[16], v[16];
 #pragma unroll
-        for (int j = 0; j < MI; ++j) {
-          const int m = m1 + 32 * j + r32;
-          if (m < end1)
-            store_channels<E, SWIGLU>(a, m, n1 + 32 * i + 16 * half, sw, psa[32 * j], acc[i][j]);
+          for (int q = 0; q < 16; ++q) sw[q] = psw[32 * i + q];
+          channel_values<E, SWIGLU>(v, sw, psa[32 * j], acc[i][j]);
+          if constexpr (OB == 16) {  // two channel tiles fill 64 bytes of a row
+            constexpr bool odd_end = NI % 2 == 1;
+            if (odd_end && i == NI - 1) {
+              put(std::integral_constant<int, 32>{}, half, v);
+              store_rows<E, 32>(stage, lane, out + n / 2, a.os, rows, (a.N - n) / 2);
+            } else {
+              put(std::integral_constant<int, 64>{}, 2 * (i & 1) + half, v);
+              if (i & 1)
+                store_rows<E, 64>(stage, lane, out + (n - 32) / 2, a.os, rows,
+                                  (a.N - n + 32) / 2);
+            }
+          } else if constexpr (OB == 32) {
+            put(std::integral_constant<int, 64>{}, 2 * half, v);
+            put(std::integral_constant<int, 64>{}, 2 * half + 1, v + V);
+            const int c = SWIGLU ? n / 2 : n;
+            store_rows<E, 64>(stage, lane, out + c, a.os, rows, (SWIGLU ? a.N / 2 : a.N) - c);
+          } else {  // fp32: a lane holds 64 bytes of its row; one half of the wave at a time
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (half == h) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  put(std::integral_constant<int, 64>{}, c, v + 4 * c);
+              }
+              store_rows<E, 64>(stage, lane, out + n + 16 * h, a.os, rows, a.N - n - 16 * h);
+            }
+          }
         }
       }
     }

@@ -424,6 +424,31 @@ def test_product_one_weight(env, M, N, K, pad, at, kind, swiglu):
     _check_product(env, a, a_scale, w, w_scale, N, 1, None, swiglu, kind)
 
 
+LARGE = [(4090, 4098, 272, 0, 0), (8190, 2002, 160, 16, 16), (2300, 2500, 400, 0, 0),
+         (4001, 4990, 656, 0, 0), (70, 130, 4112, 0, 0), (1500, 1300, 128, 0, 0)]
+
+
+@pytest.mark.parametrize("M,N,K,pad,at", LARGE)
+@pytest.mark.parametrize("kind,swiglu", [("bf16", False), ("bf16", True), ("fp16", True),
+                                         ("fp32", False), ("fp32", True)])
+def test_product_large(env, M, N, K, pad, at, kind, swiglu):
+    """Every tile shape, with rows and channels that end inside a tile."""
+    test_product_one_weight(env, M, N, K, pad, at, kind, swiglu)
+
+
+@pytest.mark.parametrize("counts", [[1000, 0, 1731, 1, 1290, 978], [90, 300, 33, 64, 65, 127, 0],
+                                    [700] * 9 + [5000]])
+@pytest.mark.parametrize("kind,swiglu", [("bf16", True), ("fp16", False), ("fp32", False),
+                                         ("fp32", True)])
+def test_product_by_group_large(env, counts, kind, swiglu):
+    torch = env[0]
+    G, M, N, K = len(counts), sum(counts) + 3, 1186, 400
+    g = _gen(torch, M)
+    a, w = _codes(torch, g, M, K), _codes(torch, g, G * N, K)
+    a_scale, w_scale = _scales(torch, g, M, G * N)
+    _check_product(env, a, a_scale, w, w_scale, N, G, _offsets(torch, counts, 1), swiglu, kind)
+
+
 def _offsets(torch, counts, first=0):
     v = [first]
     for c in counts:
