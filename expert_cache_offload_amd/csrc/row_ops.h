@@ -20,6 +20,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // address that happens to be aligned costs nothing extra.
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef uint64_t u64_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
 
 __device__ __forceinline__ float to_f32(bf16_t e) { return __uint_as_float((uint32_t)e.v << 16); }
 __device__ __forceinline__ float to_f32(fp16_t e) { return (float)e; }
@@ -71,12 +72,16 @@ __device__ __forceinline__ Chunk<E> round_chunk(const float* v) {
 }
 
 // The chunk at p, of which the first n elements belong to the row (n >= V: all); elements past
-// the row are not touched and read as zero.
-template <class E>
+// the row are not touched and read as zero.  STREAM: nothing reads these bytes again soon, so they
+// pass the caches by.
+template <class E, bool STREAM = false>
 __device__ __forceinline__ Chunk<E> load_chunk(const E* p, int n) {
   Chunk<E> c;
   if (n >= Chunk<E>::V) {
-    c.q = *(const u32x4_any*)p;
+    if constexpr (STREAM)
+      c.q = __builtin_nontemporal_load((const u32x4_any*)p);
+    else
+      c.q = *(const u32x4_any*)p;
   } else {
     c.q = u32x4{0, 0, 0, 0};
 #pragma unroll
@@ -85,10 +90,13 @@ __device__ __forceinline__ Chunk<E> load_chunk(const E* p, int n) {
   }
   return c;
 }
-template <class E>
+template <class E, bool STREAM = false>
 __device__ __forceinline__ void store_chunk(E* p, int n, const Chunk<E>& c) {
   if (n >= Chunk<E>::V) {
-    *(u32x4_any*)p = c.q;
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(c.q, (u32x4_any*)p);
+    else
+      *(u32x4_any*)p = c.q;
   } else {
 #pragma unroll
     for (int i = 0; i < Chunk<E>::V; ++i)
@@ -123,84 +131,115 @@ __device__ __forceinline__ RowQuant row_quant(uint32_t max_bits) {
   return r;
 }
 
-// 16-bit inputs in mode 1: 127 x has at most 18 significant bits, so the residual 127 x - q m of
-// the candidate q is exact in fp32 and decides the rounding.  fp32 inputs: the quotient's error
-// is below 3 * 2^-24 * 127 < 2^-15; candidates that near a tie are decided in 64 bits, where
-// 127 x is exact and a quotient that is no tie differs from one by 2^-33 at least.
+// The bits of 1.5 * 2^23 + 127 x / m, whose low byte is the code (fp32 addition rounds to
+// nearest even at that size).  t = 127 x, y = t / m up to 2 roundings, and y + (t - y m) / m is
+// the quotient to half a step: where the quotient is a tie it is a number of fp32 and comes out
+// exactly.  16-bit inputs: t is exact (18 bits) and a quotient 127 X 2^e / M that is no tie (X and M
+// of 11 bits) is 2^e / 4094 from one at least, its error below 127 * 2^(e - 22): the rounding is
+// right.  fp32 inputs: t may be rounded; quotients within 2^-14 of a tie (their error is below
+// 2^-15) are decided in 64 bits, where 127 x is exact and a quotient that is no tie differs from
+// one by 2^-33 at least.
 template <class E>
-__device__ __forceinline__ int quant_code(float x, const RowQuant& r) {
-  if (r.mode == 0) return 0;
-  if (r.mode == 2) return (int)rint(127.0 * (double)x / (double)r.m);
+__device__ __forceinline__ uint32_t quant_bits(float x, const RowQuant& r) {
   const float t = 127.0f * x;
-  const float y = t * r.inv;
-  float q = rintf(y);
-  if constexpr (sizeof(E) == 2) {
-    const float d = 2.0f * fmaf(-q, r.m, t);
-    const bool odd = (int)q & 1;
-    if (d > r.m || (d == r.m && odd)) q += 1.0f;
-    if (d < -r.m || (d == -r.m && odd)) q -= 1.0f;
-    return (int)q;
-  } else {
-    if (fabsf(fabsf(y - q) - 0.5f) < 0x1p-14f)
-      return (int)rint(127.0 * (double)x / (double)r.m);
-    return (int)q;
+  float y = t * r.inv;
+  y = fmaf(fmaf(-y, r.m, t), r.inv, y);
+  if constexpr (sizeof(E) == 4) {
+    if (fabsf(fabsf(y - rintf(y)) - 0.5f) < 0x1p-14f) y = (float)rint(127.0 * (double)x / (double)r.m);
   }
+  return __float_as_uint(y + 12582912.0f);
+}
+// The same for rows whose largest magnitude fp32 arithmetic does not serve.
+__device__ __forceinline__ uint32_t quant_bits_wide(float x, const RowQuant& r) {
+  return r.mode == 0 ? 0u : (uint32_t)(int)rint(127.0 * (double)x / (double)r.m);
 }
 
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 |
-         (uint32_t)(d & 255) << 24;
-}
-
-// Four codes of elements e[0..3].
+// The codes of one chunk, four to a word.
 template <class E>
-__device__ __forceinline__ uint32_t quant4(const E* e, const RowQuant& r) {
-  return pack4(quant_code<E>(to_f32(e[0]), r), quant_code<E>(to_f32(e[1]), r),
-               quant_code<E>(to_f32(e[2]), r), quant_code<E>(to_f32(e[3]), r));
+struct Codes {
+  static constexpr int W = Chunk<E>::V / 4;
+  uint32_t w[W];
+};
+template <class E>
+__device__ __forceinline__ Codes<E> quant_chunk(const Chunk<E>& c, const RowQuant& r) {
+  Codes<E> o;
+#pragma unroll
+  for (int i = 0; i < Codes<E>::W; ++i) {
+    uint32_t b[4];
+    if (r.mode == 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) b[k] = quant_bits<E>(to_f32(c.e[4 * i + k]), r);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) b[k] = quant_bits_wide(to_f32(c.e[4 * i + k]), r);
+    }
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+    o.w[i] = lo | hi;
+  }
+  return o;
+}
+template <class E, bool STREAM = false>
+__device__ __forceinline__ void store_codes(int8_t* p, int n, const Codes<E>& c) {
+  constexpr int V = Chunk<E>::V;
+  if (n >= V) {
+    if constexpr (V == 8) {
+      const uint64_t v = (uint64_t)c.w[1] << 32 | c.w[0];
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(v, (u64_any*)p);
+      else
+        *(u64_any*)p = v;
+    } else {
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(c.w[0], (u32_any*)p);
+      else
+        *(u32_any*)p = c.w[0];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = (int8_t)(c.w[i / 4] >> (8 * (i % 4)));
+  }
 }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)v, s);
-    v = v > o ? v : o;
-  }
-  return v;
-}
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
   return v;
 }
 
+// The larger of m and the largest abs_bits() of a chunk.
 template <class E>
 __device__ __forceinline__ uint32_t chunk_max_bits(const Chunk<E>& c, uint32_t m) {
+  if constexpr (sizeof(E) == 4) {
 #pragma unroll
-  for (int i = 0; i < Chunk<E>::V; ++i) {
-    const uint32_t b = abs_bits(to_f32(c.e[i]));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = c.q[i] & 0x7fffffffu;
+      m = m > b ? m : b;
+    }
+  } else {  // magnitudes of 16 bits order as their bits do: pairs at a time
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 p = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p = __builtin_elementwise_max(p, __builtin_bit_cast(u16x2, c.q[i] & 0x7fff7fffu));
+    Chunk<E> big;
+    big.q.x = p[0] > p[1] ? p[0] : p[1];
+    const uint32_t b = abs_bits(to_f32(big.e[0]));
     m = m > b ? m : b;
   }
   return m;
 }
 
-// The codes of one chunk, the first n of which belong to the row.
-template <class E>
-__device__ __forceinline__ void store_codes(int8_t* p, int n, const Chunk<E>& c,
-                                            const RowQuant& r) {
-  constexpr int V = Chunk<E>::V;
-  uint32_t w[V / 4];
+// The largest of m over groups of G neighbouring lanes (G <= 64).
+template <int G>
+__device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) w[i] = quant4(c.e + 4 * i, r);
-  if (n >= V) {
-    if constexpr (V == 8)
-      *(u64_any*)p = (uint64_t)w[1] << 32 | w[0];
-    else
-      __builtin_memcpy(p, w, 4);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) p[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+  for (int s = G / 2; s > 0; s >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, s);
+    v = v > o ? v : o;
   }
+  return v;
 }
 
 inline size_t elem_bytes(int type) {

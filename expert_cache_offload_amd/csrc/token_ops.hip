@@ -23,7 +23,14 @@ constexpr int kChunkIds = 1024;     // assignments of a counted chunk (whole tok
 constexpr int kChunkWaves = kChunkIds / 64;
 constexpr int kSubTokens = 16;      // tokens a workgroup of the move kernel sorts and moves
 constexpr int kMaxT = 1 << 20;
+// A rows matrix above this is streamed past the caches (non-temporal loads and stores): it would
+// not be there any more for whoever reads it next, and the chip moves it faster so (16384 tokens
+// of 8 rows, 2048 bf16: sort 137 -> 116 us, combine 118 -> 102, its gradient 226 -> 207, 131072 rows
+// of 768 quantised 54.7 -> 52.0; a gradient over 34 MB, which stays in the 256 MB cache, got slower
+// so, 13.7 -> 15.4 us).
+constexpr int64_t kStreamBytes = 128 << 20;
 constexpr int SCAN_T = 1024;
+constexpr int kScanHeld = 16;
 
 struct SortArgs {
   const int* ids;
@@ -47,48 +54,90 @@ __device__ __forceinline__ int key_of_id(int id, int E) {
   return (unsigned)id < (unsigned)E ? id : 0x7fffffff;
 }
 
-// Copies one row of H elements to k rows of the sorted matrix, threads [tid, nthr) of it over
-// columns [c0, c1) in chunks.
-template <class E>
+// Chunks of a row that a thread holds at once.
+constexpr int kHeld = 4;
+
+// Copies a row's chunks [c0, c1) to its k places, threads tid of nthr; kHeld loads are in flight
+// before the first store.  A choice that was dropped has place -1.
+template <class E, bool STREAM>
 __device__ __forceinline__ void copy_row(const E* x, int H, const int* place, int k, E* rows,
                                          int64_t rs, int c0, int c1, int tid, int nthr) {
   constexpr int V = Chunk<E>::V;
-  for (int c = c0 + tid; c < c1; c += nthr) {
-    const int n = H - c * V;
-    const Chunk<E> v = load_chunk(x + (int64_t)c * V, n);
+  for (int c = c0 + tid; c < c1; c += kHeld * nthr) {
+    Chunk<E> v[kHeld];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const int ch = c + h * nthr;
+      if (ch < c1) v[h] = load_chunk(x + (int64_t)ch * V, H - ch * V);
+    }
     for (int j = 0; j < k; ++j) {
       const int p = place[j];
-      if (p >= 0) store_chunk(rows + (int64_t)p * rs + (int64_t)c * V, n, v);
+      if (p < 0) continue;
+      E* const out = rows + (int64_t)p * rs;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        const int ch = c + h * nthr;
+        if (ch < c1) store_chunk<E, STREAM>(out + (int64_t)ch * V, H - ch * V, v[h]);
+      }
     }
   }
 }
 
-// The same with the row's 8-bit codes.
-template <class E>
-__device__ __forceinline__ void quant_row_to(const E* x, int H, const RowQuant& r,
-                                             const int* place, int k, int8_t* rows, int64_t rs,
-                                             float* row_scale, int tid, int nthr) {
+// A row of H elements by G neighbouring lanes (G > 64: the whole workgroup): its scale and its
+// codes, computed once.  The row stays in registers between the maximum and the codes if G lanes
+// hold it (kHeld chunks each), else it is read again.  put(c, n, codes): the codes of chunk c,
+// of whose elements n are left.
+template <class E, int G, class Put>
+__device__ __forceinline__ RowQuant quant_row(const E* x, int H, int lane, uint32_t* s_max,
+                                              Put&& put) {
   constexpr int V = Chunk<E>::V;
   const int nc = (H + V - 1) / V;
-  for (int c = tid; c < nc; c += nthr) {
-    const int n = H - c * V;
-    const Chunk<E> v = load_chunk(x + (int64_t)c * V, n);
-    for (int j = 0; j < k; ++j) {
-      const int p = place[j];
-      if (p >= 0) store_codes(rows + (int64_t)p * rs + (int64_t)c * V, n, v, r);
-    }
-  }
-  if (tid < k && place[tid] >= 0) row_scale[place[tid]] = r.scale;
-}
-
-template <class E>
-__device__ __forceinline__ uint32_t row_max_bits(const E* x, int H, int tid, int nthr) {
-  constexpr int V = Chunk<E>::V;
-  const int nc = (H + V - 1) / V;
+  Chunk<E> v[kHeld];
   uint32_t m = 0;
-  for (int c = tid; c < nc; c += nthr)
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int c = lane + h * G;
+    if (c < nc) v[h] = load_chunk(x + (int64_t)c * V, H - c * V);
+  }
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (lane + h * G < nc) m = chunk_max_bits(v[h], m);
+  for (int c = lane + kHeld * G; c < nc; c += G)
     m = chunk_max_bits(load_chunk(x + (int64_t)c * V, H - c * V), m);
-  return m;
+  if constexpr (G <= 64) {
+    m = group_max_u32<G>(m);
+  } else {
+    m = group_max_u32<64>(m);
+    if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < G / 64; ++w) m = m > s_max[w] ? m : s_max[w];
+  }
+  const RowQuant r = row_quant(m);
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int c = lane + h * G;
+    if (c < nc) put(c, H - c * V, quant_chunk(v[h], r));
+  }
+  for (int c = lane + kHeld * G; c < nc; c += G)
+    put(c, H - c * V, quant_chunk(load_chunk(x + (int64_t)c * V, H - c * V), r));
+  return r;
+}
+
+// The codes of a token's row to its k places.
+template <class E, int G, bool STREAM>
+__device__ __forceinline__ void quant_row_to(const E* x, int H, const int* place, int k,
+                                             int8_t* rows, int64_t rs, float* row_scale, int lane,
+                                             uint32_t* s_max) {
+  constexpr int V = Chunk<E>::V;
+  const RowQuant r =
+      quant_row<E, G>(x, H, lane, s_max, [&](int c, int n, const Codes<E>& codes) {
+        for (int j = 0; j < k; ++j) {
+          const int p = place[j];
+          if (p >= 0) store_codes<E, STREAM>(rows + (int64_t)p * rs + (int64_t)c * V, n, codes);
+        }
+      });
+  if (lane < k && place[lane] >= 0) row_scale[place[lane]] = r.scale;
 }
 
 // offsets[0..E] from per-expert totals in LDS, one workgroup of nthr threads.
@@ -146,8 +195,6 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
     return;
   }
   const E* x = (const E*)a.x + (int64_t)t * a.xs;
-  uint32_t mb = 0;
-  if constexpr (I8) mb = wave_max_u32(row_max_bits(x, a.H, tid, TOK_T));
   int own[kMaxTopK], cnt[kMaxTopK];
 #pragma unroll
   for (int j = 0; j < kMaxTopK; ++j) {
@@ -165,7 +212,6 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
 #pragma unroll
   for (int j = 0; j < kMaxTopK; ++j)
     if (j < a.k && lane == 0) s_cnt[wave][j] = cnt[j];
-  if (lane == 0) s_max[wave] = mb;
   __syncthreads();
   if (tid < a.k) {
     int p = 0;
@@ -182,16 +228,13 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
   __syncthreads();
   if (!a.x) return;
   if constexpr (I8) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int w = 0; w < TOK_T / 64; ++w) m = m > s_max[w] ? m : s_max[w];
-    quant_row_to(x, a.H, row_quant(m), s_place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, tid,
-                 TOK_T);
+    quant_row_to<E, TOK_T, false>(x, a.H, s_place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, tid,
+                                  s_max);
   } else {
     const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
     const int per = (nc + gridDim.y - 1) / gridDim.y;
     const int c0 = blockIdx.y * per, c1 = min(nc, c0 + per);
-    copy_row(x, a.H, s_place, a.k, (E*)a.rows, a.rs, c0, c1, tid, TOK_T);
+    copy_row<E, false>(x, a.H, s_place, a.k, (E*)a.rows, a.rs, c0, c1, tid, TOK_T);
   }
 }
 
@@ -223,9 +266,16 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
   const int nseg = SCAN_T / ep, e = threadIdx.x & (ep - 1), g = threadIdx.x / ep;
   const int per = (a.nblk + nseg - 1) / nseg;
   const int b0 = min(a.nblk, g * per), b1 = min(a.nblk, b0 + per);
+  // the counts of up to kScanHeld chunks stay in registers between the passes
+  int held[kScanHeld];
   int sum = 0;
+  const int* base = a.base + (int64_t)b0 * a.E + e;
+#pragma unroll
+  for (int i = 0; i < kScanHeld; ++i) held[i] = e < a.E && b0 + i < b1 ? base[(int64_t)i * a.E] : 0;
+#pragma unroll
+  for (int i = 0; i < kScanHeld; ++i) sum += held[i];
   if (e < a.E)
-    for (int b = b0; b < b1; ++b) sum += a.base[(int64_t)b * a.E + e];
+    for (int i = kScanHeld; b0 + i < b1; ++i) sum += base[(int64_t)i * a.E];
   s_seg[threadIdx.x] = sum;
   __syncthreads();
   if (g == 0 && e < a.E) {
@@ -243,10 +293,15 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
   for (int i = threadIdx.x; i <= a.E; i += SCAN_T) a.offsets[i] = s_off[i];
   if (e < a.E) {
     int run = s_off[e] + s_seg[threadIdx.x];
-    for (int b = b0; b < b1; ++b) {
-      const int64_t i = (int64_t)b * a.E + e;
-      const int v = a.base[i];
-      a.base[i] = run;
+    int* out = a.base + (int64_t)b0 * a.E + e;
+#pragma unroll
+    for (int i = 0; i < kScanHeld; ++i) {
+      if (b0 + i < b1) out[(int64_t)i * a.E] = run;
+      run += held[i];
+    }
+    for (int i = kScanHeld; b0 + i < b1; ++i) {
+      const int v = out[(int64_t)i * a.E];
+      out[(int64_t)i * a.E] = run;
       run += v;
     }
   }
@@ -255,11 +310,12 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
 // Third: a workgroup takes kSubTokens tokens of a chunk, ranks the chunk's ids up to its own last
 // one (a wave finds the lanes that hold its id by ballots over the id's bits; counts per wave and
 // expert in LDS), writes their places and moves their rows, a wave per token.
-template <class E, bool I8>
+template <class E, bool I8, bool WIDE, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int subs) {
   extern __shared__ __align__(16) uint16_t s_cnt[];  // [kChunkWaves][E]
   __shared__ int s_id[kSubTokens * kMaxTopK], s_rank[kSubTokens * kMaxTopK];
   __shared__ int s_place[kSubTokens * kMaxTopK];
+  __shared__ uint32_t s_max[2][TOK_T / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x / subs, sub = blockIdx.x % subs;
   const int t_blk = b * a.tok_blk;
@@ -300,15 +356,21 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int subs) 
   }
   __syncthreads();
   if (!a.x) return;
-  for (int t = t0 + wave; t < t1; t += TOK_T / 64) {
-    const E* x = (const E*)a.x + (int64_t)t * a.xs;
-    const int* place = s_place + (t - t0) * a.k;
-    if constexpr (I8) {
-      const RowQuant r = row_quant(wave_max_u32(row_max_bits(x, a.H, lane, 64)));
-      quant_row_to(x, a.H, r, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, lane, 64);
-    } else {
-      const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
-      copy_row(x, a.H, place, a.k, (E*)a.rows, a.rs, 0, nc, lane, 64);
+  if constexpr (I8 && WIDE) {  // rows that only the whole workgroup holds
+    for (int t = t0; t < t1; ++t)
+      quant_row_to<E, TOK_T, STREAM>((const E*)a.x + (int64_t)t * a.xs, a.H,
+                                     s_place + (t - t0) * a.k, a.k, (int8_t*)a.rows, a.rs,
+                                     a.row_scale, tid, s_max[t & 1]);
+  } else {
+    for (int t = t0 + wave; t < t1; t += TOK_T / 64) {
+      const E* x = (const E*)a.x + (int64_t)t * a.xs;
+      const int* place = s_place + (t - t0) * a.k;
+      if constexpr (I8)
+        quant_row_to<E, 64, STREAM>(x, a.H, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, lane,
+                                    nullptr);
+      else
+        copy_row<E, STREAM>(x, a.H, place, a.k, (E*)a.rows, a.rs, 0,
+                            (a.H + Chunk<E>::V - 1) / Chunk<E>::V, lane, 64);
     }
   }
 }
@@ -326,12 +388,14 @@ struct CombineArgs {
 };
 
 // y[t] = sum_j w[t][j] rows[place[t][j]], fp32, j ascending, rounded once.  A thread holds one
-// 16-byte chunk of one token's row; 2^tpt_log threads share a token.
-template <class E, bool W>
+// 16-byte chunk of one token's row and has the loads of eight choices in flight; 2^tpt_log
+// threads share a token (UNI: whole waves do, so places and weights are scalar loads).
+template <class E, bool W, bool UNI, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void combine_kernel(CombineArgs a) {
-  constexpr int V = Chunk<E>::V;
+  constexpr int V = Chunk<E>::V, HELD = 8;
   const int64_t g = (int64_t)blockIdx.x * TOK_T + threadIdx.x;
-  const int t = (int)(g >> a.tpt_log);
+  int t = (int)(g >> a.tpt_log);
+  if constexpr (UNI) t = __builtin_amdgcn_readfirstlane(t);
   const int c = (int)(g & ((1 << a.tpt_log) - 1)) + ((int)blockIdx.y << a.tpt_log);
   const int n = a.H - c * V;
   if (t >= a.T || n <= 0) return;
@@ -341,14 +405,23 @@ __global__ __launch_bounds__(TOK_T) void combine_kernel(CombineArgs a) {
   const int* place = a.place + (int64_t)t * a.k;
   const float* w = W ? a.w + (int64_t)t * a.k : nullptr;
   const E* rows = (const E*)a.rows + (int64_t)c * V;
-  for (int j = 0; j < a.k; ++j) {
-    const int p = place[j];
-    if ((unsigned)p >= (unsigned)a.n_rows) continue;
-    const Chunk<E> v = load_chunk(rows + (int64_t)p * a.rs, n);
-    const float wj = W ? w[j] : 1.f;
+  for (int j0 = 0; j0 < a.k; j0 += HELD) {
+    Chunk<E> v[HELD];
+    bool in[HELD];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = W ? fmaf(wj, to_f32(v.e[i]), acc[i])
-                                           : acc[i] + to_f32(v.e[i]);
+    for (int h = 0; h < HELD; ++h) {
+      const int p = j0 + h < a.k ? place[j0 + h] : -1;
+      in[h] = (unsigned)p < (unsigned)a.n_rows;
+      if (in[h]) v[h] = load_chunk<E, STREAM>(rows + (int64_t)p * a.rs, n);
+    }
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+      if (!in[h]) continue;
+      const float wj = W ? w[j0 + h] : 1.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        acc[i] = W ? fmaf(wj, to_f32(v[h].e[i]), acc[i]) : acc[i] + to_f32(v[h].e[i]);
+    }
   }
   store_chunk((E*)a.out + (int64_t)t * a.os + (int64_t)c * V, n, round_chunk<E>(acc));
 }
@@ -368,37 +441,50 @@ struct CombineGradArgs {
 };
 
 // A wave per assignment: drows[p] = w dy, dw = <dy, rows[p]> (fp32 products, per-lane partial
-// sums joined by shuffles in a fixed order).  The waves of a token read its dy row together.
-template <class E>
+// sums joined by shuffles in a fixed order), four chunks of each row in flight.  The waves of a
+// token read its dy row together.
+template <class E, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) {
   constexpr int V = Chunk<E>::V;
   const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * (TOK_T / 64) + (threadIdx.x >> 6);
+  const int64_t at = (int64_t)blockIdx.x * (TOK_T / 64) +
+                     __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (at >= (int64_t)a.T * a.k) return;
   const int p = a.place[at];
   if ((unsigned)p >= (unsigned)a.n_rows) {
     if (a.dw && lane == 0) a.dw[at] = 0.f;
     return;
   }
-  const float w = a.w ? a.w[at] : 1.f;
+  const float w = a.w[at];
   const E* dy = (const E*)a.dout + at / a.k * a.ds;
   const E* r = (const E*)a.rows + (int64_t)p * a.rs;
   E* dr = (E*)a.drows + (int64_t)p * a.drs;
   const int nc = (a.H + V - 1) / V;
   float sum = 0.f;
-  for (int c = lane; c < nc; c += 64) {
-    const int n = a.H - c * V;
-    const Chunk<E> g = load_chunk(dy + (int64_t)c * V, n);
-    if (a.dw) {
-      const Chunk<E> v = load_chunk(r + (int64_t)c * V, n);
+  for (int c0 = lane; c0 < nc; c0 += 64 * kHeld) {
+    Chunk<E> g[kHeld], v[kHeld];
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum = fmaf(to_f32(g.e[i]), to_f32(v.e[i]), sum);
+    for (int h = 0; h < kHeld; ++h) {
+      const int c = c0 + 64 * h;
+      if (c < nc) {
+        g[h] = load_chunk(dy + (int64_t)c * V, a.H - c * V);
+        if (a.dw) v[h] = load_chunk<E, STREAM>(r + (int64_t)c * V, a.H - c * V);
+      }
     }
-    if (a.drows) {
-      float v[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = w * to_f32(g.e[i]);
-      store_chunk(dr + (int64_t)c * V, n, round_chunk<E>(v));
+    for (int h = 0; h < kHeld; ++h) {
+      const int c = c0 + 64 * h;
+      if (c >= nc) continue;
+      if (a.drows) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = w * to_f32(g[h].e[i]);
+        store_chunk<E, STREAM>(dr + (int64_t)c * V, a.H - c * V, round_chunk<E>(o));
+      }
+      if (a.dw) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum = fmaf(to_f32(g[h].e[i]), to_f32(v[h].e[i]), sum);
+      }
     }
   }
   if (a.dw) {
@@ -417,21 +503,19 @@ struct QuantArgs {
   const int* rows_end;  // may be null
 };
 
-// A wave per row: the maximum, then the codes (the second read of the row hits the cache).
-template <class E>
+// G lanes per row (G = 256: a workgroup); one read of the row where they hold it.
+template <class E, int G, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void quantise_kernel(QuantArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int row = blockIdx.x * (TOK_T / 64) + (threadIdx.x >> 6);
-  if (row >= a.M || (a.rows_end && row >= *a.rows_end)) return;
-  const E* x = (const E*)a.x + (int64_t)row * a.xs;
-  const RowQuant r = row_quant(wave_max_u32(row_max_bits(x, a.K, lane, 64)));
+  __shared__ uint32_t s_max[TOK_T / 64];
   constexpr int V = Chunk<E>::V;
-  const int nc = (a.K + V - 1) / V;
+  const int lane = threadIdx.x % G, row = blockIdx.x * (TOK_T / G) + threadIdx.x / G;
+  const int end = a.rows_end ? min(*a.rows_end, a.M) : a.M;
+  if (row >= end) return;
   int8_t* codes = a.codes + (int64_t)row * a.cs;
-  for (int c = lane; c < nc; c += 64) {
-    const int n = a.K - c * V;
-    store_codes(codes + (int64_t)c * V, n, load_chunk(x + (int64_t)c * V, n), r);
-  }
+  const RowQuant r = quant_row<E, G>((const E*)a.x + (int64_t)row * a.xs, a.K, lane, s_max,
+                                     [&](int c, int n, const Codes<E>& q) {
+                                       store_codes<E, STREAM>(codes + (int64_t)c * V, n, q);
+                                     });
   if (lane == 0) a.scale[row] = r.scale;
 }
 
@@ -458,8 +542,16 @@ void launch_sort(SortArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
   hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
   const int subs = (a.tok_blk + kSubTokens - 1) / kSubTokens;
-  hipLaunchKernelGGL((sort_move_kernel<E, I8>), dim3(a.nblk * subs), dim3(TOK_T),
-                     (size_t)kChunkWaves * a.E * 2, s, a, subs);
+  const dim3 grid(a.nblk * subs);
+  const size_t lds = (size_t)kChunkWaves * a.E * 2;
+  const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
+  const bool wide = I8 && nc > 64 * kHeld;
+  const bool stream = (int64_t)a.N * a.H * (I8 ? 1 : (int)sizeof(E)) > kStreamBytes;
+  const auto kernel = wide ? stream ? sort_move_kernel<E, I8, I8, true>
+                                    : sort_move_kernel<E, I8, I8, false>
+                           : stream ? sort_move_kernel<E, I8, false, true>
+                                    : sort_move_kernel<E, I8, false, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(TOK_T), lds, s, a, subs);
 }
 
 template <class E>
@@ -471,10 +563,46 @@ void launch_combine(CombineArgs& a, hipStream_t s) {
   const int64_t thr = (int64_t)a.T << a.tpt_log;
   const dim3 grid((unsigned)((thr + TOK_T - 1) / TOK_T),
                   (unsigned)((nc + (1 << a.tpt_log) - 1) >> a.tpt_log));
-  if (a.w)
-    hipLaunchKernelGGL((combine_kernel<E, true>), grid, dim3(TOK_T), 0, s, a);
+  const bool uni = a.tpt_log >= 6;
+  const bool stream = (int64_t)a.T * a.k * a.H * (int)sizeof(E) > kStreamBytes;
+  const auto kernel = a.w ? uni ? stream ? combine_kernel<E, true, true, true>
+                                         : combine_kernel<E, true, true, false>
+                                : combine_kernel<E, true, false, false>
+                          : uni ? stream ? combine_kernel<E, false, true, true>
+                                         : combine_kernel<E, false, true, false>
+                                : combine_kernel<E, false, false, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(TOK_T), 0, s, a);
+}
+
+template <class E>
+void launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
+  const bool stream = (int64_t)a.T * a.k * a.H * (int)sizeof(E) > kStreamBytes;
+  const auto kernel = stream ? combine_grad_kernel<E, true> : combine_grad_kernel<E, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T * a.k + TOK_T / 64 - 1) / (TOK_T / 64))),
+                     dim3(TOK_T), 0, s, a);
+}
+
+template <class E, int G>
+void launch_quantise_by(const QuantArgs& a, hipStream_t s) {
+  constexpr int rows = TOK_T / G;
+  const bool stream = (int64_t)a.M * a.K * (int)sizeof(E) > kStreamBytes;
+  const auto kernel = stream ? quantise_kernel<E, G, true> : quantise_kernel<E, G, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(((int64_t)a.M + rows - 1) / rows)), dim3(TOK_T), 0,
+                     s, a);
+}
+
+// As few lanes per row as hold it in kHeld chunks each.
+template <class E>
+void launch_quantise(const QuantArgs& a, hipStream_t s) {
+  const int nc = (a.K + Chunk<E>::V - 1) / Chunk<E>::V;
+  if (nc <= 16 * kHeld)
+    launch_quantise_by<E, 16>(a, s);
+  else if (nc <= 32 * kHeld)
+    launch_quantise_by<E, 32>(a, s);
+  else if (nc <= 64 * kHeld)
+    launch_quantise_by<E, 64>(a, s);
   else
-    hipLaunchKernelGGL((combine_kernel<E, false>), grid, dim3(TOK_T), 0, s, a);
+    launch_quantise_by<E, 256>(a, s);
 }
 
 moe_status combine(const void* rows, int64_t rs, int n_rows, int type, const int* place,
@@ -573,13 +701,12 @@ moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const 
   CombineGradArgs a{dout, dout_stride, rows, rows_stride, n_rows, place, weights, T,
                     top_k, hidden, drows, drows_stride, dweights};
   const hipStream_t s = (hipStream_t)stream;
-  const dim3 grid((unsigned)((T * top_k + TOK_T / 64 - 1) / (TOK_T / 64)));
   if (type == MOE_T_BF16)
-    hipLaunchKernelGGL(combine_grad_kernel<bf16_t>, grid, dim3(TOK_T), 0, s, a);
+    launch_combine_grad<bf16_t>(a, s);
   else if (type == MOE_T_FP16)
-    hipLaunchKernelGGL(combine_grad_kernel<fp16_t>, grid, dim3(TOK_T), 0, s, a);
+    launch_combine_grad<fp16_t>(a, s);
   else
-    hipLaunchKernelGGL(combine_grad_kernel<float>, grid, dim3(TOK_T), 0, s, a);
+    launch_combine_grad<float>(a, s);
   return launched();
 }
 
@@ -593,13 +720,12 @@ moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int3
   if (M == 0) return MOE_OK;
   QuantArgs a{x, x_stride, M, K, codes, codes_stride, scale, rows_end};
   const hipStream_t s = (hipStream_t)stream;
-  const dim3 grid((unsigned)(((int64_t)M + TOK_T / 64 - 1) / (TOK_T / 64)));
   if (type == MOE_T_BF16)
-    hipLaunchKernelGGL(quantise_kernel<bf16_t>, grid, dim3(TOK_T), 0, s, a);
+    launch_quantise<bf16_t>(a, s);
   else if (type == MOE_T_FP16)
-    hipLaunchKernelGGL(quantise_kernel<fp16_t>, grid, dim3(TOK_T), 0, s, a);
+    launch_quantise<fp16_t>(a, s);
   else
-    hipLaunchKernelGGL(quantise_kernel<float>, grid, dim3(TOK_T), 0, s, a);
+    launch_quantise<float>(a, s);
   return launched();
 }
 
