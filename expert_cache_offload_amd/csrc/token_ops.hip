@@ -9,19 +9,23 @@
 //
 // All of it is movement: every kernel is bound by the bytes of the rows it reads and writes.
 // Every count is an integer from ballots, so nothing depends on the order of execution.
+#include <algorithm>
+
 #include "row_ops.h"
 
 namespace moe {
 namespace {
 
 constexpr int TOK_T = 256;          // threads of every kernel here but the scan
-constexpr int kSmallIds = 4096;     // assignments that one kernel sorts (each workgroup counts
-                                    // all of them for the ids of its own token)
+constexpr int kSmallIds = 2048;     // assignments that one kernel sorts (each workgroup counts
+                                    // all of them for the ids of its own token): 2048 take
+                                    // 11.1 us so and 11.7 with a launch more, 4096 18.8 and 12.5
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
 constexpr int kChunkIds = 1024;     // assignments of a counted chunk (whole tokens)
 constexpr int kChunkWaves = kChunkIds / 64;
-constexpr int kSubTokens = 16;      // tokens a workgroup of the move kernel sorts and moves
+constexpr int kSubTokens = 16;      // most tokens a workgroup of the move kernel sorts and moves
+constexpr int kSelfChunks = 16;     // most chunks whose counts the move kernel adds up itself
 constexpr int kMaxT = 1 << 20;
 // A rows matrix above this is streamed past the caches (non-temporal loads and stores): it would
 // not be there any more for whoever reads it next, and the chip moves it faster so (16384 tokens
@@ -140,8 +144,9 @@ __device__ __forceinline__ void quant_row_to(const E* x, int H, const int* place
   if (lane < k && place[lane] >= 0) row_scale[place[lane]] = r.scale;
 }
 
-// offsets[0..E] from per-expert totals in LDS, one workgroup of nthr threads.
-__device__ void write_offsets(const int* total, int E, int* offsets, int* s_wave, int tid,
+// first[0..E] = exclusive prefix of total[0..E-1] (LDS), one workgroup of nthr threads; first may be
+// global.  Ends with the workgroup's writes done but not yet synchronised.
+__device__ void prefix_counts(const int* total, int E, int* first_of, int* s_wave, int tid,
                               int nthr) {
   const int per = (E + nthr - 1) / nthr;
   int sum = 0;
@@ -162,9 +167,9 @@ __device__ void write_offsets(const int* total, int E, int* offsets, int* s_wave
   for (int i = 0; i < per; ++i) {
     const int e = tid * per + i;
     if (e < E) {
-      offsets[e] = first;
+      first_of[e] = first;
       first += total[e];
-      if (e == E - 1) offsets[E] = first;
+      if (e == E - 1) first_of[E] = first;
     }
   }
 }
@@ -191,7 +196,7 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
       if ((unsigned)id < (unsigned)a.E) atomicAdd(&s_hist[id], 1);
     }
     __syncthreads();
-    write_offsets(s_hist, a.E, a.offsets, s_wave, tid, TOK_T);
+    prefix_counts(s_hist, a.E, a.offsets, s_wave, tid, TOK_T);
     return;
   }
   const E* x = (const E*)a.x + (int64_t)t * a.xs;
@@ -201,13 +206,24 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
     own[j] = j < a.k ? key_of_id(a.ids[t * a.k + j], a.E) : 0;
     cnt[j] = 0;
   }
-  for (int i0 = wave * 64; i0 < a.N; i0 += TOK_T) {
-    const int i = i0 + lane;
-    const int key = i < a.N ? key_of_id(a.ids[i], a.E) : 0x7fffffff;
+  constexpr int AHEAD = 8;  // ids of a lane in flight
+  for (int i0 = wave * 64; i0 < a.N; i0 += AHEAD * TOK_T) {
+    int id[AHEAD];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j)
-      if (j < a.k)
-        cnt[j] += __popcll(__ballot(key < own[j] || (key == own[j] && i < t * a.k + j)));
+    for (int h = 0; h < AHEAD; ++h) {
+      const int i = i0 + h * TOK_T + lane;
+      id[h] = i < a.N ? a.ids[i] : -1;
+    }
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h) {
+      const int i = i0 + h * TOK_T + lane;
+      if (i - lane >= a.N) break;
+      const int key = key_of_id(id[h], a.E);
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j)
+        if (j < a.k)
+          cnt[j] += __popcll(__ballot(key < own[j] || (key == own[j] && i < t * a.k + j)));
+    }
   }
 #pragma unroll
   for (int j = 0; j < kMaxTopK; ++j)
@@ -238,7 +254,7 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
   }
 }
 
-// Many assignments, first of three launches: the ids of each chunk counted by expert.
+// Many assignments, first of two or three launches: the ids of each chunk counted by expert.
 __global__ __launch_bounds__(TOK_T) void sort_count_kernel(SortArgs a) {
   __shared__ int s_hist[kMaxExperts];
   const int b = blockIdx.x;
@@ -253,7 +269,8 @@ __global__ __launch_bounds__(TOK_T) void sort_count_kernel(SortArgs a) {
   for (int e = threadIdx.x; e < a.E; e += TOK_T) a.base[(int64_t)b * a.E + e] = s_hist[e];
 }
 
-// Second: one workgroup turns the counts into first places.  Thread (g, e) adds up a segment g of
+// Second, where there are more than kSelfChunks chunks: one workgroup turns the counts into first
+// places.  Thread (g, e) adds up a segment g of
 // the chunks of expert e, the segments and then the experts are scanned, and a second pass over
 // the counts writes the running place.
 __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
@@ -288,7 +305,7 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
     s_total[e] = run;
   }
   __syncthreads();
-  write_offsets(s_total, a.E, s_off, s_wave, threadIdx.x, SCAN_T);
+  prefix_counts(s_total, a.E, s_off, s_wave, threadIdx.x, SCAN_T);
   __syncthreads();
   for (int i = threadIdx.x; i <= a.E; i += SCAN_T) a.offsets[i] = s_off[i];
   if (e < a.E) {
@@ -307,21 +324,52 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
   }
 }
 
-// Third: a workgroup takes kSubTokens tokens of a chunk, ranks the chunk's ids up to its own last
-// one (a wave finds the lanes that hold its id by ballots over the id's bits; counts per wave and
-// expert in LDS), writes their places and moves their rows, a wave per token.
-template <class E, bool I8, bool WIDE, bool STREAM>
-__global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int subs) {
+// Last: a workgroup takes `sub` tokens of a chunk, ranks the chunk's ids up to its own last one (a
+// wave finds the lanes that hold its id by ballots over the id's bits; counts per wave and expert
+// in LDS), writes their places and moves their rows, a wave per token or (WIDE) all waves on one
+// token after the other.  SELF: the counts are few enough that each workgroup adds them up itself
+// instead of a launch between.
+template <class E, bool I8, bool WIDE, bool STREAM, bool SELF>
+__global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, int subs) {
   extern __shared__ __align__(16) uint16_t s_cnt[];  // [kChunkWaves][E]
   __shared__ int s_id[kSubTokens * kMaxTopK], s_rank[kSubTokens * kMaxTopK];
   __shared__ int s_place[kSubTokens * kMaxTopK];
   __shared__ uint32_t s_max[2][TOK_T / 64];
+  __shared__ int s_base[SELF ? kMaxExperts + 1 : 1], s_total[SELF ? kMaxExperts : 1];
+  __shared__ int s_wave[TOK_T / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b = blockIdx.x / subs, sub = blockIdx.x % subs;
+  const int b = blockIdx.x / subs;
   const int t_blk = b * a.tok_blk;
-  const int t0 = t_blk + sub * kSubTokens;
-  const int t1 = min(min(a.T, t_blk + a.tok_blk), t0 + kSubTokens);
+  const int t0 = t_blk + (blockIdx.x % subs) * sub;
+  const int t1 = min(min(a.T, t_blk + a.tok_blk), t0 + sub);
   if (t0 >= t1) return;
+  if constexpr (SELF) {
+    int before[kMaxExperts / TOK_T];  // in the chunks before this one
+#pragma unroll
+    for (int q = 0; q < kMaxExperts / TOK_T; ++q) {
+      const int e = tid + q * TOK_T;
+      before[q] = 0;
+      if (e >= a.E) continue;
+      int cnt[kSelfChunks], sum = 0;
+#pragma unroll
+      for (int c = 0; c < kSelfChunks; ++c) cnt[c] = c < a.nblk ? a.base[c * a.E + e] : 0;
+#pragma unroll
+      for (int c = 0; c < kSelfChunks; ++c) {
+        before[q] += c < b ? cnt[c] : 0;
+        sum += cnt[c];
+      }
+      s_total[e] = sum;
+    }
+    __syncthreads();
+    prefix_counts(s_total, a.E, s_base, s_wave, tid, TOK_T);
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int e = tid; e <= a.E; e += TOK_T) a.offsets[e] = s_base[e];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kMaxExperts / TOK_T; ++q)
+      if (tid + q * TOK_T < a.E) s_base[tid + q * TOK_T] += before[q];
+  }
   const int first = t_blk * a.k, own0 = (t0 - t_blk) * a.k, own1 = (t1 - t_blk) * a.k;
   const int waves = (own1 + 63) / 64;
   for (int i = tid; i < waves * a.E; i += TOK_T) s_cnt[i] = 0;
@@ -347,7 +395,7 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int subs) 
     const int i = own0 + tid, id = s_id[tid];
     int p = -1;
     if (id >= 0) {
-      p = a.base[(int64_t)b * a.E + id] + s_rank[tid];
+      p = s_rank[tid] + (SELF ? s_base[id] : a.base[(int64_t)b * a.E + id]);
       for (int it = 0; it < i / 64; ++it) p += s_cnt[it * a.E + id];
       if (a.order) a.order[p] = first + i;
     }
@@ -356,22 +404,16 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int subs) 
   }
   __syncthreads();
   if (!a.x) return;
-  if constexpr (I8 && WIDE) {  // rows that only the whole workgroup holds
-    for (int t = t0; t < t1; ++t)
-      quant_row_to<E, TOK_T, STREAM>((const E*)a.x + (int64_t)t * a.xs, a.H,
-                                     s_place + (t - t0) * a.k, a.k, (int8_t*)a.rows, a.rs,
-                                     a.row_scale, tid, s_max[t & 1]);
-  } else {
-    for (int t = t0 + wave; t < t1; t += TOK_T / 64) {
-      const E* x = (const E*)a.x + (int64_t)t * a.xs;
-      const int* place = s_place + (t - t0) * a.k;
-      if constexpr (I8)
-        quant_row_to<E, 64, STREAM>(x, a.H, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, lane,
-                                    nullptr);
-      else
-        copy_row<E, STREAM>(x, a.H, place, a.k, (E*)a.rows, a.rs, 0,
-                            (a.H + Chunk<E>::V - 1) / Chunk<E>::V, lane, 64);
-    }
+  const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
+  constexpr int G = WIDE ? TOK_T : 64;
+  for (int t = t0 + (WIDE ? 0 : wave); t < t1; t += WIDE ? 1 : TOK_T / 64) {
+    const E* x = (const E*)a.x + (int64_t)t * a.xs;
+    const int* place = s_place + (t - t0) * a.k;
+    if constexpr (I8)
+      quant_row_to<E, G, STREAM>(x, a.H, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale,
+                                 WIDE ? tid : lane, s_max[t & 1]);
+    else
+      copy_row<E, STREAM>(x, a.H, place, a.k, (E*)a.rows, a.rs, 0, nc, WIDE ? tid : lane, G);
   }
 }
 
@@ -540,18 +582,25 @@ void launch_sort(SortArgs& a, hipStream_t s) {
     return;
   }
   hipLaunchKernelGGL(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
-  hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
-  const int subs = (a.tok_blk + kSubTokens - 1) / kSubTokens;
-  const dim3 grid(a.nblk * subs);
-  const size_t lds = (size_t)kChunkWaves * a.E * 2;
+  const bool self = a.nblk <= kSelfChunks;
+  if (!self) hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
   const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
-  const bool wide = I8 && nc > 64 * kHeld;
+  // a wave per token, unless there are too few tokens for that to fill the chip, or rows of codes
+  // that a wave cannot hold; 16 tokens per workgroup amortise its counting, fewer fill the chip
+  // (8 rows of 2048 bf16 per token: 4096 tokens 36 us with 4, 41 with 4 and whole workgroups per
+  // token; 1024 tokens of 8 rows of 4096, quantised: 18 us with one per workgroup, 64 with 16)
+  const bool wide = a.T < 2048 || (I8 && nc > 64 * kHeld);
+  const int sub = a.T < 2048 ? 1 : a.T < 8192 ? 4 : kSubTokens;
   const bool stream = (int64_t)a.N * a.H * (I8 ? 1 : (int)sizeof(E)) > kStreamBytes;
-  const auto kernel = wide ? stream ? sort_move_kernel<E, I8, I8, true>
-                                    : sort_move_kernel<E, I8, I8, false>
-                           : stream ? sort_move_kernel<E, I8, false, true>
-                                    : sort_move_kernel<E, I8, false, false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(TOK_T), lds, s, a, subs);
+  const auto kernel = self ? wide ? sort_move_kernel<E, I8, true, false, true>
+                                  : sort_move_kernel<E, I8, false, false, true>
+                      : wide ? stream ? sort_move_kernel<E, I8, true, true, false>
+                                      : sort_move_kernel<E, I8, true, false, false>
+                             : stream ? sort_move_kernel<E, I8, false, true, false>
+                                      : sort_move_kernel<E, I8, false, false, false>;
+  const int subs = (a.tok_blk + sub - 1) / sub;
+  hipLaunchKernelGGL(kernel, dim3(a.nblk * subs), dim3(TOK_T), (size_t)kChunkWaves * a.E * 2, s, a,
+                     sub, subs);
 }
 
 template <class E>
