@@ -135,22 +135,6 @@ __device__ __forceinline__ void channel_values(float (&v)[16], const float (&sw)
   }
 }
 
-// Stores a lane's 16 channels n .. n + 15 (n a multiple of 16) of output row m.
-template <class E, bool SWIGLU>
-__device__ __forceinline__ void store_channels(const ProdArgs& a, int64_t m, int n,
-                                               const float (&sw)[16], float sa,
-                                               const i32x16& acc) {
-  constexpr int V = Chunk<E>::V, NO = SWIGLU ? 8 : 16;
-  const int have = SWIGLU ? (a.N - n) / 2 : a.N - n;
-  if (have <= 0) return;
-  float v[16];
-  channel_values<E, SWIGLU>(v, sw, sa, acc);
-  E* out = (E*)a.out + m * a.os + (SWIGLU ? n / 2 : n);
-#pragma unroll
-  for (int c = 0; c < NO; c += V)
-    if (have > c) store_chunk(out + c, have - c, round_chunk<E>(v + c));
-}
-
 // 32 output rows of RB bytes each that a wave has put into its LDS (row r's 16-byte chunk c at
 // chunk c ^ swz(r)) go to memory with neighbouring lanes on neighbouring chunks: a request per 64
 // bytes instead of one per 16, which is what the stores of a tile cost otherwise (a launch
@@ -176,131 +160,6 @@ __device__ __forceinline__ void store_rows(const int8_t* stage, int lane, E* out
   for (int t = 0; t < CPR / 2; ++t) {
     const int row = t * (64 / CPR) + lane / CPR, c = (lane % CPR) ^ out_swz<RB>(row);
     if (row < rows && c * V < cols) store_chunk(out + row * os + c * V, cols - c * V, v[t]);
-  }
-}
-
-// The scales of channels n .. n + 15 of a group, those past N repeated.
-__device__ __forceinline__ void load_scales(float (&sw)[16], const float* w_scale, int n, int N) {
-  if (n + 16 <= N) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 q = *(const u32x4_any*)(w_scale + n + 4 * i);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) sw[4 * i + b] = __uint_as_float(q[b]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) sw[i] = w_scale[min(n + i, N - 1)];
-  }
-}
-
-// ------------------------------------------------------------------ general tile
-// 128 rows x 128 channels, four waves of 64 x 64, stages of 64 contraction elements through
-// registers into LDS: any stride, alignment and length.  Rows past a group's end load its last
-// row, channels past N the last channel; bytes past K are zero.
-constexpr int GT = 256, GM = 128, GN = 128, GK = 64;
-
-__device__ __forceinline__ int g_swz(int row, int chunk) {  // byte of (row, 16-byte chunk)
-  return row * GK + ((chunk ^ ((row >> 2) & 3)) << 4);
-}
-
-template <class E, bool SWIGLU>
-__global__ __launch_bounds__(GT) void product_any_kernel(ProdArgs a) {
-  __shared__ __align__(16) int8_t s_t[2][(GM + GN) * GK];  // channels, then rows
-  __shared__ int s_mt[kMaxGroups + 1];
-  __shared__ int2 s_rows[kMaxGroups];
-  __shared__ int s_wave[GT / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  tile_prefix<GM>(a, s_mt, s_rows, s_wave, tid, GT);
-  const int NT = (a.N + GN - 1) / GN;
-  const int mt = blockIdx.x / NT, nt = blockIdx.x - mt * NT;
-  if (mt >= s_mt[a.groups]) return;
-  const int g = find_group(s_mt, a.groups, mt, lane);
-  const int2 rr = s_rows[g];
-  const int m0 = rr.x + (mt - s_mt[g]) * GM, n0 = nt * GN;
-  const int8_t* w = a.w + (int64_t)g * a.N * a.ws;
-  // thread: chunk tid % 4 of rows tid / 4 + 64 i of the stage
-  const int8_t* src[4];
-  const int ck = (tid & 3) * 16;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (tid >> 2) + 64 * i;
-    if (r < GN)
-      src[i] = w + (int64_t)min(n0 + r, a.N - 1) * a.ws + ck;
-    else
-      src[i] = a.a + (int64_t)min(m0 + r - GN, rr.y - 1) * a.as + ck;
-  }
-  Chunk<int8_t> st[4];
-  auto load = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = a.K - k0 - ck;
-      if (n >= 16) {
-        st[i].q = *(const u32x4_any*)(src[i] + k0);
-      } else {
-        st[i].q = u32x4{0, 0, 0, 0};
-        for (int b = 0; b < n; ++b) {  // the end of the row
-          const uint32_t v = (uint32_t)(uint8_t)src[i][k0 + b] << (8 * (b & 3));
-          const int d = b >> 2;
-          st[i].q.x |= d == 0 ? v : 0;
-          st[i].q.y |= d == 1 ? v : 0;
-          st[i].q.z |= d == 2 ? v : 0;
-          st[i].q.w |= d == 3 ? v : 0;
-        }
-      }
-    }
-  };
-  auto put = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *(u32x4*)(s_t[buf] + g_swz((tid >> 2) + 64 * i, tid & 3)) = st[i].q;
-  };
-  const int wn = (wave & 1) * 64, wm = (wave >> 1) * 64;
-  i32x16 acc[2][2];  // [channel tile][row tile]
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-  const int stages = (a.K + GK - 1) / GK;
-  load(0);
-  put(0);
-  __syncthreads();
-  const int wrow = channel_of_row(lane & 31), arow = lane & 31, half = lane >> 5;
-  for (int s = 0; s < stages; ++s) {
-    if (s + 1 < stages) load((s + 1) * GK);
-    const int8_t* t = s_t[s & 1];
-#pragma unroll
-    for (int kk = 0; kk < GK / 32; ++kk) {
-      i32x4 fw[2], fa[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fw[i] = *(const i32x4*)(t + g_swz(wn + 32 * i + wrow, 2 * kk + half));
-        fa[i] = *(const i32x4*)(t + g_swz(GN + wm + 32 * i + arow, 2 * kk + half));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
-    }
-    if (s + 1 < stages) {
-      put((s + 1) & 1);  // last read in stage s - 1, before the barrier that ended it
-      __syncthreads();
-    }
-  }
-  const float* w_scale = a.w_scale + (int64_t)g * a.N;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = n0 + wn + 32 * i + 16 * half;
-    float sw[16];
-    load_scales(sw, w_scale, n, a.N);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int m = m0 + wm + 32 * j + arow;
-      if (m < rr.y) store_channels<E, SWIGLU>(a, m, n, sw, a.a_scale[m], acc[i][j]);
-    }
   }
 }
 
@@ -464,7 +323,7 @@ __device__ __forceinline__ void tile_of(int tile, int MT, int NT, int& mt, int& 
   mt = block * 4 + in - nt * rows;
 }
 
-template <class E, bool SWIGLU, int WM, int WN, int MI, int NI, int KS, int PER_CU>
+template <class E, bool SWIGLU, bool ANY, int WM, int WN, int MI, int NI, int KS, int PER_CU>
 __global__ __launch_bounds__(64 * WM * WN * KS, WM * WN * KS * PER_CU / 4)
 void product_tile_kernel(ProdArgs a) {
   constexpr int TW = WM * WN, LT = 64 * TW * KS;  // waves of a tile; threads
@@ -494,14 +353,16 @@ void product_tile_kernel(ProdArgs a) {
   if (tile >= ntiles) return;
   int m0, n0, end;  // the tile's first row and channel, its group's last row + 1
   const int8_t *wbase, *abase;
-  uint32_t off[LPW];
   // load i of this wave: stage rows 8 (wave * LPW + i) .. + 7, lane l brings row + l / 8, chunk
-  // l % 8 in LDS; rows past the group or past N load the last valid one
+  // l % 8 in LDS; rows past the group or past N load the last valid one, bytes past K are zero
   auto chunk_of = [&](int i) {
     const int row = (wave * LPW + i) * 8 + (lane >> 3);
     const int r = row < BN ? row_of_channel(row & 31) : row & 31;
     return (lane & 7) ^ ((r >> 1) & 7);
   };
+  uint32_t off[LPW];        // aligned: the rows' byte offsets,
+  const int8_t* src[LPW];   // else their addresses, and the stage under way to LDS
+  i32x4 held[LPW];
   auto load_stage = [&](int round, int buf) {
     const int st = round * KS + ks;
     const uint32_t dst = lds0 + buf * STAGE + wave * LPW * 1024;
@@ -513,15 +374,31 @@ void product_tile_kernel(ProdArgs a) {
         load_to_lds(dst + i * 1024, off[i], (wave * LPW + i) * 8 < BN ? wk : ak);
     } else if (st < nst) {
       const int left = (a.K - st * LK) / 16;  // chunks of the row in this stage
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < LPW; ++i) {
-        const int row = (wave * LPW + i) * 8 + (lane >> 3), c = chunk_of(i);
-        const int8_t* src = row < BN ? wk + (int64_t)min(row, a.N - 1 - n0) * a.ws
-                                     : ak + (int64_t)min(row - BN, end - 1 - m0) * a.as;
-        i32x4 v = i32x4{0, 0, 0, 0};  // past K
-        if (c < left) v = *(const i32x4*)(src + 16 * c);
-        *(i32x4*)(stages + buf * STAGE + (wave * LPW + i) * 1024 + lane * 16) = v;
+        if (chunk_of(i) < left)
+          load_to_lds(dst + i * 1024, off[i], (wave * LPW + i) * 8 < BN ? wk : ak);
+        else
+          *(i32x4*)(stages + buf * STAGE + (wave * LPW + i) * 1024 + lane * 16) =
+              i32x4{0, 0, 0, 0};
       }
+    }
+  };
+  auto fetch = [&](int round) {
+    const int k0 = (round * KS + ks) * LK;
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) held[i] = load_k(src[i] + k0, a.K - k0 - 16 * chunk_of(i));
+  };
+  // Stage `round` on its way to half buf: by loads to LDS, or from registers while the next one is
+  // fetched into them.
+  auto advance = [&](int round, int buf) {
+    if constexpr (ANY) {
+#pragma unroll
+      for (int i = 0; i < LPW; ++i)
+        *(i32x4*)(stages + buf * STAGE + (wave * LPW + i) * 1024 + lane * 16) = held[i];
+      if (round + 1 < rounds) fetch(round + 1);
+    } else {
+      load_stage(round, buf);
     }
   };
   // Takes up a tile: its first stage and its scales (into half sb of their arrays).
@@ -547,11 +424,15 @@ void product_tile_kernel(ProdArgs a) {
 #pragma unroll
     for (int i = 0; i < LPW; ++i) {
       const int row = (wave * LPW + i) * 8 + (lane >> 3);
-      off[i] = (row < BN ? (uint32_t)min(row, a.N - 1 - n0) * (uint32_t)a.ws
-                         : (uint32_t)min(row - BN, end - 1 - m0) * (uint32_t)a.as) +
-               16 * chunk_of(i);
+      const int64_t at = row < BN ? (int64_t)min(row, a.N - 1 - n0) * a.ws
+                                  : (int64_t)min(row - BN, end - 1 - m0) * a.as;
+      if constexpr (ANY)
+        src[i] = (row < BN ? wbase : abase) + at + 16 * chunk_of(i);
+      else
+        off[i] = (uint32_t)at + 16 * chunk_of(i);
     }
-    load_stage(0, 0);
+    if constexpr (ANY) fetch(0);
+    advance(0, 0);
   };
   begin(tile, 0);
   const int8_t* rw = stages + (wn + channel_of_row(r32)) * LK;
@@ -576,7 +457,7 @@ void product_tile_kernel(ProdArgs a) {
     const bool active = m1 < end && n1 < a.N;
     const int mine = active ? (nst - ks + KS - 1) / KS : 0;  // rounds this wave multiplies in
     stage_barrier();
-    if (rounds > 1) load_stage(1, 1);
+    if (rounds > 1) advance(1, 1);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -595,13 +476,13 @@ void product_tile_kernel(ProdArgs a) {
       read(fw1, fa1, buf, 3);
       multiply(fw0, fa0);
       stage_barrier();
-      if (rd + 2 < rounds) load_stage(rd + 2, buf);
+      if (rd + 2 < rounds) advance(rd + 2, buf);
       if (rd + 1 < mine) read(fw0, fa0, buf ^ 1, 0);
       multiply(fw1, fa1);
     }
     for (; rd < rounds; ++rd) {
       stage_barrier();
-      if (rd + 2 < rounds) load_stage(rd + 2, rd & 1);
+      if (rd + 2 < rounds) advance(rd + 2, rd & 1);
     }
     if constexpr (KS > 1) {  // the parts of K added up by the first (integers: exact)
       static_assert(NI == 1 && MI == 1 && (KS - 1) * TW * 4096 <= 2 * KS * STAGE);
@@ -685,11 +566,11 @@ void product_tile_kernel(ProdArgs a) {
   }
 }
 
-template <class E, bool SWIGLU, int WM, int WN, int MI, int NI, int KS, int PER_CU>
+template <class E, bool SWIGLU, bool ANY, int WM, int WN, int MI, int NI, int KS, int PER_CU>
 void launch_tile(const ProdArgs& a, hipStream_t s) {
   constexpr int BM = 32 * WM * MI, BN = 32 * WN * NI, LT = 64 * WM * WN * KS;
   const int lds = 2 * KS * (BM + BN) * LK + 12 * a.groups + 4;
-  const auto kernel = product_tile_kernel<E, SWIGLU, WM, WN, MI, NI, KS, PER_CU>;
+  const auto kernel = product_tile_kernel<E, SWIGLU, ANY, WM, WN, MI, NI, KS, PER_CU>;
   if (lds > 64 * 1024)
     (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                               lds);
@@ -749,25 +630,23 @@ void launch_product(const ProdArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((product_few_kernel<E, SWIGLU, 4>), dim3(nf), dim3(FT), 0, s, a);
     return;
   }
-  if (aligned) {
-    int best = 0;
-    for (int i = 1; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i)
-      if (!(kShapes[i].bn == 320 && a.groups > 512) &&  // LDS
-          tile_cost(kShapes[i], a) < tile_cost(kShapes[best], a))
-        best = i;
-    switch (best) {
-      case 0: return launch_tile<E, SWIGLU, 4, 2, 2, 4, 1, 1>(a, s);
-      case 1: return launch_tile<E, SWIGLU, 4, 2, 2, 5, 1, 1>(a, s);
-      case 2: return launch_tile<E, SWIGLU, 4, 2, 1, 2, 1, 2>(a, s);
-      case 3: return launch_tile<E, SWIGLU, 2, 2, 1, 1, 1, 4>(a, s);
-      case 4: return launch_tile<E, SWIGLU, 2, 2, 1, 1, 2, 2>(a, s);
-      default: return launch_tile<E, SWIGLU, 2, 2, 1, 1, 4, 1>(a, s);
-    }
+  int best = aligned ? 0 : 2;  // the two largest shapes have no registers for the other path
+  for (int i = best + 1; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i)
+    if (!(kShapes[i].bn == 320 && a.groups > 512) &&  // LDS
+        tile_cost(kShapes[i], a) < tile_cost(kShapes[best], a))
+      best = i;
+  switch (best) {
+    case 0: return launch_tile<E, SWIGLU, false, 4, 2, 2, 4, 1, 1>(a, s);
+    case 1: return launch_tile<E, SWIGLU, false, 4, 2, 2, 5, 1, 1>(a, s);
+    case 2: return aligned ? launch_tile<E, SWIGLU, false, 4, 2, 1, 2, 1, 2>(a, s)
+                           : launch_tile<E, SWIGLU, true, 4, 2, 1, 2, 1, 2>(a, s);
+    case 3: return aligned ? launch_tile<E, SWIGLU, false, 2, 2, 1, 1, 1, 4>(a, s)
+                           : launch_tile<E, SWIGLU, true, 2, 2, 1, 1, 1, 4>(a, s);
+    case 4: return aligned ? launch_tile<E, SWIGLU, false, 2, 2, 1, 1, 2, 2>(a, s)
+                           : launch_tile<E, SWIGLU, true, 2, 2, 1, 1, 2, 2>(a, s);
+    default: return aligned ? launch_tile<E, SWIGLU, false, 2, 2, 1, 1, 4, 1>(a, s)
+                            : launch_tile<E, SWIGLU, true, 2, 2, 1, 1, 4, 1>(a, s);
   }
-  const int64_t mt = a.M / GM + (a.offsets ? std::min(a.groups, a.M) : 1);
-  const int64_t nt = (a.N + GN - 1) / GN;
-  hipLaunchKernelGGL((product_any_kernel<E, SWIGLU>), dim3((unsigned)(mt * nt)), dim3(GT), 0, s,
-                     a);
 }
 
 }  // namespace
