@@ -24,7 +24,7 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 constexpr int kMaxK = 131071;  // 128 * 128 * K stays below 2^31
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxN = 1 << 20;
-constexpr int kMaxM = 1 << 24;
+constexpr int kMaxM = (1 << 24) - 1;
 
 struct ProdArgs {
   const int8_t* a;
@@ -48,14 +48,15 @@ __device__ __forceinline__ float exp_neg(float z) {
   const float rest = fmaf(-z, kL, -t) - z * kLlo;
   const float e = __builtin_amdgcn_exp2f(t);
   // |t| beyond exp2's range: e is 0 or infinity already, and the term must not make it a NaN
-  return fabsf(t) < 126.f ? fmaf(e, rest * 0.693147181f, e) : e;
+  return fabsf(t) < 128.f ? fmaf(e, rest * 0.693147181f, e) : e;
 }
 // silu(z) for an output of type E.  For 16-bit outputs exp2 of the rounded exponent is enough: its
 // error, below 2^-17 where the result is not negligible, is far inside half a step (2^-12).
+// The reciprocal instruction returns 0 for what lies above 2^126, so it is given a sixteenth.
 template <class E>
 __device__ __forceinline__ float silu_for(float z) {
   const float e = sizeof(E) == 2 ? __builtin_amdgcn_exp2f(-1.44269504f * z) : exp_neg(z);
-  return z * __builtin_amdgcn_rcpf(1.0f + e);
+  return z * (__builtin_amdgcn_rcpf(fmaf(e, 0.0625f, 0.0625f)) * 0.0625f);
 }
 
 // Channel (row of a 32-row weight tile) that row r of the matrix instruction holds: a lane's 16
@@ -135,22 +136,33 @@ __device__ __forceinline__ void channel_values(float (&v)[16], const float (&sw)
   }
 }
 
-// 32 output rows of RB bytes each that a wave has put into its LDS (row r's 16-byte chunk c at
-// chunk c ^ swz(r)) go to memory with neighbouring lanes on neighbouring chunks: a request per 64
-// bytes instead of one per 16, which is what the stores of a tile cost otherwise (a launch
-// that writes 403 MB: 165 us with a lane per row, 126 so).
 // A wave's LDS accesses execute in order; this keeps the compiler, which sees one lane's only, from
 // reordering or merging them where lanes read what others wrote.
 __device__ __forceinline__ void wave_lds_order() { asm volatile("" ::: "memory"); }
 
+// 32 output rows of RB bytes each that a wave has put into its LDS (row r's 16-byte chunk c at
+// chunk c ^ out_swz(r)) go to memory with neighbouring lanes on neighbouring chunks: a request per
+// 64 bytes instead of one per 16, which is what the stores of a tile cost otherwise (a launch
+// that writes 403 MB: 165 us with a lane per row, 126 so).
 template <int RB>
 __device__ __forceinline__ int out_swz(int row) {
   return RB == 64 ? (row >> 2) & 3 : (row >> 3) & 1;
 }
+// The first n elements of a chunk (n >= its size: all).
+template <class E>
+__device__ __forceinline__ void store_part(E* p, int n, const Chunk<E>& c) {
+  if (n >= kChunk<E>) {
+    store_chunk(p, c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kChunk<E>; ++i)
+      if (i < n) p[i] = c.e[i];
+  }
+}
 template <class E, int RB>
 __device__ __forceinline__ void store_rows(const int8_t* stage, int lane, E* out, int64_t os,
                                            int rows, int cols) {
-  constexpr int CPR = RB / 16, V = Chunk<E>::V;
+  constexpr int CPR = RB / 16, V = kChunk<E>;
   Chunk<E> v[CPR / 2];
   wave_lds_order();
 #pragma unroll
@@ -159,15 +171,17 @@ __device__ __forceinline__ void store_rows(const int8_t* stage, int lane, E* out
 #pragma unroll
   for (int t = 0; t < CPR / 2; ++t) {
     const int row = t * (64 / CPR) + lane / CPR, c = (lane % CPR) ^ out_swz<RB>(row);
-    if (row < rows && c * V < cols) store_chunk(out + row * os + c * V, cols - c * V, v[t]);
+    if (row < rows && c * V < cols) store_part(out + row * os + c * V, cols - c * V, v[t]);
   }
 }
 
 // ------------------------------------------------------------------ few rows
 // Up to RT * 16 rows of one group times 16 channels per workgroup, the contraction split over its
 // four waves and joined in LDS (integers: in any order the same).  Operands go straight from
-// memory into the registers of a 16 x 16 x 64 matrix instruction; every weight byte is read once
-// for the group's rows, and that stream is the bound.
+// memory into the registers of a 16 x 16 x 64 matrix instruction, eight steps of 64 bytes in
+// flight; every weight byte is read once for the group's rows, and that stream is the bound: gate
+// and up of one token's eight experts (25.2 MB of 2048-wide rows) take 6.6 us, 3.8 TB/s, of
+// which launch, the search of the group and the first load's way are about half.
 constexpr int FT = 256, FN = 16, FU = 8;  // threads, channels, steps in flight
 
 __device__ __forceinline__ i32x4 load_k(const int8_t* p, int n) {  // n bytes of the row are left
@@ -266,19 +280,28 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ large tiles
+// ------------------------------------------------------------------ tiles
 // 32 WM MI rows x 32 WN NI channels per tile, WM x WN waves of 32 MI rows x 32 NI channels,
-// workgroups persistent over the tiles.  Stages of 128 contraction bytes go from memory straight
-// into LDS (16-byte global-to-LDS loads), double buffered: the loads of stage s + 2 are issued
-// when every wave has read stage s, and a tile's first two stages while the previous tile's
-// epilogue runs.  Rows are 128 bytes unpadded; 16-byte chunk c of a row sits at chunk
+// workgroups persistent over the tiles; with KS > 1 as many sets of waves share the stages of K
+// and add up in LDS, for launches of few tiles.  Stages of 128 contraction bytes go from memory
+// straight into LDS (16-byte global-to-LDS loads), double buffered: the loads of stage s + 2 are
+// issued when every wave has read stage s, and a tile's first stage and scales while the previous
+// tile's epilogue runs.  Rows are 128 bytes unpadded; 16-byte chunk c of a row sits at chunk
 // c ^ ((r / 2) % 8), r the row's place in its matrix instruction: the 16 lanes that LDS serves at
 // once then read 16 distinct 16-byte bank slots.  Fragments of a 32-deep step are read while the
 // previous step's matrix instructions run, also across a stage's end.  A wave whose rows (or
 // channels) lie past the group's end loads and waits with the others but multiplies nothing.
 // The loads are asm so that the compiler does not hold LDS reads back for them; they return
 // nothing to registers, and the waits for them are the stage's own.
-// Needs 16-byte aligned operands and strides and K a multiple of 16.
+// They need 16-byte aligned operands and strides and K a multiple of 16; for others (ANY) a stage
+// goes through registers, fetched one stage before it is put into LDS.
+//
+// What bounds the large shapes is power: 8192 x 8192 x 8192 runs at 2.46 POP/s with normally
+// distributed codes and at 3.48 with zeros; with the former the clock falls to 1.6 GHz of 2.4
+// while the matrix units are 67% busy (a vendor library's plain 8-bit product: 2.08, zeros 3.26).
+// Stages of 64 bytes four deep, 128 x 128 per wave, four waves of 64 x 64 per SIMD and fixed
+// orders of reads and products were within 15% of this or slower.  131072 rows over 128 experts x
+// 1536 channels x 2048, SwiGLU: 437 us, 1.89 POP/s, of which the epilogues are about 45.
 constexpr int LK = 128;
 
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, const int8_t* base) {
@@ -486,8 +509,8 @@ void product_tile_kernel(ProdArgs a) {
     }
     if constexpr (KS > 1) {  // the parts of K added up by the first (integers: exact)
       static_assert(NI == 1 && MI == 1 && (KS - 1) * TW * 4096 <= 2 * KS * STAGE);
-      i32x4* part = (i32x4*)(l_smem + ((ks - 1) * TW + wave) * 4096) + lane;
       if (ks > 0) {
+        i32x4* const part = (i32x4*)(l_smem + ((ks - 1) * TW + wave) * 4096) + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           part[64 * q] = i32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2],
@@ -512,7 +535,7 @@ void product_tile_kernel(ProdArgs a) {
     if (more) begin(tile, sb ^ 1);  // the first half of the stages, the other half of the scales
     if (active && ks == 0) {
       // the second half of the stages is free until the next tile's first barrier: 2 KiB a wave
-      constexpr int V = Chunk<E>::V, OB = 16 * (int)sizeof(E) / (SWIGLU ? 2 : 1);
+      constexpr int V = kChunk<E>, OB = 16 * (int)sizeof(E) / (SWIGLU ? 2 : 1);
       static_assert(TW * 2048 <= STAGE);
       int8_t* const stage = l_smem + STAGE + wave * 2048;
       const float* psw = s_scale[sb] + wn + 16 * half;
@@ -583,9 +606,12 @@ void launch_tile(const ProdArgs& a, hipStream_t s) {
 // The tile shapes, and what the choice among them goes by: microseconds of one round of KS
 // stages with one tile on a CU (low) and what each further tile there adds (more), or with a
 // tile on most CUs, where the chip's power limit lowers the clock (full); microseconds a tile
-// spends outside its stages (rest).  Measured with K = 1024 .. 8192; the sum
-// over the launch's rounds came within 15% of the measured time of launches of 64 to 131072
-// rows, and its order of the shapes was the measured one but for near ties.
+// spends outside its stages (rest).  Measured with K = 768 .. 8192 and 64 to 131072 rows, one
+// weight and up to 128: the shape of the smallest sum over the launch's rounds was the fastest
+// measured one, or within a few percent of it (600 x 2 rows over 8 experts, 2000 x 1024: 12.4 us
+// with 64 x 64, 14.9 with 128 x 128, 19.4 with 256 x 256; 4001 x 5000 x 4096: 145 us with
+// 256 x 256, 134 with 128 x 128, 95 with 256 x 320, one round; 256 x 5000 x 4096: 45, 26, 20 with
+// 64 x 64, 17.4 with two and 22.7 with four sets of waves).
 struct TileShape {
   int bm, bn, ks, per_cu;
   float low, more, full, rest;

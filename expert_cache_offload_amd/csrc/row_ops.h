@@ -40,19 +40,36 @@ __device__ __forceinline__ float from_f32<float>(float f) {
   return f;
 }
 
-// One 16-byte chunk of a row: V elements.
+// A chunk of a row: V elements, 16 bytes (or one element, for rows shorter than that).  Chunk c of
+// a row of H >= V elements starts at element chunk_at(c): the last one ends with the row and, where
+// H is no multiple of V, overlaps the one before; what both write there is the same.
 template <class E>
+constexpr int kChunk = 16 / (int)sizeof(E);
+template <class E, int V = kChunk<E>>
 union Chunk {
-  static constexpr int V = 16 / (int)sizeof(E);
   u32x4 q;
   E e[V];
 };
+template <class E>
+union Chunk<E, 1> {
+  E e[1];
+};
+template <int V>
+__device__ __forceinline__ int chunk_at(int c, int H) {
+  return min(c * V, H - V);
+}
+template <int V>
+__host__ __device__ __forceinline__ int chunk_count(int H) {
+  return (H + V - 1) / V;
+}
 
 // V values rounded to a chunk (two at a time: one instruction converts a pair).
-template <class E>
-__device__ __forceinline__ Chunk<E> round_chunk(const float* v) {
-  Chunk<E> c;
-  if constexpr (sizeof(E) == 2) {
+template <class E, int V = kChunk<E>>
+__device__ __forceinline__ Chunk<E, V> round_chunk(const float* v) {
+  Chunk<E, V> c;
+  if constexpr (V == 1) {
+    c.e[0] = from_f32<E>(v[0]);
+  } else if constexpr (sizeof(E) == 2) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
@@ -71,37 +88,26 @@ __device__ __forceinline__ Chunk<E> round_chunk(const float* v) {
   return c;
 }
 
-// The chunk at p, of which the first n elements belong to the row (n >= V: all); elements past
-// the row are not touched and read as zero.  STREAM: nothing reads these bytes again soon, so they
-// pass the caches by.
-template <class E, bool STREAM = false>
-__device__ __forceinline__ Chunk<E> load_chunk(const E* p, int n) {
-  Chunk<E> c;
-  if (n >= Chunk<E>::V) {
-    if constexpr (STREAM)
-      c.q = __builtin_nontemporal_load((const u32x4_any*)p);
-    else
-      c.q = *(const u32x4_any*)p;
-  } else {
-    c.q = u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < Chunk<E>::V; ++i)
-      if (i < n) c.e[i] = p[i];
-  }
+// STREAM: nothing reads these bytes again soon, so they pass the caches by.
+template <int V, bool STREAM = false, class E>
+__device__ __forceinline__ Chunk<E, V> load_chunk(const E* p) {
+  Chunk<E, V> c;
+  if constexpr (V == 1)
+    c.e[0] = p[0];
+  else if constexpr (STREAM)
+    c.q = __builtin_nontemporal_load((const u32x4_any*)p);
+  else
+    c.q = *(const u32x4_any*)p;
   return c;
 }
-template <class E, bool STREAM = false>
-__device__ __forceinline__ void store_chunk(E* p, int n, const Chunk<E>& c) {
-  if (n >= Chunk<E>::V) {
-    if constexpr (STREAM)
-      __builtin_nontemporal_store(c.q, (u32x4_any*)p);
-    else
-      *(u32x4_any*)p = c.q;
-  } else {
-#pragma unroll
-    for (int i = 0; i < Chunk<E>::V; ++i)
-      if (i < n) p[i] = c.e[i];
-  }
+template <bool STREAM = false, class E, int V>
+__device__ __forceinline__ void store_chunk(E* p, const Chunk<E, V>& c) {
+  if constexpr (V == 1)
+    p[0] = c.e[0];
+  else if constexpr (STREAM)
+    __builtin_nontemporal_store(c.q, (u32x4_any*)p);
+  else
+    *(u32x4_any*)p = c.q;
 }
 
 // 8-bit quantisation of a row with m = max |x|: scale = m / 127 and code = 127 x / m rounded to
@@ -109,8 +115,10 @@ __device__ __forceinline__ void store_chunk(E* p, int n, const Chunk<E>& c) {
 // zeros has scale 0 and codes 0; a row that holds a NaN or an infinity has scale NaN and codes
 // 0, so that whatever is computed from it is NaN.
 struct RowQuant {
-  float m, inv, scale;
-  int mode;  // 0: codes are zero, 1: fp32 arithmetic, 2: 64-bit arithmetic
+  float m, inv;  // largest magnitude and its reciprocal, scaled by a power of two
+  float k;       // 127 times that power: 127 x and 1 / m stay normal numbers of fp32
+  float scale;
+  bool live;     // false: the codes are zero
 };
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
@@ -118,87 +126,81 @@ __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f
 // max_bits: the largest abs_bits() of the row (a NaN's are above infinity's, above a number's).
 __device__ __forceinline__ RowQuant row_quant(uint32_t max_bits) {
   RowQuant r;
-  r.m = __uint_as_float(max_bits);
+  const float m = __uint_as_float(max_bits);
+  // elements so small beside m that the scaling rounds them have code 0 either way
+  const float by = m < 0x1p-60f ? 0x1p100f : m > 0x1p60f ? 0x1p-60f : 1.0f;
+  r.m = m * by;
   r.inv = 1.0f / r.m;
-  r.scale = r.m / 127.0f;
-  // fp32: 127 x must not overflow and 1 / m must be a normal number
-  r.mode = r.m >= 0x1p-100f && r.m <= 0x1p100f ? 1 : 2;
-  if (max_bits == 0) r.mode = 0;
-  if (max_bits >= 0x7f800000u) {
-    r.mode = 0;
-    r.scale = __uint_as_float(0x7fc00000u);
-  }
+  r.k = 127.0f * by;
+  r.live = max_bits != 0 && max_bits < 0x7f800000u;
+  r.scale = max_bits < 0x7f800000u ? m / 127.0f : __uint_as_float(0x7fc00000u);
   return r;
 }
 
-// The bits of 1.5 * 2^23 + 127 x / m, whose low byte is the code (fp32 addition rounds to
-// nearest even at that size).  t = 127 x, y = t / m up to 2 roundings, and y + (t - y m) / m is
-// the quotient to half a step: where the quotient is a tie it is a number of fp32 and comes out
-// exactly.  16-bit inputs: t is exact (18 bits) and a quotient 127 X 2^e / M that is no tie (X and M
-// of 11 bits) is 2^e / 4094 from one at least, its error below 127 * 2^(e - 22): the rounding is
-// right.  fp32 inputs: t may be rounded; quotients within 2^-14 of a tie (their error is below
-// 2^-15) are decided in 64 bits, where 127 x is exact and a quotient that is no tie differs from
-// one by 2^-33 at least.
+// The bits of 1.5 * 2^23 + code, whose low byte is the code (fp32 addition rounds to nearest even
+// at that size).  t = 127 x, y = t / m up to 2 roundings.
+// 16-bit inputs: y + (t - y m) / m is the quotient to half a step; t is exact (18 bits), and where
+// the quotient is a tie it is a number of fp32 and comes out exactly.  A quotient 127 X 2^e / M that
+// is no tie (X and M of 11 bits) is 2^e / 4094 from one at least, its error below
+// 127 * 2^(e - 22): the rounding is right.
+// fp32 inputs: t + u = 127 x exactly, and so is the remainder t - q m of the candidate q = rint(y),
+// a multiple of m's last place below m; its double against m, with u, decides.
 template <class E>
 __device__ __forceinline__ uint32_t quant_bits(float x, const RowQuant& r) {
-  const float t = 127.0f * x;
+  const float t = r.k * x;
   float y = t * r.inv;
-  y = fmaf(fmaf(-y, r.m, t), r.inv, y);
-  if constexpr (sizeof(E) == 4) {
-    if (fabsf(fabsf(y - rintf(y)) - 0.5f) < 0x1p-14f) y = (float)rint(127.0 * (double)x / (double)r.m);
+  if constexpr (sizeof(E) == 2) {
+    y = fmaf(fmaf(-y, r.m, t), r.inv, y);
+  } else {
+    const float u = -2.0f * fmaf(r.k, x, -t);
+    y = rintf(y);
+    const float rest = fmaf(-y, r.m, t);
+    const float up = fmaf(2.0f, rest, -r.m), down = fmaf(2.0f, rest, r.m);
+    const bool odd = (int)y & 1;
+    if (up > u || (up == u && odd)) y += 1.0f;
+    if (down < u || (down == u && odd)) y -= 1.0f;
   }
   return __float_as_uint(y + 12582912.0f);
 }
-// The same for rows whose largest magnitude fp32 arithmetic does not serve.
-__device__ __forceinline__ uint32_t quant_bits_wide(float x, const RowQuant& r) {
-  return r.mode == 0 ? 0u : (uint32_t)(int)rint(127.0 * (double)x / (double)r.m);
-}
 
 // The codes of one chunk, four to a word.
-template <class E>
+template <class E, int V>
 struct Codes {
-  static constexpr int W = Chunk<E>::V / 4;
-  uint32_t w[W];
+  uint32_t w[(V + 3) / 4];
 };
-template <class E>
-__device__ __forceinline__ Codes<E> quant_chunk(const Chunk<E>& c, const RowQuant& r) {
-  Codes<E> o;
+template <class E, int V>
+__device__ __forceinline__ Codes<E, V> quant_chunk(const Chunk<E, V>& c, const RowQuant& r) {
+  Codes<E, V> o;
+  if constexpr (V == 1) {
+    o.w[0] = r.live ? quant_bits<E>(to_f32(c.e[0]), r) : 0u;
+  } else {
 #pragma unroll
-  for (int i = 0; i < Codes<E>::W; ++i) {
-    uint32_t b[4];
-    if (r.mode == 1) {
+    for (int i = 0; i < V / 4; ++i) {
+      uint32_t b[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) b[k] = quant_bits<E>(to_f32(c.e[4 * i + k]), r);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) b[k] = quant_bits_wide(to_f32(c.e[4 * i + k]), r);
+      const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+      o.w[i] = r.live ? lo | hi : 0u;
     }
-    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
-    o.w[i] = lo | hi;
   }
   return o;
 }
-template <class E, bool STREAM = false>
-__device__ __forceinline__ void store_codes(int8_t* p, int n, const Codes<E>& c) {
-  constexpr int V = Chunk<E>::V;
-  if (n >= V) {
-    if constexpr (V == 8) {
-      const uint64_t v = (uint64_t)c.w[1] << 32 | c.w[0];
-      if constexpr (STREAM)
-        __builtin_nontemporal_store(v, (u64_any*)p);
-      else
-        *(u64_any*)p = v;
-    } else {
-      if constexpr (STREAM)
-        __builtin_nontemporal_store(c.w[0], (u32_any*)p);
-      else
-        *(u32_any*)p = c.w[0];
-    }
+template <bool STREAM = false, class E, int V>
+__device__ __forceinline__ void store_codes(int8_t* p, const Codes<E, V>& c) {
+  if constexpr (V == 1) {
+    p[0] = (int8_t)c.w[0];
+  } else if constexpr (V == 8) {
+    const uint64_t v = (uint64_t)c.w[1] << 32 | c.w[0];
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(v, (u64_any*)p);
+    else
+      *(u64_any*)p = v;
   } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) p[i] = (int8_t)(c.w[i / 4] >> (8 * (i % 4)));
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(c.w[0], (u32_any*)p);
+    else
+      *(u32_any*)p = c.w[0];
   }
 }
 
@@ -209,9 +211,12 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // The larger of m and the largest abs_bits() of a chunk.
-template <class E>
-__device__ __forceinline__ uint32_t chunk_max_bits(const Chunk<E>& c, uint32_t m) {
-  if constexpr (sizeof(E) == 4) {
+template <class E, int V>
+__device__ __forceinline__ uint32_t chunk_max_bits(const Chunk<E, V>& c, uint32_t m) {
+  if constexpr (V == 1) {
+    const uint32_t b = abs_bits(to_f32(c.e[0]));
+    m = m > b ? m : b;
+  } else if constexpr (sizeof(E) == 4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t b = c.q[i] & 0x7fffffffu;
@@ -223,7 +228,7 @@ __device__ __forceinline__ uint32_t chunk_max_bits(const Chunk<E>& c, uint32_t m
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       p = __builtin_elementwise_max(p, __builtin_bit_cast(u16x2, c.q[i] & 0x7fff7fffu));
-    Chunk<E> big;
+    Chunk<E, V> big;
     big.q.x = p[0] > p[1] ? p[0] : p[1];
     const uint32_t b = abs_bits(to_f32(big.e[0]));
     m = m > b ? m : b;

@@ -27,6 +27,7 @@ constexpr int kChunkWaves = kChunkIds / 64;
 constexpr int kSubTokens = 16;      // most tokens a workgroup of the move kernel sorts and moves
 constexpr int kSelfChunks = 16;     // most chunks whose counts the move kernel adds up itself
 constexpr int kMaxT = 1 << 20;
+constexpr int kMaxRows = (1 << 24) - 1;  // a workgroup each stays a launch's size
 // A rows matrix above this is streamed past the caches (non-temporal loads and stores): it would
 // not be there any more for whoever reads it next, and the chip moves it faster so (16384 tokens
 // of 8 rows, 2048 bf16: sort 137 -> 116 us, combine 118 -> 102, its gradient 226 -> 207, 131072 rows
@@ -61,53 +62,49 @@ __device__ __forceinline__ int key_of_id(int id, int E) {
 // Chunks of a row that a thread holds at once.
 constexpr int kHeld = 4;
 
-// Copies a row's chunks [c0, c1) to its k places, threads tid of nthr; kHeld loads are in flight
-// before the first store.  A choice that was dropped has place -1.
-template <class E, bool STREAM>
-__device__ __forceinline__ void copy_row(const E* x, int H, const int* place, int k, E* rows,
-                                         int64_t rs, int c0, int c1, int tid, int nthr) {
-  constexpr int V = Chunk<E>::V;
-  for (int c = c0 + tid; c < c1; c += kHeld * nthr) {
-    Chunk<E> v[kHeld];
+// Loads chunks c, c + nthr, ... below c1 of a row.
+template <class E, int V>
+__device__ __forceinline__ void load_row(Chunk<E, V> (&v)[kHeld], const E* x, int H, int c,
+                                         int c1, int nthr) {
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-      const int ch = c + h * nthr;
-      if (ch < c1) v[h] = load_chunk(x + (int64_t)ch * V, H - ch * V);
-    }
+  for (int h = 0; h < kHeld; ++h)
+    if (c + h * nthr < c1) v[h] = load_chunk<V>(x + chunk_at<V>(c + h * nthr, H));
+}
+
+// Copies a row's chunks [c0, c1) to its k places, threads tid of nthr, each with kHeld loads in
+// flight before its first store (the first of them in v already).  A choice that was dropped
+// has place -1.
+template <bool STREAM, class E, int V>
+__device__ __forceinline__ void copy_row(const E* x, int H, const int* place, int k, E* rows,
+                                         int64_t rs, int c0, int c1, int tid, int nthr,
+                                         Chunk<E, V> (&v)[kHeld]) {
+  for (int c = c0 + tid; c < c1; c += kHeld * nthr) {
+    if (c != c0 + tid) load_row(v, x, H, c, c1, nthr);
     for (int j = 0; j < k; ++j) {
       const int p = place[j];
       if (p < 0) continue;
       E* const out = rows + (int64_t)p * rs;
 #pragma unroll
-      for (int h = 0; h < kHeld; ++h) {
-        const int ch = c + h * nthr;
-        if (ch < c1) store_chunk<E, STREAM>(out + (int64_t)ch * V, H - ch * V, v[h]);
-      }
+      for (int h = 0; h < kHeld; ++h)
+        if (c + h * nthr < c1) store_chunk<STREAM>(out + chunk_at<V>(c + h * nthr, H), v[h]);
     }
   }
 }
 
 // A row of H elements by G neighbouring lanes (G > 64: the whole workgroup): its scale and its
 // codes, computed once.  The row stays in registers between the maximum and the codes if G lanes
-// hold it (kHeld chunks each), else it is read again.  put(c, n, codes): the codes of chunk c,
-// of whose elements n are left.
-template <class E, int G, class Put>
+// hold it (kHeld chunks each, loaded by load_row before), else the rest is read twice.
+// put(at, codes): the codes of the chunk that starts at element `at`.
+template <int G, class E, int V, class Put>
 __device__ __forceinline__ RowQuant quant_row(const E* x, int H, int lane, uint32_t* s_max,
-                                              Put&& put) {
-  constexpr int V = Chunk<E>::V;
-  const int nc = (H + V - 1) / V;
-  Chunk<E> v[kHeld];
+                                              const Chunk<E, V> (&v)[kHeld], Put&& put) {
+  const int nc = chunk_count<V>(H);
   uint32_t m = 0;
-#pragma unroll
-  for (int h = 0; h < kHeld; ++h) {
-    const int c = lane + h * G;
-    if (c < nc) v[h] = load_chunk(x + (int64_t)c * V, H - c * V);
-  }
 #pragma unroll
   for (int h = 0; h < kHeld; ++h)
     if (lane + h * G < nc) m = chunk_max_bits(v[h], m);
   for (int c = lane + kHeld * G; c < nc; c += G)
-    m = chunk_max_bits(load_chunk(x + (int64_t)c * V, H - c * V), m);
+    m = chunk_max_bits(load_chunk<V>(x + chunk_at<V>(c, H)), m);
   if constexpr (G <= 64) {
     m = group_max_u32<G>(m);
   } else {
@@ -119,26 +116,25 @@ __device__ __forceinline__ RowQuant quant_row(const E* x, int H, int lane, uint3
   }
   const RowQuant r = row_quant(m);
 #pragma unroll
-  for (int h = 0; h < kHeld; ++h) {
-    const int c = lane + h * G;
-    if (c < nc) put(c, H - c * V, quant_chunk(v[h], r));
+  for (int h = 0; h < kHeld; ++h)
+    if (lane + h * G < nc) put(chunk_at<V>(lane + h * G, H), quant_chunk(v[h], r));
+  for (int c = lane + kHeld * G; c < nc; c += G) {
+    const int at = chunk_at<V>(c, H);
+    put(at, quant_chunk(load_chunk<V>(x + at), r));
   }
-  for (int c = lane + kHeld * G; c < nc; c += G)
-    put(c, H - c * V, quant_chunk(load_chunk(x + (int64_t)c * V, H - c * V), r));
   return r;
 }
 
 // The codes of a token's row to its k places.
-template <class E, int G, bool STREAM>
+template <int G, bool STREAM, class E, int V>
 __device__ __forceinline__ void quant_row_to(const E* x, int H, const int* place, int k,
                                              int8_t* rows, int64_t rs, float* row_scale, int lane,
-                                             uint32_t* s_max) {
-  constexpr int V = Chunk<E>::V;
+                                             uint32_t* s_max, const Chunk<E, V> (&v)[kHeld]) {
   const RowQuant r =
-      quant_row<E, G>(x, H, lane, s_max, [&](int c, int n, const Codes<E>& codes) {
+      quant_row<G>(x, H, lane, s_max, v, [&](int at, const Codes<E, V>& codes) {
         for (int j = 0; j < k; ++j) {
           const int p = place[j];
-          if (p >= 0) store_codes<E, STREAM>(rows + (int64_t)p * rs + (int64_t)c * V, n, codes);
+          if (p >= 0) store_codes<STREAM>(rows + (int64_t)p * rs + at, codes);
         }
       });
   if (lane < k && place[lane] >= 0) row_scale[place[lane]] = r.scale;
@@ -178,7 +174,7 @@ __device__ void prefix_counts(const int* total, int E, int* first_of, int* s_wav
 // token t's k assignments (a wave takes 64 ids at a time and adds up ballots), and moves column
 // slice y of the token's row; workgroup (T, 0) writes the offsets.  Latency is what it costs: one
 // read of the ids (L2), one barrier, one read and k writes of the row.
-template <class E, bool I8>
+template <class E, int V, bool I8>
 __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
   __shared__ int s_cnt[TOK_T / 64][kMaxTopK];
   __shared__ int s_place[kMaxTopK];
@@ -200,10 +196,17 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
     return;
   }
   const E* x = (const E*)a.x + (int64_t)t * a.xs;
+  // this workgroup's slice of the row, under way while the ids are counted
+  const int nc = a.x ? chunk_count<V>(a.H) : 0;
+  const int per = (nc + gridDim.y - 1) / gridDim.y;
+  const int c0 = blockIdx.y * per, c1 = min(nc, c0 + per);
+  Chunk<E, V> v[kHeld];
+  load_row(v, x, a.H, c0 + tid, c1, TOK_T);
   int own[kMaxTopK], cnt[kMaxTopK];
+  const int mine = lane < a.k ? key_of_id(a.ids[t * a.k + lane], a.E) : 0;
 #pragma unroll
   for (int j = 0; j < kMaxTopK; ++j) {
-    own[j] = j < a.k ? key_of_id(a.ids[t * a.k + j], a.E) : 0;
+    own[j] = __builtin_amdgcn_readlane(mine, j);
     cnt[j] = 0;
   }
   constexpr int AHEAD = 8;  // ids of a lane in flight
@@ -227,14 +230,15 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < kMaxTopK; ++j)
-    if (j < a.k && lane == 0) s_cnt[wave][j] = cnt[j];
+    if (j < a.k && lane == 0)
+      s_cnt[wave][j] = own[j] == 0x7fffffff ? -kSmallIds : cnt[j];
   __syncthreads();
   if (tid < a.k) {
     int p = 0;
 #pragma unroll
     for (int w = 0; w < TOK_T / 64; ++w) p += s_cnt[w][tid];
     const int at = t * a.k + tid;
-    if ((unsigned)a.ids[at] >= (unsigned)a.E) p = -1;
+    if (p < 0) p = -1;
     s_place[tid] = p;
     if (blockIdx.y == 0) {
       a.place[at] = p;
@@ -243,15 +247,11 @@ __global__ __launch_bounds__(TOK_T) void sort_small_kernel(SortArgs a) {
   }
   __syncthreads();
   if (!a.x) return;
-  if constexpr (I8) {
-    quant_row_to<E, TOK_T, false>(x, a.H, s_place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, tid,
-                                  s_max);
-  } else {
-    const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
-    const int per = (nc + gridDim.y - 1) / gridDim.y;
-    const int c0 = blockIdx.y * per, c1 = min(nc, c0 + per);
-    copy_row<E, false>(x, a.H, s_place, a.k, (E*)a.rows, a.rs, c0, c1, tid, TOK_T);
-  }
+  if constexpr (I8)  // one slice
+    quant_row_to<TOK_T, false>(x, a.H, s_place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, tid,
+                               s_max, v);
+  else
+    copy_row<false>(x, a.H, s_place, a.k, (E*)a.rows, a.rs, c0, c1, tid, TOK_T, v);
 }
 
 // Many assignments, first of two or three launches: the ids of each chunk counted by expert.
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
 // in LDS), writes their places and moves their rows, a wave per token or (WIDE) all waves on one
 // token after the other.  SELF: the counts are few enough that each workgroup adds them up itself
 // instead of a launch between.
-template <class E, bool I8, bool WIDE, bool STREAM, bool SELF>
+template <class E, int V, bool I8, bool WIDE, bool STREAM, bool SELF>
 __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, int subs) {
   extern __shared__ __align__(16) uint16_t s_cnt[];  // [kChunkWaves][E]
   __shared__ int s_id[kSubTokens * kMaxTopK], s_rank[kSubTokens * kMaxTopK];
@@ -404,16 +404,19 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, i
   }
   __syncthreads();
   if (!a.x) return;
-  const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
+  const int nc = chunk_count<V>(a.H);
   constexpr int G = WIDE ? TOK_T : 64;
   for (int t = t0 + (WIDE ? 0 : wave); t < t1; t += WIDE ? 1 : TOK_T / 64) {
     const E* x = (const E*)a.x + (int64_t)t * a.xs;
     const int* place = s_place + (t - t0) * a.k;
+    const int l = WIDE ? tid : lane;
+    Chunk<E, V> v[kHeld];
+    load_row(v, x, a.H, l, nc, G);
     if constexpr (I8)
-      quant_row_to<E, G, STREAM>(x, a.H, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale,
-                                 WIDE ? tid : lane, s_max[t & 1]);
+      quant_row_to<G, STREAM>(x, a.H, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, l,
+                              s_max[t & 1], v);
     else
-      copy_row<E, STREAM>(x, a.H, place, a.k, (E*)a.rows, a.rs, 0, nc, WIDE ? tid : lane, G);
+      copy_row<STREAM>(x, a.H, place, a.k, (E*)a.rows, a.rs, 0, nc, l, G, v);
   }
 }
 
@@ -432,29 +435,29 @@ struct CombineArgs {
 // y[t] = sum_j w[t][j] rows[place[t][j]], fp32, j ascending, rounded once.  A thread holds one
 // 16-byte chunk of one token's row and has the loads of eight choices in flight; 2^tpt_log
 // threads share a token (UNI: whole waves do, so places and weights are scalar loads).
-template <class E, bool W, bool UNI, bool STREAM>
+template <class E, int V, bool W, bool UNI, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void combine_kernel(CombineArgs a) {
-  constexpr int V = Chunk<E>::V, HELD = 8;
+  constexpr int HELD = 8;
   const int64_t g = (int64_t)blockIdx.x * TOK_T + threadIdx.x;
   int t = (int)(g >> a.tpt_log);
   if constexpr (UNI) t = __builtin_amdgcn_readfirstlane(t);
   const int c = (int)(g & ((1 << a.tpt_log) - 1)) + ((int)blockIdx.y << a.tpt_log);
-  const int n = a.H - c * V;
-  if (t >= a.T || n <= 0) return;
+  if (t >= a.T || c >= chunk_count<V>(a.H)) return;
+  const int col = chunk_at<V>(c, a.H);
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
   const int* place = a.place + (int64_t)t * a.k;
   const float* w = W ? a.w + (int64_t)t * a.k : nullptr;
-  const E* rows = (const E*)a.rows + (int64_t)c * V;
+  const E* rows = (const E*)a.rows + col;
   for (int j0 = 0; j0 < a.k; j0 += HELD) {
-    Chunk<E> v[HELD];
+    Chunk<E, V> v[HELD];
     bool in[HELD];
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
       const int p = j0 + h < a.k ? place[j0 + h] : -1;
       in[h] = (unsigned)p < (unsigned)a.n_rows;
-      if (in[h]) v[h] = load_chunk<E, STREAM>(rows + (int64_t)p * a.rs, n);
+      if (in[h]) v[h] = load_chunk<V, STREAM>(rows + (int64_t)p * a.rs);
     }
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
@@ -465,7 +468,7 @@ __global__ __launch_bounds__(TOK_T) void combine_kernel(CombineArgs a) {
         acc[i] = W ? fmaf(wj, to_f32(v[h].e[i]), acc[i]) : acc[i] + to_f32(v[h].e[i]);
     }
   }
-  store_chunk((E*)a.out + (int64_t)t * a.os + (int64_t)c * V, n, round_chunk<E>(acc));
+  store_chunk((E*)a.out + (int64_t)t * a.os + col, round_chunk<E, V>(acc));
 }
 
 struct CombineGradArgs {
@@ -485,9 +488,8 @@ struct CombineGradArgs {
 // A wave per assignment: drows[p] = w dy, dw = <dy, rows[p]> (fp32 products, per-lane partial
 // sums joined by shuffles in a fixed order), four chunks of each row in flight.  The waves of a
 // token read its dy row together.
-template <class E, bool STREAM>
+template <class E, int V, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) {
-  constexpr int V = Chunk<E>::V;
   const int lane = threadIdx.x & 63;
   const int64_t at = (int64_t)blockIdx.x * (TOK_T / 64) +
                      __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -501,31 +503,36 @@ __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) 
   const E* dy = (const E*)a.dout + at / a.k * a.ds;
   const E* r = (const E*)a.rows + (int64_t)p * a.rs;
   E* dr = (E*)a.drows + (int64_t)p * a.drs;
-  const int nc = (a.H + V - 1) / V;
+  const int nc = chunk_count<V>(a.H);
   float sum = 0.f;
   for (int c0 = lane; c0 < nc; c0 += 64 * kHeld) {
-    Chunk<E> g[kHeld], v[kHeld];
+    Chunk<E, V> g[kHeld], v[kHeld];
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
       const int c = c0 + 64 * h;
       if (c < nc) {
-        g[h] = load_chunk(dy + (int64_t)c * V, a.H - c * V);
-        if (a.dw) v[h] = load_chunk<E, STREAM>(r + (int64_t)c * V, a.H - c * V);
+        g[h] = load_chunk<V>(dy + chunk_at<V>(c, a.H));
+        if (a.dw) v[h] = load_chunk<V, STREAM>(r + chunk_at<V>(c, a.H));
       }
     }
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
       const int c = c0 + 64 * h;
       if (c >= nc) continue;
+      const int at = chunk_at<V>(c, a.H);
       if (a.drows) {
         float o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = w * to_f32(g[h].e[i]);
-        store_chunk<E, STREAM>(dr + (int64_t)c * V, a.H - c * V, round_chunk<E>(o));
+        store_chunk<STREAM>(dr + at, round_chunk<E, V>(o));
       }
       if (a.dw) {
+        const int twice = c * V - at;  // elements that the chunk before has added up
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum = fmaf(to_f32(g[h].e[i]), to_f32(v[h].e[i]), sum);
+        for (int i = 0; i < V; ++i) {
+          const float f = fmaf(to_f32(g[h].e[i]), to_f32(v[h].e[i]), sum);
+          sum = i >= twice ? f : sum;
+        }
       }
     }
   }
@@ -546,18 +553,19 @@ struct QuantArgs {
 };
 
 // G lanes per row (G = 256: a workgroup); one read of the row where they hold it.
-template <class E, int G, bool STREAM>
+template <class E, int V, int G, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void quantise_kernel(QuantArgs a) {
   __shared__ uint32_t s_max[TOK_T / 64];
-  constexpr int V = Chunk<E>::V;
   const int lane = threadIdx.x % G, row = blockIdx.x * (TOK_T / G) + threadIdx.x / G;
   const int end = a.rows_end ? min(*a.rows_end, a.M) : a.M;
   if (row >= end) return;
   int8_t* codes = a.codes + (int64_t)row * a.cs;
-  const RowQuant r = quant_row<E, G>((const E*)a.x + (int64_t)row * a.xs, a.K, lane, s_max,
-                                     [&](int c, int n, const Codes<E>& q) {
-                                       store_codes<E, STREAM>(codes + (int64_t)c * V, n, q);
-                                     });
+  const E* x = (const E*)a.x + (int64_t)row * a.xs;
+  Chunk<E, V> v[kHeld];
+  load_row(v, x, a.K, lane, chunk_count<V>(a.K), G);
+  const RowQuant r = quant_row<G>(x, a.K, lane, s_max, v, [&](int at, const Codes<E, V>& q) {
+    store_codes<STREAM>(codes + at, q);
+  });
   if (lane == 0) a.scale[row] = r.scale;
 }
 
@@ -570,21 +578,21 @@ bool float_type(int type) { return type >= MOE_T_BF16 && type <= MOE_T_FP32; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
 constexpr int kMaxCols = 1 << 20;
 
-int chunk_tokens(int k) { return kChunkIds / k; }
-int chunk_count(int T, int k) { return (T + chunk_tokens(k) - 1) / chunk_tokens(k); }
+int block_tokens(int k) { return kChunkIds / k; }
+int block_count(int T, int k) { return (T + block_tokens(k) - 1) / block_tokens(k); }
 
-template <class E, bool I8>
-void launch_sort(SortArgs& a, hipStream_t s) {
+template <class E, int V, bool I8>
+void launch_sort_by(SortArgs& a, hipStream_t s) {
+  const int nc = a.x ? chunk_count<V>(a.H) : 0;
   if (a.N <= kSmallIds) {
-    const int slices = I8 || !a.x ? 1 : (a.H + 64 * Chunk<E>::V * 4 - 1) / (64 * Chunk<E>::V * 4);
-    hipLaunchKernelGGL((sort_small_kernel<E, I8>), dim3(a.T + 1, min(slices, 64)), dim3(TOK_T), 0,
-                       s, a);
+    const int slices = I8 ? 1 : std::max(1, std::min(64, (nc + TOK_T - 1) / TOK_T));
+    hipLaunchKernelGGL((sort_small_kernel<E, V, I8>), dim3(a.T + 1, slices), dim3(TOK_T), 0, s,
+                       a);
     return;
   }
   hipLaunchKernelGGL(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
   const bool self = a.nblk <= kSelfChunks;
   if (!self) hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
-  const int nc = (a.H + Chunk<E>::V - 1) / Chunk<E>::V;
   // a wave per token, unless there are too few tokens for that to fill the chip, or rows of codes
   // that a wave cannot hold; 16 tokens per workgroup amortise its counting, fewer fill the chip
   // (8 rows of 2048 bf16 per token: 4096 tokens 36 us with 4, 41 with 4 and whole workgroups per
@@ -592,21 +600,27 @@ void launch_sort(SortArgs& a, hipStream_t s) {
   const bool wide = a.T < 2048 || (I8 && nc > 64 * kHeld);
   const int sub = a.T < 2048 ? 1 : a.T < 8192 ? 4 : kSubTokens;
   const bool stream = (int64_t)a.N * a.H * (I8 ? 1 : (int)sizeof(E)) > kStreamBytes;
-  const auto kernel = self ? wide ? sort_move_kernel<E, I8, true, false, true>
-                                  : sort_move_kernel<E, I8, false, false, true>
-                      : wide ? stream ? sort_move_kernel<E, I8, true, true, false>
-                                      : sort_move_kernel<E, I8, true, false, false>
-                             : stream ? sort_move_kernel<E, I8, false, true, false>
-                                      : sort_move_kernel<E, I8, false, false, false>;
+  const auto kernel = self ? wide ? sort_move_kernel<E, V, I8, true, false, true>
+                                  : sort_move_kernel<E, V, I8, false, false, true>
+                      : wide ? stream ? sort_move_kernel<E, V, I8, true, true, false>
+                                      : sort_move_kernel<E, V, I8, true, false, false>
+                             : stream ? sort_move_kernel<E, V, I8, false, true, false>
+                                      : sort_move_kernel<E, V, I8, false, false, false>;
   const int subs = (a.tok_blk + sub - 1) / sub;
   hipLaunchKernelGGL(kernel, dim3(a.nblk * subs), dim3(TOK_T), (size_t)kChunkWaves * a.E * 2, s, a,
                      sub, subs);
 }
 
-template <class E>
-void launch_combine(CombineArgs& a, hipStream_t s) {
-  constexpr int V = Chunk<E>::V;
-  const int nc = (a.H + V - 1) / V;
+// Rows shorter than a chunk go element by element, in all the launches.
+template <class E, bool I8>
+void launch_sort(SortArgs& a, hipStream_t s) {
+  a.H >= kChunk<E> || !a.x ? launch_sort_by<E, kChunk<E>, I8>(a, s)
+                           : launch_sort_by<E, 1, I8>(a, s);
+}
+
+template <class E, int V>
+void launch_combine_by(CombineArgs& a, hipStream_t s) {
+  const int nc = chunk_count<V>(a.H);
   a.tpt_log = 0;
   while (a.tpt_log < 8 && (1 << a.tpt_log) < nc) ++a.tpt_log;
   const int64_t thr = (int64_t)a.T << a.tpt_log;
@@ -614,28 +628,34 @@ void launch_combine(CombineArgs& a, hipStream_t s) {
                   (unsigned)((nc + (1 << a.tpt_log) - 1) >> a.tpt_log));
   const bool uni = a.tpt_log >= 6;
   const bool stream = (int64_t)a.T * a.k * a.H * (int)sizeof(E) > kStreamBytes;
-  const auto kernel = a.w ? uni ? stream ? combine_kernel<E, true, true, true>
-                                         : combine_kernel<E, true, true, false>
-                                : combine_kernel<E, true, false, false>
-                          : uni ? stream ? combine_kernel<E, false, true, true>
-                                         : combine_kernel<E, false, true, false>
-                                : combine_kernel<E, false, false, false>;
+  const auto kernel = a.w ? uni ? stream ? combine_kernel<E, V, true, true, true>
+                                         : combine_kernel<E, V, true, true, false>
+                                : combine_kernel<E, V, true, false, false>
+                          : uni ? stream ? combine_kernel<E, V, false, true, true>
+                                         : combine_kernel<E, V, false, true, false>
+                                : combine_kernel<E, V, false, false, false>;
   hipLaunchKernelGGL(kernel, grid, dim3(TOK_T), 0, s, a);
+}
+template <class E>
+void launch_combine(CombineArgs& a, hipStream_t s) {
+  a.H >= kChunk<E> ? launch_combine_by<E, kChunk<E>>(a, s) : launch_combine_by<E, 1>(a, s);
 }
 
 template <class E>
 void launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
   const bool stream = (int64_t)a.T * a.k * a.H * (int)sizeof(E) > kStreamBytes;
-  const auto kernel = stream ? combine_grad_kernel<E, true> : combine_grad_kernel<E, false>;
+  const auto kernel = a.H < kChunk<E> ? combine_grad_kernel<E, 1, false>
+                      : stream        ? combine_grad_kernel<E, kChunk<E>, true>
+                                      : combine_grad_kernel<E, kChunk<E>, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T * a.k + TOK_T / 64 - 1) / (TOK_T / 64))),
                      dim3(TOK_T), 0, s, a);
 }
 
-template <class E, int G>
+template <class E, int V, int G>
 void launch_quantise_by(const QuantArgs& a, hipStream_t s) {
   constexpr int rows = TOK_T / G;
   const bool stream = (int64_t)a.M * a.K * (int)sizeof(E) > kStreamBytes;
-  const auto kernel = stream ? quantise_kernel<E, G, true> : quantise_kernel<E, G, false>;
+  const auto kernel = stream ? quantise_kernel<E, V, G, true> : quantise_kernel<E, V, G, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(((int64_t)a.M + rows - 1) / rows)), dim3(TOK_T), 0,
                      s, a);
 }
@@ -643,15 +663,18 @@ void launch_quantise_by(const QuantArgs& a, hipStream_t s) {
 // As few lanes per row as hold it in kHeld chunks each.
 template <class E>
 void launch_quantise(const QuantArgs& a, hipStream_t s) {
-  const int nc = (a.K + Chunk<E>::V - 1) / Chunk<E>::V;
-  if (nc <= 16 * kHeld)
-    launch_quantise_by<E, 16>(a, s);
+  constexpr int V = kChunk<E>;
+  const int nc = chunk_count<V>(a.K);
+  if (a.K < V)
+    launch_quantise_by<E, 1, 16>(a, s);
+  else if (nc <= 16 * kHeld)
+    launch_quantise_by<E, V, 16>(a, s);
   else if (nc <= 32 * kHeld)
-    launch_quantise_by<E, 32>(a, s);
+    launch_quantise_by<E, V, 32>(a, s);
   else if (nc <= 64 * kHeld)
-    launch_quantise_by<E, 64>(a, s);
+    launch_quantise_by<E, V, 64>(a, s);
   else
-    launch_quantise_by<E, 256>(a, s);
+    launch_quantise_by<E, V, 256>(a, s);
 }
 
 moe_status combine(const void* rows, int64_t rs, int n_rows, int type, const int* place,
@@ -680,7 +703,7 @@ extern "C" {
 
 size_t moe_sort_workspace_bytes(int32_t T, int32_t top_k, int32_t experts) {
   if (!tokens_ok(T, top_k, experts) || T * top_k <= kSmallIds) return 0;
-  return sizeof(int) * (size_t)chunk_count(T, top_k) * (size_t)experts;
+  return sizeof(int) * (size_t)block_count(T, top_k) * (size_t)experts;
 }
 
 moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, int32_t experts,
@@ -706,7 +729,7 @@ moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, in
   if (!on_current_device(offsets)) return MOE_E_INVALID;
   SortArgs a{topk_idx, T,       top_k, experts, T * top_k, x,
              x_stride, hidden,  offsets, order, place,     rows,
-             rows_stride, row_scale, (int*)workspace, chunk_tokens(top_k), chunk_count(T, top_k)};
+             rows_stride, row_scale, (int*)workspace, block_tokens(top_k), block_count(T, top_k)};
   const hipStream_t s = (hipStream_t)stream;
   const int type = x ? x_type : MOE_T_FP32;
   if (type == MOE_T_BF16)
@@ -762,7 +785,7 @@ moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const 
 moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
                              int8_t* codes, int64_t codes_stride, float* scale,
                              const int32_t* rows_end, void* stream) {
-  if (!float_type(type) || M < 0 || K < 1 || K > kMaxCols || !rows_ok(x, x_stride, K, type) ||
+  if (!float_type(type) || M < 0 || M > kMaxRows || K < 1 || K > kMaxCols || !rows_ok(x, x_stride, K, type) ||
       !rows_ok(codes, codes_stride, K, MOE_T_I8) || !scale || !aligned4(scale) ||
       !aligned4(rows_end) || !on_current_device(codes))
     return MOE_E_INVALID;

@@ -457,7 +457,7 @@ moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const 
  * magnitude, scale = m / 127 (fp32) and code = 127 x / m to the nearest integer, ties to even,
  * exactly.  A row of zeros has scale 0; a row that holds a NaN or an infinity has scale NaN and
  * codes 0.  rows_end: NULL, or a device word: rows from *rows_end on are not read and their
- * outputs left as they were (offsets + experts of a sort).  K 1..1048576. */
+ * outputs left as they were (offsets + experts of a sort).  M 0..16777215, K 1..1048576. */
 moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
                              int8_t* codes, int64_t codes_stride, float* scale,
                              const int32_t* rows_end, void* stream);
@@ -471,7 +471,7 @@ moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int3
  * to no group are left as they were.  The integer sum is exact.
  * epilogue MOE_EPI_NONE: out [M][N] = c.  MOE_EPI_SWIGLU (N even): channels 2i and 2i + 1 are
  * gate and up (the order of an expert blob's rows), out [M][N/2] = silu(c[2i]) * c[2i + 1].
- * out_type bf16, fp16 or fp32.  M 0..16777216, N 1..1048576, K 1..131071 (a longer sum could
+ * out_type bf16, fp16 or fp32.  M 0..16777215, N 1..1048576, K 1..131071 (a longer sum could
  * leave 32 bits), groups 1..1024. */
 #define MOE_EPI_NONE 0
 #define MOE_EPI_SWIGLU 1

@@ -131,7 +131,8 @@ SORTS = [  # T, k, experts, share dropped, H, padding, start
     (1, 1, 1, 0, 1, 0, 0), (1, 8, 128, 0, 2048, 0, 0), (4, 8, 256, 0, 6144, 0, 0),
     (3, 16, 7, 0.3, 257, 3, 1), (512, 8, 128, 0, 96, 0, 0), (513, 8, 128, 0.5, 96, 8, 0),
     (1000, 6, 60, 0.1, 130, 1, 3), (2049, 2, 1024, 0, 40, 0, 0), (5000, 1, 3, 0.9, 64, 0, 0),
-    (300, 16, 16, 1.0, 33, 0, 0), (4100, 1, 1, 0, 17, 0, 5)]
+    (300, 16, 16, 1.0, 33, 0, 0), (4100, 1, 1, 0, 17, 0, 5),
+    (700, 6, 9, 0.2, 3, 1, 0), (40, 2, 4, 0, 7, 0, 1), (9000, 2, 20, 0.1, 12, 0, 0)]
 
 
 @pytest.mark.parametrize("T,k,experts,drop,H,pad,at", SORTS)
@@ -175,6 +176,11 @@ def test_quantise_values(env, kind):
     x[10] = torch.linspace(-1, 1, K, device="cuda") * torch.finfo(types[kind]).max
     x[11] *= 1e-6
     x[12:40] = torch.round(x[12:40] * 16) / 16  # few distinct values: many ties
+    x[40:44] *= 1e25
+    x[44:48] *= 1e-25
+    odd = torch.arange(-127, 128, 2, device="cuda").double() / 254  # code ties, in full precision
+    x[48:56, :128] = odd * torch.randint(1, 1 << 20, (8, 1), generator=g, device="cuda")
+    x[48:56, 128:] = x[48:56, :1] * 2
     x = x.to(types[kind])
     codes = torch.full((64, K), 99, dtype=torch.int8, device="cuda")
     scale = torch.full((64,), 99.0, device="cuda")
@@ -188,6 +194,7 @@ def test_quantise_values(env, kind):
 
 @pytest.mark.parametrize("M,K,pad,at", [(1, 1, 0, 0), (8, 768, 0, 0), (1, 20001, 0, 0),
                                         (1000, 129, 3, 1), (5, 8191, 8, 0), (70000, 72, 0, 0),
+                                        (100, 5, 1, 1), (33, 515, 0, 0), (17, 2050, 2, 2),
                                         (3, 131072, 0, 0)])
 @pytest.mark.parametrize("kind", KINDS)
 def test_quantise(env, M, K, pad, at, kind):
@@ -219,7 +226,8 @@ def _places(torch, g, T, k, drop):
 
 COMBINES = [(1, 8, 2048, 0, 0, 0), (8, 8, 2048, 0, 0, 0), (1, 1, 1, 0, 0, 0),
             (777, 6, 1000, 0, 0, 0), (300, 16, 257, 0.3, 3, 1), (100, 3, 63, 1.0, 0, 0),
-            (2, 5, 20001, 0.2, 1, 0), (3000, 2, 40, 0.5, 8, 0), (64, 8, 6144, 0.1, 0, 0)]
+            (2, 5, 20001, 0.2, 1, 0), (3000, 2, 40, 0.5, 8, 0), (64, 8, 6144, 0.1, 0, 0),
+            (500, 4, 5, 0.2, 2, 1), (333, 7, 9, 0.1, 0, 3), (50, 2, 515, 0, 0, 0)]
 
 
 def _wide_out(torch, rows, cols, kind):
@@ -368,8 +376,10 @@ def _product_ref(torch, a, a_scale, w, w_scale, N, offsets, swiglu):
             ref[lo:hi] = gate * torch.sigmoid(gate) * up
             # gate and up: the sum's conversion and two scales (3 roundings each), an error of
             # the gate acts on silu 1 + |gate| times at most; exp, 1 + exp, reciprocal (1 ulp
-            # each, the exponent's own remainder) and three products
-            tol[lo:hi] = ref[lo:hi].abs() * (16 + 3 * gate.abs()) + 1e-30 * up.abs()
+            # each, the exponent's own remainder) and three products; where exp(-gate) leaves
+            # fp32, above 2^128, the result is 0 and |silu| was below |gate| 2^-128
+            tol[lo:hi] = (ref[lo:hi].abs() * (16 + 3 * gate.abs())
+                          + (gate * up).abs() * 2.0 ** -128 / U32)
         else:
             ref[lo:hi] = c
             tol[lo:hi] = 3 * c.abs()
@@ -475,6 +485,19 @@ def test_product_by_group(env, name, N, K, pad, kind, swiglu):
     a_scale, w_scale = _scales(torch, g, M, G * N)
     _check_product(env, a, a_scale, w, w_scale, N, G, _offsets(torch, counts, before), swiglu,
                    kind)
+
+
+@pytest.mark.parametrize("M", [5, 70, 1500])
+def test_product_swiglu_range(env, M):
+    """Gates from -127 to 127 (sums of one product), where exp(-gate) runs from 0 to infinity."""
+    torch = env[0]
+    w = torch.empty(2 * 255, 1, dtype=torch.int8, device="cuda")
+    w[0::2, 0] = torch.arange(-127, 128, device="cuda").to(torch.int8)
+    w[1::2, 0] = 100
+    a = torch.ones(M, 1, dtype=torch.int8, device="cuda")
+    one = torch.ones(2 * 255, device="cuda")
+    for kind in KINDS:
+        _check_product(env, a, torch.ones(M, device="cuda"), w, one, 510, 1, None, True, kind)
 
 
 def test_product_extremes(env):

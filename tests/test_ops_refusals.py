@@ -85,7 +85,8 @@ def test_combine_grad_refuses(bad):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(x=None), dict(x_stride=63), dict(type=I8), dict(M=-1), dict(K=0), dict(K=(1 << 20) + 1),
+    dict(x=None), dict(x_stride=63), dict(type=I8), dict(M=-1), dict(M=1 << 24), dict(K=0),
+    dict(K=(1 << 20) + 1),
     dict(codes=None), dict(codes_stride=63), dict(scale=None), dict(scale=P + 2),
     dict(rows_end=P + 1), dict(x=P + 1)])
 def test_quantise_refuses(bad):
@@ -100,7 +101,7 @@ PRODUCT = dict(a=P, a_stride=64, a_scale=P, M=16, K=64, w=P, w_stride=64, w_scal
 
 @pytest.mark.parametrize("bad", [
     dict(a=None), dict(a_stride=63), dict(a_scale=None), dict(a_scale=P + 2), dict(M=-1),
-    dict(M=(1 << 24) + 1), dict(K=0), dict(K=131072, a_stride=131072, w_stride=131072),
+    dict(M=1 << 24), dict(K=0), dict(K=131072, a_stride=131072, w_stride=131072),
     dict(w=None), dict(w_stride=63), dict(w_scale=None), dict(w_scale=P + 2), dict(N=0),
     dict(N=(1 << 20) + 1), dict(groups=0), dict(groups=1025), dict(offsets=None),
     dict(offsets=P + 2), dict(epilogue=2), dict(epilogue=-1), dict(epilogue=1, N=31),
