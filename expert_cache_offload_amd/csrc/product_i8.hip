@@ -184,13 +184,32 @@ __device__ __forceinline__ void store_rows(const int8_t* stage, int lane, E* out
 // which launch, the search of the group and the first load's way are about half.
 constexpr int FT = 256, FN = 16, FU = 8;  // threads, channels, steps in flight
 
-__device__ __forceinline__ i32x4 load_k(const int8_t* p, int n) {  // n bytes of the row are left
-  if (n >= 16) return *(const i32x4*)&(*(const u32x4_any*)p);
-  uint32_t v[4] = {0, 0, 0, 0};
+__device__ __forceinline__ i32x4 load_16(const int8_t* p) {
+  return __builtin_bit_cast(i32x4, *(const u32x4_any*)p);
+}
+
+// 16 bytes for a step of the product from p on, where n bytes of a row of K >= 16 are left: all 16,
+// or the row's last 16 with those before p zeroed (which byte of a step is which does not matter,
+// as long as both operands agree), or zeros.
+__device__ __forceinline__ i32x4 load_end(const int8_t* p, int n) {
+  i32x4 q = load_16(n >= 16 ? p : p + n - 16);
+  const int cut = 16 - min(max(n, 0), 16);
 #pragma unroll
-  for (int b = 0; b < 15; ++b)
-    if (b < n) v[b >> 2] |= (uint32_t)(uint8_t)p[b] << (8 * (b & 3));
-  return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+  for (int d = 0; d < 4; ++d) {
+    const int b = cut - 4 * d;  // bytes of this word that lie before p
+    q[d] = b >= 4 ? 0 : b <= 0 ? q[d] : q[d] & (int)(~0u << (8 * b));
+  }
+  return q;
+}
+// The same for rows of K < 16 bytes, n = K of them at p (or none).
+__device__ __forceinline__ i32x4 load_short(const int8_t* p, int n) {
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int b = n - 1; b >= 0; --b) {
+    hi = hi << 8 | lo >> 56;
+    lo = lo << 8 | (uint8_t)p[b];
+  }
+  return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
 }
 
 template <class E, bool SWIGLU, int RT>
@@ -237,9 +256,9 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
     i32x4 fw[FU], fa[FU][RT];
 #pragma unroll
     for (int u = 0; u < FU; ++u) {
-      fw[u] = load_k(pw + (s + u) * 64, 16);
+      fw[u] = load_16(pw + (s + u) * 64);
 #pragma unroll
-      for (int t = 0; t < RT; ++t) fa[u][t] = load_k(pa[t] + (s + u) * 64, 16);
+      for (int t = 0; t < RT; ++t) fa[u][t] = load_16(pa[t] + (s + u) * 64);
     }
 #pragma unroll
     for (int u = 0; u < FU; ++u)
@@ -249,11 +268,12 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
   }
   for (; s < s1; ++s) {
     const int n = a.K - s * 64 - piece;
-    const i32x4 fw = load_k(pw + s * 64, n);
+    const i32x4 fw = a.K >= 16 ? load_end(pw + s * 64, n) : load_short(pw, n);
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw, load_k(pa[t] + s * 64, n), acc[t], 0, 0,
-                                                    0);
+    for (int t = 0; t < RT; ++t) {
+      const i32x4 fa = a.K >= 16 ? load_end(pa[t] + s * 64, n) : load_short(pa[t], n);
+      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw, fa, acc[t], 0, 0, 0);
+    }
   }
   // lane: row lane % 16 of the tile, channels 4 (lane / 16) + 0..3
 #pragma unroll
@@ -409,22 +429,20 @@ void product_tile_kernel(ProdArgs a) {
   };
   auto fetch = [&](int round) {
     const int k0 = (round * KS + ks) * LK;
+    if (k0 + LK <= a.K) {
 #pragma unroll
-    for (int i = 0; i < LPW; ++i) held[i] = load_k(src[i] + k0, a.K - k0 - 16 * chunk_of(i));
-  };
-  // Stage `round` on its way to half buf: by loads to LDS, or from registers while the next one is
-  // fetched into them.
-  auto advance = [&](int round, int buf) {
-    if constexpr (ANY) {
+      for (int i = 0; i < LPW; ++i) held[i] = load_16(src[i] + k0);
+    } else if (a.K >= 16) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i)
-        *(i32x4*)(stages + buf * STAGE + (wave * LPW + i) * 1024 + lane * 16) = held[i];
-      if (round + 1 < rounds) fetch(round + 1);
+        held[i] = load_end(src[i] + k0, a.K - k0 - 16 * chunk_of(i));
     } else {
-      load_stage(round, buf);
+#pragma unroll
+      for (int i = 0; i < LPW; ++i)
+        held[i] = load_short(src[i], chunk_of(i) == 0 && k0 == 0 ? a.K : 0);
     }
   };
-  // Takes up a tile: its first stage and its scales (into half sb of their arrays).
+  // Takes up a tile: its scales (into half sb of their arrays) and its first stage.
   auto begin = [&](int t, int sb) {
     int mt, nt;
     tile_of(t, MT, NT, mt, nt);
@@ -454,10 +472,12 @@ void product_tile_kernel(ProdArgs a) {
       else
         off[i] = (uint32_t)at + 16 * chunk_of(i);
     }
-    if constexpr (ANY) fetch(0);
-    advance(0, 0);
+    if constexpr (ANY)
+      fetch(0);
+    else
+      load_stage(0, 0);
   };
-  begin(tile, 0);
+  if constexpr (!ANY) begin(tile, 0);
   const int8_t* rw = stages + (wn + channel_of_row(r32)) * LK;
   const int8_t* ra = stages + (BN + wm + r32) * LK;
   auto read = [&](i32x4 (&fw)[NI], i32x4 (&fa)[MI], int buf, int kk) {
@@ -476,11 +496,10 @@ void product_tile_kernel(ProdArgs a) {
         for (int j = 0; j < MI; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
     };
+    if constexpr (ANY) begin(tile, sb);
     const int m1 = m0 + wm, n1 = n0 + wn, end1 = end;
     const bool active = m1 < end && n1 < a.N;
     const int mine = active ? (nst - ks + KS - 1) / KS : 0;  // rounds this wave multiplies in
-    stage_barrier();
-    if (rounds > 1) advance(1, 1);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -488,24 +507,47 @@ void product_tile_kernel(ProdArgs a) {
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
     i32x4 fw0[NI], fa0[MI], fw1[NI], fa1[MI];
-    if (mine > 0) read(fw0, fa0, 0, 0);
-    int rd = 0;
-    for (; rd < mine; ++rd) {
-      const int buf = rd & 1;
+    // a round's products up to its last step, whose fragments are then in registers
+    const auto most = [&](int buf) {
       read(fw1, fa1, buf, 1);
       multiply(fw0, fa0);
       read(fw0, fa0, buf, 2);
       multiply(fw1, fa1);
       read(fw1, fa1, buf, 3);
       multiply(fw0, fa0);
+    };
+    if constexpr (ANY) {
+      // the two rounds before the first only bring the first two stages in
+      for (int rd = -2; rd < rounds; ++rd) {
+        const bool on = rd >= 0 && rd < mine;
+        if (on) most(rd & 1);
+        stage_barrier();
+        if (rd + 2 < rounds) {
+#pragma unroll
+          for (int i = 0; i < LPW; ++i)
+            *(i32x4*)(stages + (rd & 1) * STAGE + (wave * LPW + i) * 1024 + lane * 16) = held[i];
+          if (rd + 3 < rounds) fetch(rd + 3);
+        }
+        if (rd >= -1 && rd + 1 < mine) read(fw0, fa0, (rd + 1) & 1, 0);
+        if (on) multiply(fw1, fa1);
+      }
+    } else {
       stage_barrier();
-      if (rd + 2 < rounds) advance(rd + 2, buf);
-      if (rd + 1 < mine) read(fw0, fa0, buf ^ 1, 0);
-      multiply(fw1, fa1);
-    }
-    for (; rd < rounds; ++rd) {
-      stage_barrier();
-      if (rd + 2 < rounds) advance(rd + 2, rd & 1);
+      if (rounds > 1) load_stage(1, 1);
+      if (mine > 0) read(fw0, fa0, 0, 0);
+      int rd = 0;
+      for (; rd < mine; ++rd) {
+        const int buf = rd & 1;
+        most(buf);
+        stage_barrier();
+        if (rd + 2 < rounds) load_stage(rd + 2, buf);
+        if (rd + 1 < mine) read(fw0, fa0, buf ^ 1, 0);
+        multiply(fw1, fa1);
+      }
+      for (; rd < rounds; ++rd) {
+        stage_barrier();
+        if (rd + 2 < rounds) load_stage(rd + 2, rd & 1);
+      }
     }
     if constexpr (KS > 1) {  // the parts of K added up by the first (integers: exact)
       static_assert(NI == 1 && MI == 1 && (KS - 1) * TW * 4096 <= 2 * KS * STAGE);
@@ -532,7 +574,8 @@ void product_tile_kernel(ProdArgs a) {
     }
     tile += gridDim.x;
     const bool more = tile < ntiles;
-    if (more) begin(tile, sb ^ 1);  // the first half of the stages, the other half of the scales
+    // the first half of the stages is free, and the other half of the scales
+    if (!ANY && more) begin(tile, sb ^ 1);
     if (active && ks == 0) {
       // the second half of the stages is free until the next tile's first barrier: 2 KiB a wave
       constexpr int V = kChunk<E>, OB = 16 * (int)sizeof(E) / (SWIGLU ? 2 : 1);

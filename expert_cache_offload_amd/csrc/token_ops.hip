@@ -406,17 +406,22 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, i
   if (!a.x) return;
   const int nc = chunk_count<V>(a.H);
   constexpr int G = WIDE ? TOK_T : 64;
-  for (int t = t0 + (WIDE ? 0 : wave); t < t1; t += WIDE ? 1 : TOK_T / 64) {
-    const E* x = (const E*)a.x + (int64_t)t * a.xs;
-    const int* place = s_place + (t - t0) * a.k;
-    const int l = WIDE ? tid : lane;
-    Chunk<E, V> v[kHeld];
-    load_row(v, x, a.H, l, nc, G);
+  constexpr int STEP = WIDE ? 1 : TOK_T / 64;
+  const int l = WIDE ? tid : lane;
+  const E* x = (const E*)a.x + (int64_t)t0 * a.xs;
+  int t = WIDE ? 0 : wave;  // of the workgroup's tokens
+  Chunk<E, V> v[kHeld], next[kHeld];
+  if (t < t1 - t0) load_row(v, x + (int64_t)t * a.xs, a.H, l, nc, G);
+  for (; t < t1 - t0; t += STEP) {
+    if (t + STEP < t1 - t0) load_row(next, x + (int64_t)(t + STEP) * a.xs, a.H, l, nc, G);
+    const int* place = s_place + t * a.k;
     if constexpr (I8)
-      quant_row_to<G, STREAM>(x, a.H, place, a.k, (int8_t*)a.rows, a.rs, a.row_scale, l,
-                              s_max[t & 1], v);
+      quant_row_to<G, STREAM>(x + (int64_t)t * a.xs, a.H, place, a.k, (int8_t*)a.rows, a.rs,
+                              a.row_scale, l, s_max[t & 1], v);
     else
-      copy_row<STREAM>(x, a.H, place, a.k, (E*)a.rows, a.rs, 0, nc, l, G, v);
+      copy_row<STREAM>(x + (int64_t)t * a.xs, a.H, place, a.k, (E*)a.rows, a.rs, 0, nc, l, G, v);
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) v[h] = next[h];
   }
 }
 
