@@ -686,7 +686,7 @@ template <class E, bool SWIGLU>
 void launch_product(const ProdArgs& a, hipStream_t s) {
   const bool aligned = !(((uintptr_t)a.a | (uintptr_t)a.w | (uintptr_t)a.as | (uintptr_t)a.ws |
                           (uintptr_t)a.K) & 15) &&
-                       a.as < (1 << 23) && a.ws < (1 << 23);
+                       a.as < (1 << 22) && a.ws < (1 << 22);  // a tile's offsets: 31 bits
   // Few rows: the streaming kernel takes 16 of them as fast as one; with more the tiles win
   // (64 rows x 5000 channels x 4096: 13.5 against 22.8 us) where alignment allows them, and for
   // 128 rows of 128 groups the two are equal (42.0 and 42.5 us, the weights' bytes).

@@ -140,8 +140,8 @@ __device__ __forceinline__ void quant_row_to(const E* x, int H, const int* place
   if (lane < k && place[lane] >= 0) row_scale[place[lane]] = r.scale;
 }
 
-// first[0..E] = exclusive prefix of total[0..E-1] (LDS), one workgroup of nthr threads; first may be
-// global.  Ends with the workgroup's writes done but not yet synchronised.
+// first_of[0..E] (LDS or global) = exclusive prefix of total[0..E-1] (LDS), by one workgroup of nthr
+// threads, whose writes are not synchronised yet when it returns.
 __device__ void prefix_counts(const int* total, int E, int* first_of, int* s_wave, int tid,
                               int nthr) {
   const int per = (E + nthr - 1) / nthr;
@@ -270,9 +270,9 @@ __global__ __launch_bounds__(TOK_T) void sort_count_kernel(SortArgs a) {
 }
 
 // Second, where there are more than kSelfChunks chunks: one workgroup turns the counts into first
-// places.  Thread (g, e) adds up a segment g of
-// the chunks of expert e, the segments and then the experts are scanned, and a second pass over
-// the counts writes the running place.
+// places.  Thread (g, e) adds up a segment g of the chunks of expert e, the segments and then the
+// experts are scanned, and the running place of each chunk is written over its count.  128
+// chunks of 128 experts: 4.8 us, two memory latencies and the launch.
 __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
   __shared__ int s_seg[SCAN_T];
   __shared__ int s_total[kMaxExperts];
@@ -327,8 +327,10 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
 // Last: a workgroup takes `sub` tokens of a chunk, ranks the chunk's ids up to its own last one (a
 // wave finds the lanes that hold its id by ballots over the id's bits; counts per wave and expert
 // in LDS), writes their places and moves their rows, a wave per token or (WIDE) all waves on one
-// token after the other.  SELF: the counts are few enough that each workgroup adds them up itself
-// instead of a launch between.
+// token after the other, the next token's row under way while one is written.  SELF: the counts
+// are few enough that each workgroup adds them up itself instead of a launch between (1024 tokens
+// of 8: 16 us in all, 24 with the launch and 16 tokens per workgroup).  16384 tokens of 8 rows of
+// 2048 bf16: 104 us for 605 MB, 5.8 TB/s, the rate of writes.
 template <class E, int V, bool I8, bool WIDE, bool STREAM, bool SELF>
 __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, int subs) {
   extern __shared__ __align__(16) uint16_t s_cnt[];  // [kChunkWaves][E]
@@ -439,7 +441,8 @@ struct CombineArgs {
 
 // y[t] = sum_j w[t][j] rows[place[t][j]], fp32, j ascending, rounded once.  A thread holds one
 // 16-byte chunk of one token's row and has the loads of eight choices in flight; 2^tpt_log
-// threads share a token (UNI: whole waves do, so places and weights are scalar loads).
+// threads share a token (UNI: whole waves do, so places and weights are scalar loads).  16384
+// tokens of 8 rows of 2048 bf16: 104 us, 5.8 TB/s, bound by the rows' reads.
 template <class E, int V, bool W, bool UNI, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void combine_kernel(CombineArgs a) {
   constexpr int HELD = 8;
@@ -492,7 +495,8 @@ struct CombineGradArgs {
 
 // A wave per assignment: drows[p] = w dy, dw = <dy, rows[p]> (fp32 products, per-lane partial
 // sums joined by shuffles in a fixed order), four chunks of each row in flight.  The waves of a
-// token read its dy row together.
+// token read its dy row together: of 16384 tokens of 8 rows of 2048 bf16 1.22 GB move for 1.14,
+// in 205 us.
 template <class E, int V, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) {
   const int lane = threadIdx.x & 63;
@@ -557,7 +561,9 @@ struct QuantArgs {
   const int* rows_end;  // may be null
 };
 
-// G lanes per row (G = 256: a workgroup); one read of the row where they hold it.
+// G lanes per row (G = 256: a workgroup); one read of the row where they hold it.  131072 rows of
+// 768 bf16: 51 us, 5.9 TB/s; about eight instructions per element keep the arithmetic below that
+// (a fully rounded division each took 104 us).
 template <class E, int V, int G, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void quantise_kernel(QuantArgs a) {
   __shared__ uint32_t s_max[TOK_T / 64];

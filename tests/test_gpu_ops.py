@@ -576,6 +576,19 @@ def test_offsets_beyond_32_bits(env):
     assert bool(((out.double() - ref).abs() <= tol * 2 + 2.0 ** -8 * ref.abs()).all())
 
 
+@pytest.mark.parametrize("stride", [(1 << 22) - 16, 1 << 22, (1 << 22) + 5])
+def test_product_wide_strides(env, stride):
+    """Strides on both sides of what a tile's 32-bit offsets serve."""
+    torch = env[0]
+    g = _gen(torch, 41)
+    M, N, K = 90, 70, 96
+    a, w = (torch.empty(n, stride, dtype=torch.int8, device="cuda")[:, :K] for n in (M, N))
+    a.copy_(_codes(torch, g, M, K))
+    w.copy_(_codes(torch, g, N, K))
+    a_scale, w_scale = _scales(torch, g, M, N)
+    _check_product(env, a, a_scale, w, w_scale, N, 1, None, False, "fp32")
+
+
 # ------------------------------------------------------------------ together
 
 
