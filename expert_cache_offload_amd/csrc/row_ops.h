@@ -204,7 +204,7 @@ __device__ __forceinline__ void store_codes(int8_t* p, const Codes<E, V>& c) {
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
   return v;

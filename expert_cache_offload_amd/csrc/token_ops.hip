@@ -493,8 +493,9 @@ struct CombineGradArgs {
   float* dw;  // may be null
 };
 
-// A wave per assignment: drows[p] = w dy, dw = <dy, rows[p]> (fp32 products, per-lane partial
-// sums joined by shuffles in a fixed order), four chunks of each row in flight.  The waves of a
+// A wave per assignment: drows[p] = w dy, dw = <dy, rows[p]> (fp32 within a chunk, 64 bits over
+// the chunks and lanes, where a long sum may cancel; joined by shuffles in a fixed order), four
+// chunks of each row in flight.  The waves of a
 // token read its dy row together: of 16384 tokens of 8 rows of 2048 bf16 1.22 GB move for 1.14,
 // in 205 us.
 template <class E, int V, bool STREAM>
@@ -513,7 +514,7 @@ __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) 
   const E* r = (const E*)a.rows + (int64_t)p * a.rs;
   E* dr = (E*)a.drows + (int64_t)p * a.drs;
   const int nc = chunk_count<V>(a.H);
-  float sum = 0.f;
+  double sum = 0.0;
   for (int c0 = lane; c0 < nc; c0 += 64 * kHeld) {
     Chunk<E, V> g[kHeld], v[kHeld];
 #pragma unroll
@@ -537,17 +538,19 @@ __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) 
       }
       if (a.dw) {
         const int twice = c * V - at;  // elements that the chunk before has added up
+        float part = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float f = fmaf(to_f32(g[h].e[i]), to_f32(v[h].e[i]), sum);
-          sum = i >= twice ? f : sum;
+          const float f = fmaf(to_f32(g[h].e[i]), to_f32(v[h].e[i]), part);
+          part = i >= twice ? f : part;
         }
+        sum += part;
       }
     }
   }
   if (a.dw) {
     sum = wave_sum(sum);
-    if (lane == 0) a.dw[at] = sum;
+    if (lane == 0) a.dw[at] = (float)sum;
   }
 }
 
