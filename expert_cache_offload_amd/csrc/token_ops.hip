@@ -495,9 +495,8 @@ struct CombineGradArgs {
 
 // A wave per assignment: drows[p] = w dy, dw = <dy, rows[p]> (fp32 within a chunk, 64 bits over
 // the chunks and lanes, where a long sum may cancel; joined by shuffles in a fixed order), four
-// chunks of each row in flight.  The waves of a
-// token read its dy row together: of 16384 tokens of 8 rows of 2048 bf16 1.22 GB move for 1.14,
-// in 205 us.
+// chunks of each row in flight.  The waves of a token read its dy row together: of 16384 tokens of
+// 8 rows of 2048 bf16 1.22 GB move for 1.14, in 205 us.
 template <class E, int V, bool STREAM>
 __global__ __launch_bounds__(TOK_T) void combine_grad_kernel(CombineGradArgs a) {
   const int lane = threadIdx.x & 63;

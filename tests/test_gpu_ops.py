@@ -720,6 +720,36 @@ def test_expert_layer_captured_and_on_another_stream(env):
         assert _rel(b["y"], ref) <= LAYER_TOL
 
 
+def test_two_layers_at_once(env):
+    """Two layers of different sizes on two streams at the same time, each with its own buffers,
+    give what each gives alone, every time."""
+    torch, m, types, tid = env
+    layers, alone = [], []
+    for n, (T, k, E, H, I) in enumerate([(900, 4, 16, 512, 256), (37, 8, 30, 264, 72)]):
+        g = _gen(torch, 51 + n)
+        b = _layer_buffers(env, T, k, E, H, I,
+                           torch.randn(E, 2 * I, H, generator=g, device="cuda").double() * 0.05,
+                           torch.randn(E, H, I, generator=g, device="cuda").double() * 0.05)
+        b["ids"] = _ids(torch, g, T, k, E, 0.1)
+        b["weights"] = torch.softmax(torch.randn(T, k, generator=g, device="cuda"), 1)
+        b["x"] = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+        _expert_layer(env, b)
+        torch.cuda.synchronize()
+        layers.append(b)
+        alone.append(b["y"].clone())
+    streams = [torch.cuda.Stream() for _ in layers]
+    for _ in range(5):
+        for b in layers:
+            b["y"].fill_(3)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for b, s in zip(layers, streams):
+                _expert_layer(env, b, s.cuda_stream)
+        torch.cuda.synchronize()
+        for b, y in zip(layers, alone):
+            assert torch.equal(b["y"], y)
+
+
 def test_training_step_captured_beside_live_gradients(env):
     """Sort, a scaling per expert in torch, combine and every gradient, captured and replayed
     while an eager autograd graph over the same leaves is alive; gradients against autograd's of
