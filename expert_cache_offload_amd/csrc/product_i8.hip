@@ -321,7 +321,8 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
 // while the matrix units are 67% busy (a vendor library's plain 8-bit product: 2.08, zeros 3.26).
 // Stages of 64 bytes four deep, 128 x 128 per wave, four waves of 64 x 64 per SIMD and fixed
 // orders of reads and products were within 15% of this or slower.  131072 rows over 128 experts x
-// 1536 channels x 2048, SwiGLU: 437 us, 1.89 POP/s, of which the epilogues are about 45.
+// 1536 channels x 2048, SwiGLU: 437 to 460 us by the box, 1.8 to 1.9 POP/s, of which the
+// epilogues are about 45.
 constexpr int LK = 128;
 
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, const int8_t* base) {
