@@ -644,7 +644,7 @@ void launch_tile(const ProdArgs& a, hipStream_t s) {
   const int64_t mt = a.M / BM + (a.offsets ? std::min(a.groups, a.M) : 1);
   const int64_t tiles = mt * ((a.N + BN - 1) / BN);
   const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, 256 * PER_CU);
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(LT), lds, s, a);
+  launch_kernel(kernel, dim3(grid), dim3(LT), lds, s, a);
 }
 
 // The tile shapes, and what the choice among them goes by: microseconds of one round of KS
@@ -694,10 +694,10 @@ void launch_product(const ProdArgs& a, hipStream_t s) {
   if (a.M <= 16 || (a.M <= 64 && (a.offsets || !aligned))) {
     const int nf = (a.N + FN - 1) / FN;
     if (a.offsets || a.M <= 16)
-      hipLaunchKernelGGL((product_few_kernel<E, SWIGLU, 1>), dim3(nf, a.offsets ? a.M : 1),
-                         dim3(FT), 0, s, a);
+      launch_kernel(product_few_kernel<E, SWIGLU, 1>, dim3(nf, a.offsets ? a.M : 1), dim3(FT), 0,
+                    s, a);
     else
-      hipLaunchKernelGGL((product_few_kernel<E, SWIGLU, 4>), dim3(nf), dim3(FT), 0, s, a);
+      launch_kernel(product_few_kernel<E, SWIGLU, 4>, dim3(nf), dim3(FT), 0, s, a);
     return;
   }
   int best = aligned ? 0 : 2;  // the two largest shapes have no registers for the other path

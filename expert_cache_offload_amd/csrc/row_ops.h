@@ -273,6 +273,14 @@ inline bool on_current_device(const void* p) {
   return at.device == dev;
 }
 
+// A plain launch without the call configuration that the triple-bracket form pushes and pops (0.2 us
+// of the host's 3.1 per launch).
+template <class... P>
+inline void launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                          P... args) {
+  void* p[] = {(void*)&args...};
+  (void)hipLaunchKernel((const void*)kernel, grid, block, p, lds, s);
+}
 inline moe_status launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP; }
 
 }  // namespace moe

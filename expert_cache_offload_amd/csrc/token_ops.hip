@@ -599,13 +599,12 @@ void launch_sort_by(SortArgs& a, hipStream_t s) {
   const int nc = a.x ? chunk_count<V>(a.H) : 0;
   if (a.N <= kSmallIds) {
     const int slices = I8 ? 1 : std::max(1, std::min(64, (nc + TOK_T - 1) / TOK_T));
-    hipLaunchKernelGGL((sort_small_kernel<E, V, I8>), dim3(a.T + 1, slices), dim3(TOK_T), 0, s,
-                       a);
+    launch_kernel(sort_small_kernel<E, V, I8>, dim3(a.T + 1, slices), dim3(TOK_T), 0, s, a);
     return;
   }
-  hipLaunchKernelGGL(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
+  launch_kernel(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
   const bool self = a.nblk <= kSelfChunks;
-  if (!self) hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
+  if (!self) launch_kernel(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
   // a wave per token, unless there are too few tokens for that to fill the chip, or rows of codes
   // that a wave cannot hold; 16 tokens per workgroup amortise its counting, fewer fill the chip
   // (8 rows of 2048 bf16 per token: 4096 tokens 36 us with 4, 41 with 4 and whole workgroups per
@@ -620,8 +619,8 @@ void launch_sort_by(SortArgs& a, hipStream_t s) {
                              : stream ? sort_move_kernel<E, V, I8, false, true, false>
                                       : sort_move_kernel<E, V, I8, false, false, false>;
   const int subs = (a.tok_blk + sub - 1) / sub;
-  hipLaunchKernelGGL(kernel, dim3(a.nblk * subs), dim3(TOK_T), (size_t)kChunkWaves * a.E * 2, s, a,
-                     sub, subs);
+  launch_kernel(kernel, dim3(a.nblk * subs), dim3(TOK_T), (size_t)kChunkWaves * a.E * 2, s, a, sub,
+                subs);
 }
 
 // Rows shorter than a chunk go element by element, in all the launches.
@@ -647,7 +646,7 @@ void launch_combine_by(CombineArgs& a, hipStream_t s) {
                           : uni ? stream ? combine_kernel<E, V, false, true, true>
                                          : combine_kernel<E, V, false, true, false>
                                 : combine_kernel<E, V, false, false, false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(TOK_T), 0, s, a);
+  launch_kernel(kernel, grid, dim3(TOK_T), 0, s, a);
 }
 template <class E>
 void launch_combine(CombineArgs& a, hipStream_t s) {
@@ -660,8 +659,8 @@ void launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
   const auto kernel = a.H < kChunk<E> ? combine_grad_kernel<E, 1, false>
                       : stream        ? combine_grad_kernel<E, kChunk<E>, true>
                                       : combine_grad_kernel<E, kChunk<E>, false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T * a.k + TOK_T / 64 - 1) / (TOK_T / 64))),
-                     dim3(TOK_T), 0, s, a);
+  launch_kernel(kernel, dim3((unsigned)((a.T * a.k + TOK_T / 64 - 1) / (TOK_T / 64))), dim3(TOK_T),
+                0, s, a);
 }
 
 template <class E, int V, int G>
@@ -669,8 +668,7 @@ void launch_quantise_by(const QuantArgs& a, hipStream_t s) {
   constexpr int rows = TOK_T / G;
   const bool stream = (int64_t)a.M * a.K * (int)sizeof(E) > kStreamBytes;
   const auto kernel = stream ? quantise_kernel<E, V, G, true> : quantise_kernel<E, V, G, false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(((int64_t)a.M + rows - 1) / rows)), dim3(TOK_T), 0,
-                     s, a);
+  launch_kernel(kernel, dim3((unsigned)(((int64_t)a.M + rows - 1) / rows)), dim3(TOK_T), 0, s, a);
 }
 
 // As few lanes per row as hold it in kHeld chunks each.
