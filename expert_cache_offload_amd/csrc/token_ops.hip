@@ -24,7 +24,8 @@ constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
 constexpr int kChunkIds = 1024;     // assignments of a counted chunk (whole tokens)
 constexpr int kChunkWaves = kChunkIds / 64;
-constexpr int kSubTokens = 16;      // most tokens a workgroup of the move kernel sorts and moves
+constexpr int kSubTokens = 16;      // tokens a workgroup of the move kernel sorts and moves,
+constexpr int kSubIds = 256;        // and the most assignments
 constexpr int kSelfChunks = 16;     // most chunks whose counts the move kernel adds up itself
 constexpr int kMaxT = 1 << 20;
 constexpr int kMaxRows = (1 << 24) - 1;  // a workgroup each stays a launch's size
@@ -34,7 +35,8 @@ constexpr int kMaxRows = (1 << 24) - 1;  // a workgroup each stays a launch's si
 // of 768 quantised 54.7 -> 52.0; a gradient over 34 MB, which stays in the 256 MB cache, got slower
 // so, 13.7 -> 15.4 us).
 constexpr int64_t kStreamBytes = 128 << 20;
-constexpr int SCAN_T = 1024;
+constexpr int kScanExperts = 16, kScanSegs = 64;  // of a workgroup of the scan
+constexpr int SCAN_T = kScanExperts * kScanSegs;
 constexpr int kScanHeld = 16;
 
 struct SortArgs {
@@ -49,7 +51,8 @@ struct SortArgs {
   void* rows;
   int64_t rs;
   float* row_scale;
-  int* base;    // [nblk][E] counts of each chunk, then the first place of each (chunk, expert)
+  int* base;    // [nblk][E] counts of each chunk, or those of the chunks before it
+  int* total;   // [E] counts of all chunks
   int tok_blk;  // tokens of a chunk
   int nblk;
 };
@@ -269,58 +272,54 @@ __global__ __launch_bounds__(TOK_T) void sort_count_kernel(SortArgs a) {
   for (int e = threadIdx.x; e < a.E; e += TOK_T) a.base[(int64_t)b * a.E + e] = s_hist[e];
 }
 
-// Second, where there are more than kSelfChunks chunks: one workgroup turns the counts into first
-// places.  Thread (g, e) adds up a segment g of the chunks of expert e, the segments and then the
-// experts are scanned, and the running place of each chunk is written over its count.  128
-// chunks of 128 experts: 4.8 us, two memory latencies and the launch.
+// Second, where there are more than kSelfChunks chunks: a workgroup takes 16 experts and turns the
+// counts of each chunk into those of the chunks before it.  Thread (g, e) adds up segment g of the
+// chunks of expert e, a wave per expert scans the segments, and the running count is written
+// over each chunk's.  128 chunks of 128 experts 4.8 us, 1024 of 1024 6.2 (one workgroup for all
+// experts took 412).
 __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
-  __shared__ int s_seg[SCAN_T];
-  __shared__ int s_total[kMaxExperts];
-  __shared__ int s_off[kMaxExperts + 1];
-  __shared__ int s_wave[SCAN_T / 64];
-  int ep = 1;  // experts rounded up to a power of two
-  while (ep < a.E) ep <<= 1;
-  const int nseg = SCAN_T / ep, e = threadIdx.x & (ep - 1), g = threadIdx.x / ep;
-  const int per = (a.nblk + nseg - 1) / nseg;
-  const int b0 = min(a.nblk, g * per), b1 = min(a.nblk, b0 + per);
+  __shared__ int s_seg[kScanExperts][kScanSegs + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int el = tid % kScanExperts, g = tid / kScanExperts;
+  const int e = blockIdx.x * kScanExperts + el;
+  const int per = (a.nblk + kScanSegs - 1) / kScanSegs;
+  const int b0 = min(a.nblk, g * per), n = e < a.E ? min(a.nblk, b0 + per) - b0 : 0;
+  int* const base = a.base + (int64_t)b0 * a.E + e;
   // the counts of up to kScanHeld chunks stay in registers between the passes
   int held[kScanHeld];
   int sum = 0;
-  const int* base = a.base + (int64_t)b0 * a.E + e;
 #pragma unroll
-  for (int i = 0; i < kScanHeld; ++i) held[i] = e < a.E && b0 + i < b1 ? base[(int64_t)i * a.E] : 0;
+  for (int i = 0; i < kScanHeld; ++i) held[i] = i < n ? base[(int64_t)i * a.E] : 0;
 #pragma unroll
   for (int i = 0; i < kScanHeld; ++i) sum += held[i];
-  if (e < a.E)
-    for (int i = kScanHeld; b0 + i < b1; ++i) sum += base[(int64_t)i * a.E];
-  s_seg[threadIdx.x] = sum;
+#pragma unroll 8
+  for (int i = kScanHeld; i < n; ++i) sum += base[(int64_t)i * a.E];
+  s_seg[el][g] = sum;
   __syncthreads();
-  if (g == 0 && e < a.E) {
-    int run = 0;
-    for (int s = 0; s < nseg; ++s) {
-      const int v = s_seg[s * ep + e];
-      s_seg[s * ep + e] = run;
-      run += v;
+  {
+    static_assert(kScanSegs == 64 && SCAN_T / 64 == kScanExperts);
+    const int v = s_seg[wave][lane];
+    int inc = v;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int o = __shfl_up(inc, s);
+      if (lane >= s) inc += o;
     }
-    s_total[e] = run;
+    s_seg[wave][lane] = inc - v;
+    const int mine = blockIdx.x * kScanExperts + wave;
+    if (lane == 63 && mine < a.E) a.total[mine] = inc;
   }
   __syncthreads();
-  prefix_counts(s_total, a.E, s_off, s_wave, threadIdx.x, SCAN_T);
-  __syncthreads();
-  for (int i = threadIdx.x; i <= a.E; i += SCAN_T) a.offsets[i] = s_off[i];
-  if (e < a.E) {
-    int run = s_off[e] + s_seg[threadIdx.x];
-    int* out = a.base + (int64_t)b0 * a.E + e;
+  int run = s_seg[el][g];
 #pragma unroll
-    for (int i = 0; i < kScanHeld; ++i) {
-      if (b0 + i < b1) out[(int64_t)i * a.E] = run;
-      run += held[i];
-    }
-    for (int i = kScanHeld; b0 + i < b1; ++i) {
-      const int v = out[(int64_t)i * a.E];
-      out[(int64_t)i * a.E] = run;
-      run += v;
-    }
+  for (int i = 0; i < kScanHeld; ++i) {
+    if (i < n) base[(int64_t)i * a.E] = run;
+    run += held[i];
+  }
+  for (int i = kScanHeld; i < n; ++i) {
+    const int v = base[(int64_t)i * a.E];
+    base[(int64_t)i * a.E] = run;
+    run += v;
   }
 }
 
@@ -334,10 +333,10 @@ __global__ __launch_bounds__(SCAN_T) void sort_scan_kernel(SortArgs a) {
 template <class E, int V, bool I8, bool WIDE, bool STREAM, bool SELF>
 __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, int subs) {
   extern __shared__ __align__(16) uint16_t s_cnt[];  // [kChunkWaves][E]
-  __shared__ int s_id[kSubTokens * kMaxTopK], s_rank[kSubTokens * kMaxTopK];
-  __shared__ int s_place[kSubTokens * kMaxTopK];
+  static_assert(kSubTokens * kMaxTopK <= kSubIds && kSubIds <= TOK_T);
+  __shared__ int s_id[kSubIds], s_rank[kSubIds], s_place[kSubIds];
   __shared__ uint32_t s_max[2][TOK_T / 64];
-  __shared__ int s_base[SELF ? kMaxExperts + 1 : 1], s_total[SELF ? kMaxExperts : 1];
+  __shared__ int s_first[kMaxExperts + 1], s_total[kMaxExperts];
   __shared__ int s_wave[TOK_T / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x / subs;
@@ -345,13 +344,13 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, i
   const int t0 = t_blk + (blockIdx.x % subs) * sub;
   const int t1 = min(min(a.T, t_blk + a.tok_blk), t0 + sub);
   if (t0 >= t1) return;
-  if constexpr (SELF) {
-    int before[kMaxExperts / TOK_T];  // in the chunks before this one
+  int before[kMaxExperts / TOK_T];  // SELF: in the chunks before this one
 #pragma unroll
-    for (int q = 0; q < kMaxExperts / TOK_T; ++q) {
-      const int e = tid + q * TOK_T;
-      before[q] = 0;
-      if (e >= a.E) continue;
+  for (int q = 0; q < kMaxExperts / TOK_T; ++q) {
+    const int e = tid + q * TOK_T;
+    before[q] = 0;
+    if (e >= a.E) continue;
+    if constexpr (SELF) {
       int cnt[kSelfChunks], sum = 0;
 #pragma unroll
       for (int c = 0; c < kSelfChunks; ++c) cnt[c] = c < a.nblk ? a.base[c * a.E + e] : 0;
@@ -361,16 +360,20 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, i
         sum += cnt[c];
       }
       s_total[e] = sum;
+    } else {
+      s_total[e] = a.total[e];
     }
-    __syncthreads();
-    prefix_counts(s_total, a.E, s_base, s_wave, tid, TOK_T);
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int e = tid; e <= a.E; e += TOK_T) a.offsets[e] = s_base[e];
+  }
+  __syncthreads();
+  prefix_counts(s_total, a.E, s_first, s_wave, tid, TOK_T);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= a.E; e += TOK_T) a.offsets[e] = s_first[e];
+  if constexpr (SELF) {
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < kMaxExperts / TOK_T; ++q)
-      if (tid + q * TOK_T < a.E) s_base[tid + q * TOK_T] += before[q];
+      if (tid + q * TOK_T < a.E) s_first[tid + q * TOK_T] += before[q];
   }
   const int first = t_blk * a.k, own0 = (t0 - t_blk) * a.k, own1 = (t1 - t_blk) * a.k;
   const int waves = (own1 + 63) / 64;
@@ -397,7 +400,8 @@ __global__ __launch_bounds__(TOK_T) void sort_move_kernel(SortArgs a, int sub, i
     const int i = own0 + tid, id = s_id[tid];
     int p = -1;
     if (id >= 0) {
-      p = s_rank[tid] + (SELF ? s_base[id] : a.base[(int64_t)b * a.E + id]);
+      p = s_rank[tid] + s_first[id];
+      if constexpr (!SELF) p += a.base[(int64_t)b * a.E + id];
       for (int it = 0; it < i / 64; ++it) p += s_cnt[it * a.E + id];
       if (a.order) a.order[p] = first + i;
     }
@@ -604,13 +608,17 @@ void launch_sort_by(SortArgs& a, hipStream_t s) {
   }
   launch_kernel(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
   const bool self = a.nblk <= kSelfChunks;
-  if (!self) launch_kernel(sort_scan_kernel, dim3(1), dim3(SCAN_T), 0, s, a);
+  if (!self)
+    launch_kernel(sort_scan_kernel, dim3((a.E + kScanExperts - 1) / kScanExperts), dim3(SCAN_T), 0, s,
+                  a);
   // a wave per token, unless there are too few tokens for that to fill the chip, or rows of codes
   // that a wave cannot hold; 16 tokens per workgroup amortise its counting, fewer fill the chip
   // (8 rows of 2048 bf16 per token: 4096 tokens 36 us with 4, 41 with 4 and whole workgroups per
   // token; 1024 tokens of 8 rows of 4096, quantised: 18 us with one per workgroup, 64 with 16)
   const bool wide = a.T < 2048 || (I8 && nc > 64 * kHeld);
-  const int sub = a.T < 2048 ? 1 : a.T < 8192 ? 4 : kSubTokens;
+  int sub = a.T < 2048 ? 1 : a.T < 8192 ? 4 : kSubTokens;
+  // and where few choices make for few ids per token, as many as leave 1024 workgroups
+  if (a.T > 1024 * kSubTokens) sub = std::max(sub, std::min(a.T / 1024, kSubIds / 2 / a.k));
   const bool stream = (int64_t)a.N * a.H * (I8 ? 1 : (int)sizeof(E)) > kStreamBytes;
   const auto kernel = self ? wide ? sort_move_kernel<E, V, I8, true, false, true>
                                   : sort_move_kernel<E, V, I8, false, false, true>
@@ -714,7 +722,7 @@ extern "C" {
 
 size_t moe_sort_workspace_bytes(int32_t T, int32_t top_k, int32_t experts) {
   if (!tokens_ok(T, top_k, experts) || T * top_k <= kSmallIds) return 0;
-  return sizeof(int) * (size_t)block_count(T, top_k) * (size_t)experts;
+  return sizeof(int) * (size_t)(block_count(T, top_k) + 1) * (size_t)experts;
 }
 
 moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, int32_t experts,
@@ -738,9 +746,11 @@ moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, in
   if (need && (!workspace || !aligned4(workspace))) return MOE_E_INVALID;
   if (workspace_bytes < need) return MOE_E_SCRATCH;
   if (!on_current_device(offsets)) return MOE_E_INVALID;
-  SortArgs a{topk_idx, T,       top_k, experts, T * top_k, x,
-             x_stride, hidden,  offsets, order, place,     rows,
-             rows_stride, row_scale, (int*)workspace, block_tokens(top_k), block_count(T, top_k)};
+  const int nblk = block_count(T, top_k);
+  int* const base = (int*)workspace;
+  SortArgs a{topk_idx, T,     top_k, experts, T * top_k, x,           x_stride,  hidden,
+             offsets,  order, place, rows,    rows_stride, row_scale, base,
+             need ? base + (size_t)nblk * experts : nullptr, block_tokens(top_k), nblk};
   const hipStream_t s = (hipStream_t)stream;
   const int type = x ? x_type : MOE_T_FP32;
   if (type == MOE_T_BF16)
