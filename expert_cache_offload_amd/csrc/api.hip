@@ -1165,7 +1165,8 @@ const char* moe_status_string(moe_status s) {
     case MOE_E_NOMEM: return "pinned host memory unavailable";
     case MOE_E_HYBRID: return "hybrid decode: the host did not answer a step in time";
     case MOE_E_SCRATCH:
-      return "workspace larger than the library's static workspace (16 MiB per device)";
+      return "workspace larger than the library's static workspace (16 MiB per device), "
+             "or smaller than the call needs";
     default: return "unknown status";
   }
 }

@@ -73,7 +73,8 @@ typedef int32_t moe_status;
 #define MOE_E_HIP (-4)      /* a HIP runtime call failed; see moe_last_hip_error */
 #define MOE_E_NOMEM (-5)    /* pinned host allocation failed */
 #define MOE_E_HYBRID (-6)   /* hybrid decode: the host did not answer a step within ~2 s */
-#define MOE_E_SCRATCH (-7)  /* workspace above the static workspace (moe_cache_create_static) */
+#define MOE_E_SCRATCH (-7)  /* workspace above the static workspace (moe_cache_create_static),
+                            * or below what the call needs (moe_sort_tokens) */
 
 #define MOE_FMT_BF16 0
 #define MOE_FMT_FP8_E4M3_K128 1
