@@ -698,11 +698,12 @@ void launch_quantise(const QuantArgs& a, hipStream_t s) {
 
 moe_status combine(const void* rows, int64_t rs, int n_rows, int type, const int* place,
                    const float* w, int T, int k, int H, void* out, int64_t os, hipStream_t s) {
-  if (!float_type(type) || !tokens_ok(T, k, 1) || H < 1 || H > kMaxCols || n_rows < 0 || !place ||
-      !aligned4(place) || !aligned4(w) || !rows_ok(out, os, H, type) ||
+  if (!float_type(type) || !tokens_ok(T, k, 1) || H < 1 || H > kMaxCols || n_rows < 0)
+    return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;  // before the pointers: empty buffers have none
+  if (!place || !aligned4(place) || !aligned4(w) || !rows_ok(out, os, H, type) ||
       (n_rows > 0 && !rows_ok(rows, rs, H, type)) || !on_current_device(out))
     return MOE_E_INVALID;
-  if (T == 0) return MOE_OK;
   CombineArgs a{rows, rs, n_rows, place, w, T, k, H, out, os, 0};
   if (type == MOE_T_BF16)
     launch_combine<bf16_t>(a, s);
@@ -734,11 +735,14 @@ moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, in
     return MOE_E_INVALID;
   if (T > 0 && (!topk_idx || !place || !aligned4(topk_idx) || !aligned4(place)))
     return MOE_E_INVALID;
+  const bool i8 = (x || rows) && rows_type == MOE_T_I8;
+  if ((x || rows) && (!float_type(x_type) || (rows_type != x_type && !i8) || hidden < 1 ||
+                      hidden > kMaxCols))
+    return MOE_E_INVALID;
+  if (T == 0) x = rows = nullptr;  // either may be an empty buffer, which has no address
   if ((x == nullptr) != (rows == nullptr)) return MOE_E_INVALID;
-  const bool i8 = x && rows_type == MOE_T_I8;
   if (x) {
-    if (!float_type(x_type) || (rows_type != x_type && !i8) || hidden < 1 || hidden > kMaxCols ||
-        !rows_ok(x, x_stride, hidden, x_type) || !rows_ok(rows, rows_stride, hidden, rows_type))
+    if (!rows_ok(x, x_stride, hidden, x_type) || !rows_ok(rows, rows_stride, hidden, rows_type))
       return MOE_E_INVALID;
     if (i8 && (!row_scale || !aligned4(row_scale))) return MOE_E_INVALID;
   }
@@ -773,7 +777,7 @@ moe_status moe_combine_tokens(const void* rows, int64_t rows_stride, int32_t n_r
                               const int32_t* place, const float* weights, int32_t T,
                               int32_t top_k, int32_t hidden, void* out, int64_t out_stride,
                               void* stream) {
-  if (!weights) return MOE_E_INVALID;
+  if (!weights && T != 0) return MOE_E_INVALID;
   return combine(rows, rows_stride, n_rows, type, place, weights, T, top_k, hidden, out,
                  out_stride, (hipStream_t)stream);
 }
@@ -783,14 +787,16 @@ moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const 
                                    const int32_t* place, const float* weights, int32_t T,
                                    int32_t top_k, int32_t hidden, void* drows,
                                    int64_t drows_stride, float* dweights, void* stream) {
-  if (!float_type(type) || !tokens_ok(T, top_k, 1) || hidden < 1 || hidden > kMaxCols ||
-      n_rows < 0 || !place || !weights || !aligned4(place) || !aligned4(weights) ||
-      !aligned4(dweights) || (!drows && !dweights) || !rows_ok(dout, dout_stride, hidden, type) ||
+  if (!float_type(type) || !tokens_ok(T, top_k, 1) || hidden < 1 || hidden > kMaxCols || n_rows < 0)
+    return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;  // before the pointers: empty buffers have none
+  if (!place || !weights || !aligned4(place) || !aligned4(weights) || !aligned4(dweights) ||
+      (!drows && !dweights && n_rows > 0) || !rows_ok(dout, dout_stride, hidden, type) ||
       (drows && !rows_ok(drows, drows_stride, hidden, type)) ||
       (dweights && n_rows > 0 && !rows_ok(rows, rows_stride, hidden, type)) ||
       !on_current_device(dout))
     return MOE_E_INVALID;
-  if (T == 0) return MOE_OK;
+  if (!drows && !dweights) return MOE_OK;  // no rows to give a gradient to
   CombineGradArgs a{dout, dout_stride, rows, rows_stride, n_rows, place, weights, T,
                     top_k, hidden, drows, drows_stride, dweights};
   const hipStream_t s = (hipStream_t)stream;
@@ -806,11 +812,11 @@ moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const 
 moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
                              int8_t* codes, int64_t codes_stride, float* scale,
                              const int32_t* rows_end, void* stream) {
-  if (!float_type(type) || M < 0 || M > kMaxRows || K < 1 || K > kMaxCols || !rows_ok(x, x_stride, K, type) ||
-      !rows_ok(codes, codes_stride, K, MOE_T_I8) || !scale || !aligned4(scale) ||
-      !aligned4(rows_end) || !on_current_device(codes))
+  if (!float_type(type) || M < 0 || M > kMaxRows || K < 1 || K > kMaxCols) return MOE_E_INVALID;
+  if (M == 0) return MOE_OK;  // before the pointers: empty buffers have none
+  if (!rows_ok(x, x_stride, K, type) || !rows_ok(codes, codes_stride, K, MOE_T_I8) || !scale ||
+      !aligned4(scale) || !aligned4(rows_end) || !on_current_device(codes))
     return MOE_E_INVALID;
-  if (M == 0) return MOE_OK;
   QuantArgs a{x, x_stride, M, K, codes, codes_stride, scale, rows_end};
   const hipStream_t s = (hipStream_t)stream;
   if (type == MOE_T_BF16)

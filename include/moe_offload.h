@@ -400,6 +400,8 @@ moe_status moe_probe_copy(const void* src, void* dst, uint64_t bytes, int32_t re
  *    overlap inputs or each other (not checked); a buffer is free for other use once the
  *    stream has passed the call;
  *  - every argument check is made before anything is enqueued; MOE_E_HIP when a launch fails;
+ *  - with T = 0 or M = 0 sizes and types are checked, buffers that are empty then are not looked
+ *    at and may be NULL (of the sort's outputs offsets is written);
  *  - results do not depend on timing: the same inputs give the same bits. */
 #define MOE_T_BF16 0
 #define MOE_T_FP16 1
@@ -446,8 +448,8 @@ moe_status moe_combine_tokens(const void* rows, int64_t rows_stride, int32_t n_r
 
 /* Gradients of moe_combine_tokens: drows[place[t][j]] = weights[t][j] * dout[t] (rows that no
  * assignment has are left as they were) and dweights[t][j] = <dout[t], rows[place[t][j]]>, 0
- * where dropped.  drows or dweights may be NULL, rows too where dweights is.  The places in
- * [0, n_rows) have to be distinct, as moe_sort_tokens writes them. */
+ * where dropped.  drows or dweights may be NULL (both where n_rows is 0), rows too where dweights
+ * is.  The places in [0, n_rows) have to be distinct, as moe_sort_tokens writes them. */
 moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const void* rows,
                                    int64_t rows_stride, int32_t n_rows, int32_t type,
                                    const int32_t* place, const float* weights, int32_t T,

@@ -114,3 +114,38 @@ def test_no_rows_is_no_work():
     m = _m()
     m.moe_combine_tokens(**{**COMBINE, "T": 0})
     m.moe_product_i8(**{**PRODUCT, "M": 0})
+
+
+def test_no_rows_with_empty_buffers():
+    """An empty buffer has no address: calls of no tokens or no rows take null pointers for every
+    buffer that is empty then (a rank of an expert-parallel layer that was sent no token)."""
+    m = _m()
+    none = dict(rows=None, place=None, weights=None, out=None, n_rows=0, T=0)
+    m.moe_combine_tokens(**{**COMBINE, **none})
+    m.moe_combine_tokens(**{**COMBINE, **none, "rows": P, "n_rows": 5})
+    m.moe_sort_tokens_grad(None, 64, 0, BF16, None, 0, 2, 64, None, 64)
+    for drows, dweights in ((P, P), (P, None), (None, P), (None, None)):
+        m.moe_combine_tokens_grad(None, 64, None, 64, 0, FP32, None, None, 0, 2, 64, drows, 64,
+                                  dweights)
+    m.moe_quantise_rows(None, 64, FP16, 0, 64, None, 64, None)
+    m.moe_product_i8(None, 64, None, 0, 64, P, 64, P, 32, 4, P, 0, None, 32, FP32)
+    # tokens of which none was placed: no row to write a gradient to
+    m.moe_combine_tokens_grad(P, 64, None, 64, 0, FP32, P, P, 16, 2, 64, None, 64, None)
+
+
+@pytest.mark.parametrize("name,args", [
+    ("moe_combine_tokens", (None, 64, 0, I8, None, None, 0, 2, 64, None, 64)),
+    ("moe_combine_tokens", (None, 64, -1, BF16, None, None, 0, 2, 64, None, 64)),
+    ("moe_combine_tokens", (None, 64, 0, BF16, None, None, 0, 17, 64, None, 64)),
+    ("moe_sort_tokens_grad", (None, 64, 0, BF16, None, 0, 2, 0, None, 64)),
+    ("moe_combine_tokens_grad", (None, 64, None, 64, 0, I8, None, None, 0, 2, 64, None, 64, None)),
+    ("moe_quantise_rows", (None, 64, I8, 0, 64, None, 64, None)),
+    ("moe_quantise_rows", (None, 64, BF16, 0, 0, None, 64, None)),
+    ("moe_product_i8", (None, 64, None, 0, 0, P, 64, P, 32, 4, P, 0, None, 32, FP32)),
+    ("moe_sort_tokens", (None, 0, 2, 8, None, None, None)),
+    ("moe_sort_tokens", (None, 0, 2, 8, P, None, None, P, 64, 64, I8, None, 64, I8))])
+def test_no_rows_still_checks_sizes_and_types(name, args):
+    m = _m()
+    with pytest.raises(m.MoeError) as e:
+        getattr(m, name)(*args)
+    assert e.value.status == m.MOE_E_INVALID
