@@ -634,7 +634,7 @@ void product_tile_kernel(ProdArgs a) {
 }
 
 template <class E, bool SWIGLU, bool ANY, int WM, int WN, int MI, int NI, int KS, int PER_CU>
-void launch_tile(const ProdArgs& a, hipStream_t s) {
+hipError_t launch_tile(const ProdArgs& a, hipStream_t s) {
   constexpr int BM = 32 * WM * MI, BN = 32 * WN * NI, LT = 64 * WM * WN * KS;
   const int lds = 2 * KS * (BM + BN) * LK + 12 * a.groups + 4;
   const auto kernel = product_tile_kernel<E, SWIGLU, ANY, WM, WN, MI, NI, KS, PER_CU>;
@@ -644,7 +644,7 @@ void launch_tile(const ProdArgs& a, hipStream_t s) {
   const int64_t mt = a.M / BM + (a.offsets ? std::min(a.groups, a.M) : 1);
   const int64_t tiles = mt * ((a.N + BN - 1) / BN);
   const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, 256 * PER_CU);
-  launch_kernel(kernel, dim3(grid), dim3(LT), lds, s, a);
+  return launch_kernel(kernel, dim3(grid), dim3(LT), lds, s, a);
 }
 
 // The tile shapes, and what the choice among them goes by: microseconds of one round of KS
@@ -684,7 +684,7 @@ float tile_cost(const TileShape& t, const ProdArgs& a) {
 }
 
 template <class E, bool SWIGLU>
-void launch_product(const ProdArgs& a, hipStream_t s) {
+hipError_t launch_product(const ProdArgs& a, hipStream_t s) {
   const bool aligned = !(((uintptr_t)a.a | (uintptr_t)a.w | (uintptr_t)a.as | (uintptr_t)a.ws |
                           (uintptr_t)a.K) & 15) &&
                        a.as < (1 << 22) && a.ws < (1 << 22);  // a tile's offsets: 31 bits
@@ -694,11 +694,9 @@ void launch_product(const ProdArgs& a, hipStream_t s) {
   if (a.M <= 16 || (a.M <= 64 && (a.offsets || !aligned))) {
     const int nf = (a.N + FN - 1) / FN;
     if (a.offsets || a.M <= 16)
-      launch_kernel(product_few_kernel<E, SWIGLU, 1>, dim3(nf, a.offsets ? a.M : 1), dim3(FT), 0,
-                    s, a);
-    else
-      launch_kernel(product_few_kernel<E, SWIGLU, 4>, dim3(nf), dim3(FT), 0, s, a);
-    return;
+      return launch_kernel(product_few_kernel<E, SWIGLU, 1>, dim3(nf, a.offsets ? a.M : 1), dim3(FT),
+                           0, s, a);
+    return launch_kernel(product_few_kernel<E, SWIGLU, 4>, dim3(nf), dim3(FT), 0, s, a);
   }
   int best = aligned ? 0 : 2;  // the two largest shapes have no registers for the other path
   for (int i = best + 1; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i)
@@ -745,10 +743,8 @@ extern "C" moe_status moe_product_i8(const int8_t* a, int64_t a_stride, const fl
              w_scale, N, groups, offsets, out, out_stride};
   const hipStream_t s = (hipStream_t)stream;
   if (out_type == MOE_T_BF16)
-    swiglu ? launch_product<bf16_t, true>(p, s) : launch_product<bf16_t, false>(p, s);
-  else if (out_type == MOE_T_FP16)
-    swiglu ? launch_product<fp16_t, true>(p, s) : launch_product<fp16_t, false>(p, s);
-  else
-    swiglu ? launch_product<float, true>(p, s) : launch_product<float, false>(p, s);
-  return launched();
+    return launched(swiglu ? launch_product<bf16_t, true>(p, s) : launch_product<bf16_t, false>(p, s));
+  if (out_type == MOE_T_FP16)
+    return launched(swiglu ? launch_product<fp16_t, true>(p, s) : launch_product<fp16_t, false>(p, s));
+  return launched(swiglu ? launch_product<float, true>(p, s) : launch_product<float, false>(p, s));
 }

@@ -274,13 +274,18 @@ inline bool on_current_device(const void* p) {
 }
 
 // A plain launch without the call configuration that the triple-bracket form pushes and pops (0.2 us
-// of the host's 3.1 per launch).
+// of the host's 3.1 per launch), and its own status: an error that an earlier call of the thread has
+// left behind is another's.
 template <class... P>
-inline void launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
-                          P... args) {
+inline hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds,
+                                hipStream_t s, P... args) {
   void* p[] = {(void*)&args...};
-  (void)hipLaunchKernel((const void*)kernel, grid, block, p, lds, s);
+  return hipLaunchKernel((const void*)kernel, grid, block, p, lds, s);
 }
-inline moe_status launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP; }
+inline moe_status launched(hipError_t e) {
+  if (e == hipSuccess) return MOE_OK;
+  (void)hipGetLastError();  // reported here
+  return MOE_E_HIP;
+}
 
 }  // namespace moe

@@ -599,18 +599,19 @@ int block_tokens(int k) { return kChunkIds / k; }
 int block_count(int T, int k) { return (T + block_tokens(k) - 1) / block_tokens(k); }
 
 template <class E, int V, bool I8>
-void launch_sort_by(SortArgs& a, hipStream_t s) {
+hipError_t launch_sort_by(SortArgs& a, hipStream_t s) {
   const int nc = a.x ? chunk_count<V>(a.H) : 0;
   if (a.N <= kSmallIds) {
     const int slices = I8 ? 1 : std::max(1, std::min(64, (nc + TOK_T - 1) / TOK_T));
-    launch_kernel(sort_small_kernel<E, V, I8>, dim3(a.T + 1, slices), dim3(TOK_T), 0, s, a);
-    return;
+    return launch_kernel(sort_small_kernel<E, V, I8>, dim3(a.T + 1, slices), dim3(TOK_T), 0, s, a);
   }
-  launch_kernel(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
+  // each reads what the one before leaves in the workspace, so none follows a failed one
+  hipError_t e = launch_kernel(sort_count_kernel, dim3(a.nblk), dim3(TOK_T), 0, s, a);
   const bool self = a.nblk <= kSelfChunks;
-  if (!self)
-    launch_kernel(sort_scan_kernel, dim3((a.E + kScanExperts - 1) / kScanExperts), dim3(SCAN_T), 0, s,
-                  a);
+  if (e == hipSuccess && !self)
+    e = launch_kernel(sort_scan_kernel, dim3((a.E + kScanExperts - 1) / kScanExperts), dim3(SCAN_T),
+                      0, s, a);
+  if (e != hipSuccess) return e;
   // a wave per token, unless there are too few tokens for that to fill the chip, or rows of codes
   // that a wave cannot hold; 16 tokens per workgroup amortise its counting, fewer fill the chip
   // (8 rows of 2048 bf16 per token: 4096 tokens 36 us with 4, 41 with 4 and whole workgroups per
@@ -627,19 +628,19 @@ void launch_sort_by(SortArgs& a, hipStream_t s) {
                              : stream ? sort_move_kernel<E, V, I8, false, true, false>
                                       : sort_move_kernel<E, V, I8, false, false, false>;
   const int subs = (a.tok_blk + sub - 1) / sub;
-  launch_kernel(kernel, dim3(a.nblk * subs), dim3(TOK_T), (size_t)kChunkWaves * a.E * 2, s, a, sub,
-                subs);
+  return launch_kernel(kernel, dim3(a.nblk * subs), dim3(TOK_T), (size_t)kChunkWaves * a.E * 2, s, a,
+                       sub, subs);
 }
 
 // Rows shorter than a chunk go element by element, in all the launches.
 template <class E, bool I8>
-void launch_sort(SortArgs& a, hipStream_t s) {
-  a.H >= kChunk<E> || !a.x ? launch_sort_by<E, kChunk<E>, I8>(a, s)
-                           : launch_sort_by<E, 1, I8>(a, s);
+hipError_t launch_sort(SortArgs& a, hipStream_t s) {
+  return a.H >= kChunk<E> || !a.x ? launch_sort_by<E, kChunk<E>, I8>(a, s)
+                                  : launch_sort_by<E, 1, I8>(a, s);
 }
 
 template <class E, int V>
-void launch_combine_by(CombineArgs& a, hipStream_t s) {
+hipError_t launch_combine_by(CombineArgs& a, hipStream_t s) {
   const int nc = chunk_count<V>(a.H);
   a.tpt_log = 0;
   while (a.tpt_log < 8 && (1 << a.tpt_log) < nc) ++a.tpt_log;
@@ -654,46 +655,42 @@ void launch_combine_by(CombineArgs& a, hipStream_t s) {
                           : uni ? stream ? combine_kernel<E, V, false, true, true>
                                          : combine_kernel<E, V, false, true, false>
                                 : combine_kernel<E, V, false, false, false>;
-  launch_kernel(kernel, grid, dim3(TOK_T), 0, s, a);
+  return launch_kernel(kernel, grid, dim3(TOK_T), 0, s, a);
 }
 template <class E>
-void launch_combine(CombineArgs& a, hipStream_t s) {
-  a.H >= kChunk<E> ? launch_combine_by<E, kChunk<E>>(a, s) : launch_combine_by<E, 1>(a, s);
+hipError_t launch_combine(CombineArgs& a, hipStream_t s) {
+  return a.H >= kChunk<E> ? launch_combine_by<E, kChunk<E>>(a, s) : launch_combine_by<E, 1>(a, s);
 }
 
 template <class E>
-void launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
+hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
   const bool stream = (int64_t)a.T * a.k * a.H * (int)sizeof(E) > kStreamBytes;
   const auto kernel = a.H < kChunk<E> ? combine_grad_kernel<E, 1, false>
                       : stream        ? combine_grad_kernel<E, kChunk<E>, true>
                                       : combine_grad_kernel<E, kChunk<E>, false>;
-  launch_kernel(kernel, dim3((unsigned)((a.T * a.k + TOK_T / 64 - 1) / (TOK_T / 64))), dim3(TOK_T),
-                0, s, a);
+  return launch_kernel(kernel, dim3((unsigned)((a.T * a.k + TOK_T / 64 - 1) / (TOK_T / 64))),
+                       dim3(TOK_T), 0, s, a);
 }
 
 template <class E, int V, int G>
-void launch_quantise_by(const QuantArgs& a, hipStream_t s) {
+hipError_t launch_quantise_by(const QuantArgs& a, hipStream_t s) {
   constexpr int rows = TOK_T / G;
   const bool stream = (int64_t)a.M * a.K * (int)sizeof(E) > kStreamBytes;
   const auto kernel = stream ? quantise_kernel<E, V, G, true> : quantise_kernel<E, V, G, false>;
-  launch_kernel(kernel, dim3((unsigned)(((int64_t)a.M + rows - 1) / rows)), dim3(TOK_T), 0, s, a);
+  return launch_kernel(kernel, dim3((unsigned)(((int64_t)a.M + rows - 1) / rows)), dim3(TOK_T), 0, s,
+                       a);
 }
 
 // As few lanes per row as hold it in kHeld chunks each.
 template <class E>
-void launch_quantise(const QuantArgs& a, hipStream_t s) {
+hipError_t launch_quantise(const QuantArgs& a, hipStream_t s) {
   constexpr int V = kChunk<E>;
   const int nc = chunk_count<V>(a.K);
-  if (a.K < V)
-    launch_quantise_by<E, 1, 16>(a, s);
-  else if (nc <= 16 * kHeld)
-    launch_quantise_by<E, V, 16>(a, s);
-  else if (nc <= 32 * kHeld)
-    launch_quantise_by<E, V, 32>(a, s);
-  else if (nc <= 64 * kHeld)
-    launch_quantise_by<E, V, 64>(a, s);
-  else
-    launch_quantise_by<E, V, 256>(a, s);
+  if (a.K < V) return launch_quantise_by<E, 1, 16>(a, s);
+  if (nc <= 16 * kHeld) return launch_quantise_by<E, V, 16>(a, s);
+  if (nc <= 32 * kHeld) return launch_quantise_by<E, V, 32>(a, s);
+  if (nc <= 64 * kHeld) return launch_quantise_by<E, V, 64>(a, s);
+  return launch_quantise_by<E, V, 256>(a, s);
 }
 
 moe_status combine(const void* rows, int64_t rs, int n_rows, int type, const int* place,
@@ -705,13 +702,9 @@ moe_status combine(const void* rows, int64_t rs, int n_rows, int type, const int
       (n_rows > 0 && !rows_ok(rows, rs, H, type)) || !on_current_device(out))
     return MOE_E_INVALID;
   CombineArgs a{rows, rs, n_rows, place, w, T, k, H, out, os, 0};
-  if (type == MOE_T_BF16)
-    launch_combine<bf16_t>(a, s);
-  else if (type == MOE_T_FP16)
-    launch_combine<fp16_t>(a, s);
-  else
-    launch_combine<float>(a, s);
-  return launched();
+  if (type == MOE_T_BF16) return launched(launch_combine<bf16_t>(a, s));
+  if (type == MOE_T_FP16) return launched(launch_combine<fp16_t>(a, s));
+  return launched(launch_combine<float>(a, s));
 }
 
 }  // namespace
@@ -758,12 +751,10 @@ moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t top_k, in
   const hipStream_t s = (hipStream_t)stream;
   const int type = x ? x_type : MOE_T_FP32;
   if (type == MOE_T_BF16)
-    i8 ? launch_sort<bf16_t, true>(a, s) : launch_sort<bf16_t, false>(a, s);
-  else if (type == MOE_T_FP16)
-    i8 ? launch_sort<fp16_t, true>(a, s) : launch_sort<fp16_t, false>(a, s);
-  else
-    i8 ? launch_sort<float, true>(a, s) : launch_sort<float, false>(a, s);
-  return launched();
+    return launched(i8 ? launch_sort<bf16_t, true>(a, s) : launch_sort<bf16_t, false>(a, s));
+  if (type == MOE_T_FP16)
+    return launched(i8 ? launch_sort<fp16_t, true>(a, s) : launch_sort<fp16_t, false>(a, s));
+  return launched(i8 ? launch_sort<float, true>(a, s) : launch_sort<float, false>(a, s));
 }
 
 moe_status moe_sort_tokens_grad(const void* drows, int64_t drows_stride, int32_t n_rows,
@@ -800,13 +791,9 @@ moe_status moe_combine_tokens_grad(const void* dout, int64_t dout_stride, const 
   CombineGradArgs a{dout, dout_stride, rows, rows_stride, n_rows, place, weights, T,
                     top_k, hidden, drows, drows_stride, dweights};
   const hipStream_t s = (hipStream_t)stream;
-  if (type == MOE_T_BF16)
-    launch_combine_grad<bf16_t>(a, s);
-  else if (type == MOE_T_FP16)
-    launch_combine_grad<fp16_t>(a, s);
-  else
-    launch_combine_grad<float>(a, s);
-  return launched();
+  if (type == MOE_T_BF16) return launched(launch_combine_grad<bf16_t>(a, s));
+  if (type == MOE_T_FP16) return launched(launch_combine_grad<fp16_t>(a, s));
+  return launched(launch_combine_grad<float>(a, s));
 }
 
 moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
@@ -819,13 +806,9 @@ moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int3
     return MOE_E_INVALID;
   QuantArgs a{x, x_stride, M, K, codes, codes_stride, scale, rows_end};
   const hipStream_t s = (hipStream_t)stream;
-  if (type == MOE_T_BF16)
-    launch_quantise<bf16_t>(a, s);
-  else if (type == MOE_T_FP16)
-    launch_quantise<fp16_t>(a, s);
-  else
-    launch_quantise<float>(a, s);
-  return launched();
+  if (type == MOE_T_BF16) return launched(launch_quantise<bf16_t>(a, s));
+  if (type == MOE_T_FP16) return launched(launch_quantise<fp16_t>(a, s));
+  return launched(launch_quantise<float>(a, s));
 }
 
 }  // extern "C"

@@ -39,3 +39,39 @@ def test_sort_of_no_tokens_writes_offsets(calls):
                     ("moe_sort_tokens", {**SORT, **none, "offsets": None}),
                     ("moe_sort_tokens", {**SORT, **none, "x": None, "x_type": I8}))
     assert all(r["status"] == INVALID and not r["launches"] for r in refused)
+
+
+COMBINE = dict(rows=P, rows_stride=64, n_rows=32, type=BF16, place=P, weights=P, T=16, top_k=2,
+               hidden=64, out=P, out_stride=64, stream=0)
+PRODUCT = dict(a=P, a_stride=64, a_scale=P, M=16, K=64, w=P, w_stride=64, w_scale=P, N=32,
+               groups=4, offsets=P, epilogue=0, out=P, out_stride=32, out_type=BF16, stream=0)
+EACH = [  # a call of every operator, of the sort one for each number of launches
+    ("moe_sort_tokens", SORT, 1), ("moe_sort_tokens", {**SORT, "T": 4096}, 2),
+    ("moe_sort_tokens", {**SORT, "T": 40000}, 3),
+    ("moe_sort_tokens_grad", dict(drows=P, drows_stride=64, n_rows=32, type=FP16, place=P, T=16,
+                                  top_k=2, hidden=64, dx=P, dx_stride=64, stream=0), 1),
+    ("moe_combine_tokens", COMBINE, 1),
+    ("moe_combine_tokens_grad", dict(dout=P, dout_stride=64, rows=P, rows_stride=64, n_rows=32,
+                                     type=FP32, place=P, weights=P, T=16, top_k=2, hidden=64,
+                                     drows=P, drows_stride=64, dweights=P, stream=0), 1),
+    ("moe_quantise_rows", dict(x=P, x_stride=64, type=BF16, M=16, K=64, codes=P, codes_stride=64,
+                               scale=P, rows_end=None, stream=0), 1),
+    ("moe_product_i8", PRODUCT, 1), ("moe_product_i8", {**PRODUCT, "M": 5000, "N": 4096,
+                                                        "out_stride": 4096}, 1)]
+
+
+def test_error_of_another_call_is_neither_reported_nor_taken(calls):
+    for (name, args, n), r in zip(EACH, calls(*[(name, args, dict(error=1))
+                                                for name, args, _ in EACH])):
+        assert r["status"] == OK and len(r["launches"]) == n, (name, r)
+        assert r["error"] == 1, name
+
+
+def test_failed_launch_ends_the_call(calls):
+    """Nothing is launched after it: the sort's later kernels would take whatever the workspace
+    holds as counts."""
+    wanted = [(name, args, at) for name, args, n in EACH for at in range(1, n + 1)]
+    for (name, args, at), r in zip(wanted, calls(*[(name, args, dict(launch=at))
+                                                   for name, args, at in wanted])):
+        assert r["status"] == HIP and len(r["launches"]) == at, (name, at, r)
+        assert r["error"] == 0, name  # reported, so no later call finds it
