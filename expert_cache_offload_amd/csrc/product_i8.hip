@@ -10,6 +10,7 @@
 // instruction's in the order below, 16 neighbouring channels of it: gate and up meet in a lane
 // and the output is stored in 16-byte pieces.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -23,6 +24,7 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kMaxK = 131071;  // 128 * 128 * K stays below 2^31
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxGroups320 = 512;  // of the 256 x 320 tiles (LDS)
 constexpr int kMaxN = 1 << 20;
 constexpr int kMaxM = (1 << 24) - 1;
 
@@ -636,11 +638,23 @@ void product_tile_kernel(ProdArgs a) {
 template <class E, bool SWIGLU, bool ANY, int WM, int WN, int MI, int NI, int KS, int PER_CU>
 hipError_t launch_tile(const ProdArgs& a, hipStream_t s) {
   constexpr int BM = 32 * WM * MI, BN = 32 * WN * NI, LT = 64 * WM * WN * KS;
-  const int lds = 2 * KS * (BM + BN) * LK + 12 * a.groups + 4;
+  constexpr int stages = 2 * KS * (BM + BN) * LK;
+  const int lds = stages + 12 * a.groups + 4;
   const auto kernel = product_tile_kernel<E, SWIGLU, ANY, WM, WN, MI, NI, KS, PER_CU>;
-  if (lds > 64 * 1024)
-    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                              lds);
+  // More than 64 KiB of LDS has to be allowed, for a kernel on a device as a whole: calls of other
+  // threads launch under the limit that is set, so it is the largest that any call needs.
+  constexpr int most = stages + 12 * (BN == 320 ? kMaxGroups320 : kMaxGroups) + 4;
+  if constexpr (most > 64 * 1024) {
+    static std::atomic<uint64_t> allowed{0};  // a bit per device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (e == hipSuccess && !(allowed.load(std::memory_order_relaxed) & bit)) {
+      e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (e == hipSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
+    if (e != hipSuccess) return e;
+  }
   const int64_t mt = a.M / BM + (a.offsets ? std::min(a.groups, a.M) : 1);
   const int64_t tiles = mt * ((a.N + BN - 1) / BN);
   const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, 256 * PER_CU);
@@ -700,7 +714,7 @@ hipError_t launch_product(const ProdArgs& a, hipStream_t s) {
   }
   int best = aligned ? 0 : 2;  // the two largest shapes have no registers for the other path
   for (int i = best + 1; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i)
-    if (!(kShapes[i].bn == 320 && a.groups > 512) &&  // LDS
+    if (!(kShapes[i].bn == 320 && a.groups > kMaxGroups320) &&
         tile_cost(kShapes[i], a) < tile_cost(kShapes[best], a))
       best = i;
   switch (best) {

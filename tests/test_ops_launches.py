@@ -75,3 +75,34 @@ def test_failed_launch_ends_the_call(calls):
                                                    for name, args, at in wanted])):
         assert r["status"] == HIP and len(r["launches"]) == at, (name, at, r)
         assert r["error"] == 0, name  # reported, so no later call finds it
+
+
+def test_lds_limit_of_a_kernel_is_one_for_all_calls(calls):
+    """The limit belongs to the kernel, whichever thread sets it: every call on a device needs at
+    most what the first has set, and a limit that cannot be set ends the call before its launch."""
+    big = {**PRODUCT, "M": 2_000_000, "N": 4096, "K": 2048, "a_stride": 2048, "w_stride": 2048,
+           "out_stride": 4096}
+    odd = {**big, "a_stride": 2049}
+    wanted = []
+    for args in (big, odd):
+        wanted += [("moe_product_i8", args, dict(attribute=1)), ("moe_product_i8", args),
+                   ("moe_product_i8", {**args, "groups": 500}), ("moe_product_i8", args),
+                   ("moe_product_i8", args, dict(device=1)),
+                   ("moe_product_i8", args, dict(device=1))]
+    out = calls(*wanted)
+    limit = {}
+    for (_, args, *setting), r in zip(wanted, out):
+        setting = setting[0] if setting else {}
+        if setting.get("attribute"):
+            assert r["status"] == HIP and not r["launches"] and r["error"] == 0
+            continue
+        assert r["status"] == OK and len(r["launches"]) == 1
+        kernel, lds = r["launches"][0][0], r["launches"][0][4]
+        assert "product_tile_kernel" in kernel and lds > 1 << 16
+        key = kernel, setting.get("device", 0)
+        for name, value in r["attributes"]:
+            assert name == kernel and key not in limit
+            limit[key] = value
+        assert lds <= limit[key]
+    assert len(limit) == 4  # one kernel for each of the two, whatever the groups, on two devices
+    assert len(set(limit.values())) == 2
