@@ -327,24 +327,25 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
 // epilogues are about 45.
 constexpr int LK = 128;
 
+// 16 bytes per lane from base + off to the LDS bytes from lds + 16 * lane on.  The instruction takes the
+// LDS address from m0: an operand of the statement, so the compiler writes the register and knows
+// what it holds (a wait state has to lie between that and the load).
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, const int8_t* base) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
-      : "s"(lds), "v"(off), "s"(base)
+      : "{m0}"(lds), "v"(off), "s"(base)
       : "memory");
 }
 
 // The same with 4 bytes per lane.
 __device__ __forceinline__ void load4_to_lds(uint32_t lds, uint32_t off, const float* base) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
       "global_load_lds_dword %1, %2"
       :
-      : "s"(lds), "v"(off), "s"(base)
+      : "{m0}"(lds), "v"(off), "s"(base)
       : "memory");
 }
 
