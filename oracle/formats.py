@@ -29,8 +29,9 @@ def bf16_to_f64(u16) -> np.ndarray:
     return (a.astype(np.uint32) << np.uint32(16)).view(np.float32).astype(np.float64)
 
 
-def e4m3fn_to_f64(codes) -> np.ndarray:
-    c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+def _e4m3fn_values() -> np.ndarray:
+    """The value of each of the 256 codes, by the definition."""
+    c = np.arange(256)
     sign = np.where((c >> 7) & 1, -1.0, 1.0)
     exp = (c >> 3) & 15
     man = c & 7
@@ -41,14 +42,29 @@ def e4m3fn_to_f64(codes) -> np.ndarray:
     return sign * val
 
 
-def e2m1_to_f64(nibbles) -> np.ndarray:
-    n = np.asarray(nibbles).astype(np.int64) & 15
+_E4M3FN = _e4m3fn_values()
+
+
+def e4m3fn_to_f64(codes) -> np.ndarray:
+    return _E4M3FN[np.asarray(codes, dtype=np.uint8)]
+
+
+def _e2m1_values() -> np.ndarray:
+    """The value of each of the 16 codes, by the definition."""
+    n = np.arange(16)
     sign = np.where((n >> 3) & 1, -1.0, 1.0)
     exp = (n >> 1) & 3
     man = n & 1
     normal = (1.0 + man / 2.0) * np.exp2(exp.astype(np.float64) - 1.0)
     sub = man * 0.5
     return sign * np.where(exp == 0, sub, normal)
+
+
+_E2M1 = _e2m1_values()
+
+
+def e2m1_to_f64(nibbles) -> np.ndarray:
+    return _E2M1[np.asarray(nibbles) & 15]
 
 
 def e8m0_to_f64(codes) -> np.ndarray:
