@@ -2,7 +2,9 @@
 
 Argument marshalling only: every step of the path runs in the HIP kernels of
 ``libmoe_offload.so``.  Pointers are passed as integers (``tensor.data_ptr()``), streams
-as ``torch.cuda.Stream.cuda_stream`` integers (0 = null stream).  Importing this
+as ``torch.cuda.Stream.cuda_stream`` integers (0 = null stream).  The operators on device
+buffers take tensors too and refuse one that they would misread (elements of another width,
+host memory).  Importing this
 package fails loudly when the library has not been built (``python -m
 expert_cache_offload_amd.build`` or ``__graft_entry__.build()``).
 """
@@ -156,6 +158,27 @@ def _p(x) -> int | None:
         return None
     if isinstance(x, int):
         return x
+    return x.data_ptr()
+
+
+_T_BYTES = {MOE_T_BF16: 2, MOE_T_FP16: 2, MOE_T_FP32: 4, MOE_T_I8: 1}
+
+
+def _b(x, size: int | None) -> int | None:
+    """Address of an operator's buffer.  A tensor has to be on the GPU (or pinned) and its elements
+    `size` bytes wide (None: of any width), as the call reads them: 64-bit expert ids, as
+    torch.topk gives them, would be taken for twice as many of 32 bits.  An address is taken as
+    it is."""
+    if x is None:
+        return None
+    try:
+        if x.itemsize == size and x.is_cuda:
+            return x.data_ptr()
+    except AttributeError:
+        return _p(x)
+    if (size and x.itemsize != size) or not (x.is_cuda or x.is_pinned()):
+        raise MoeError(MOE_E_INVALID, f"{x.dtype} tensor on {x.device} (elements of {size} bytes "
+                                      "in the GPU's memory are read)")
     return x.data_ptr()
 
 
@@ -429,51 +452,66 @@ def moe_sort_tokens(topk_idx, T: int, top_k: int, experts: int, offsets, order, 
                     rows_stride: int = 0, rows_type: int = MOE_T_BF16, row_scale=None,
                     workspace=None, workspace_bytes: int = 0, stream: int = 0) -> None:
     """Tokens sorted by expert, their rows copied or quantised (see the header)."""
-    _check(_lib.moe_sort_tokens(_p(topk_idx), T, top_k, experts, _p(offsets), _p(order),
-                                _p(place), _p(x), x_stride, hidden, x_type, _p(rows),
-                                rows_stride, rows_type, _p(row_scale), _p(workspace),
-                                workspace_bytes, stream), "moe_sort_tokens")
+    st = _lib.moe_sort_tokens(_b(topk_idx, 4), T, top_k, experts, _b(offsets, 4), _b(order, 4),
+                              _b(place, 4), _b(x, _T_BYTES.get(x_type)), x_stride, hidden, x_type,
+                              _b(rows, _T_BYTES.get(rows_type)), rows_stride, rows_type,
+                              _b(row_scale, 4), _b(workspace, None), workspace_bytes, stream)
+    if st:
+        _check(st, "moe_sort_tokens")
 
 
 def moe_sort_tokens_grad(drows, drows_stride: int, n_rows: int, type: int, place, T: int,
                          top_k: int, hidden: int, dx, dx_stride: int, stream: int = 0) -> None:
     """dx[t] = sum of drows at the token's places (see the header)."""
-    _check(_lib.moe_sort_tokens_grad(_p(drows), drows_stride, n_rows, type, _p(place), T, top_k,
-                                     hidden, _p(dx), dx_stride, stream), "moe_sort_tokens_grad")
+    size = _T_BYTES.get(type)
+    st = _lib.moe_sort_tokens_grad(_b(drows, size), drows_stride, n_rows, type, _b(place, 4), T,
+                                   top_k, hidden, _b(dx, size), dx_stride, stream)
+    if st:
+        _check(st, "moe_sort_tokens_grad")
 
 
 def moe_combine_tokens(rows, rows_stride: int, n_rows: int, type: int, place, weights, T: int,
                        top_k: int, hidden: int, out, out_stride: int, stream: int = 0) -> None:
     """Sorted rows back to tokens with the routing weights applied (see the header)."""
-    _check(_lib.moe_combine_tokens(_p(rows), rows_stride, n_rows, type, _p(place), _p(weights),
-                                   T, top_k, hidden, _p(out), out_stride, stream),
-           "moe_combine_tokens")
+    size = _T_BYTES.get(type)
+    st = _lib.moe_combine_tokens(_b(rows, size), rows_stride, n_rows, type, _b(place, 4),
+                                 _b(weights, 4), T, top_k, hidden, _b(out, size), out_stride,
+                                 stream)
+    if st:
+        _check(st, "moe_combine_tokens")
 
 
 def moe_combine_tokens_grad(dout, dout_stride: int, rows, rows_stride: int, n_rows: int,
                             type: int, place, weights, T: int, top_k: int, hidden: int, drows,
                             drows_stride: int, dweights, stream: int = 0) -> None:
     """Gradients of moe_combine_tokens for the rows and the weights (see the header)."""
-    _check(_lib.moe_combine_tokens_grad(_p(dout), dout_stride, _p(rows), rows_stride, n_rows,
-                                        type, _p(place), _p(weights), T, top_k, hidden,
-                                        _p(drows), drows_stride, _p(dweights), stream),
-           "moe_combine_tokens_grad")
+    size = _T_BYTES.get(type)
+    st = _lib.moe_combine_tokens_grad(_b(dout, size), dout_stride, _b(rows, size), rows_stride,
+                                      n_rows, type, _b(place, 4), _b(weights, 4), T, top_k,
+                                      hidden, _b(drows, size), drows_stride, _b(dweights, 4),
+                                      stream)
+    if st:
+        _check(st, "moe_combine_tokens_grad")
 
 
 def moe_quantise_rows(x, x_stride: int, type: int, M: int, K: int, codes, codes_stride: int,
                       scale, rows_end=None, stream: int = 0) -> None:
     """8-bit codes and one scale for each row (see the header)."""
-    _check(_lib.moe_quantise_rows(_p(x), x_stride, type, M, K, _p(codes), codes_stride,
-                                  _p(scale), _p(rows_end), stream), "moe_quantise_rows")
+    st = _lib.moe_quantise_rows(_b(x, _T_BYTES.get(type)), x_stride, type, M, K, _b(codes, 1),
+                                codes_stride, _b(scale, 4), _b(rows_end, 4), stream)
+    if st:
+        _check(st, "moe_quantise_rows")
 
 
 def moe_product_i8(a, a_stride: int, a_scale, M: int, K: int, w, w_stride: int, w_scale, N: int,
                    groups: int, offsets, epilogue: int, out, out_stride: int, out_type: int,
                    stream: int = 0) -> None:
     """Product of 8-bit integers with scales per row and channel (see the header)."""
-    _check(_lib.moe_product_i8(_p(a), a_stride, _p(a_scale), M, K, _p(w), w_stride, _p(w_scale),
-                               N, groups, _p(offsets), epilogue, _p(out), out_stride, out_type,
-                               stream), "moe_product_i8")
+    st = _lib.moe_product_i8(_b(a, 1), a_stride, _b(a_scale, 4), M, K, _b(w, 1), w_stride,
+                             _b(w_scale, 4), N, groups, _b(offsets, 4), epilogue,
+                             _b(out, _T_BYTES.get(out_type)), out_stride, out_type, stream)
+    if st:
+        _check(st, "moe_product_i8")
 
 
 def moe_status_string(status: int) -> str:

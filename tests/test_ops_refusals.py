@@ -149,3 +149,34 @@ def test_no_rows_still_checks_sizes_and_types(name, args):
     with pytest.raises(m.MoeError) as e:
         getattr(m, name)(*args)
     assert e.value.status == m.MOE_E_INVALID
+
+
+def test_tensors_that_a_call_would_misread():
+    """Tensors whose elements are of another width than the call reads (64-bit expert ids, as
+    torch.topk gives them, 16-bit weights) and tensors in ordinary host memory are refused."""
+    import torch
+    m = _m()
+    wide, half = torch.zeros(64, dtype=torch.int64), torch.zeros(64, dtype=torch.bfloat16)
+    word, real = torch.zeros(64, dtype=torch.int32), torch.zeros(64)
+    for name in ("topk_idx", "offsets", "order", "place"):
+        for t in (wide, word):  # another width; host memory
+            _refused("moe_sort_tokens", m.MOE_E_INVALID, **{**SORT, name: t})
+    for name, t in (("x", real), ("rows", real), ("row_scale", half), ("workspace", word)):
+        _refused("moe_sort_tokens", m.MOE_E_INVALID, **{**SORT, name: t})
+    for name, t in (("rows", real), ("place", wide), ("weights", half), ("out", real)):
+        _refused("moe_combine_tokens", m.MOE_E_INVALID, **{**COMBINE, name: t})
+    for name, t in (("a", word), ("a_scale", half), ("w", word), ("w_scale", half),
+                    ("offsets", wide), ("out", real)):
+        _refused("moe_product_i8", m.MOE_E_INVALID, **{**PRODUCT, name: t})
+    grad = dict(dout=P, dout_stride=64, rows=P, rows_stride=64, n_rows=32, type=BF16, place=P,
+                weights=P, T=16, top_k=2, hidden=64, drows=P, drows_stride=64, dweights=P)
+    for name, t in (("dout", real), ("rows", real), ("place", wide), ("weights", half),
+                    ("drows", real), ("dweights", half)):
+        _refused("moe_combine_tokens_grad", m.MOE_E_INVALID, **{**grad, name: t})
+    grad = dict(drows=P, drows_stride=64, n_rows=32, type=BF16, place=P, T=16, top_k=2, hidden=64,
+                dx=P, dx_stride=64)
+    for name, t in (("drows", real), ("place", wide), ("dx", real)):
+        _refused("moe_sort_tokens_grad", m.MOE_E_INVALID, **{**grad, name: t})
+    rows = dict(x=P, x_stride=64, type=BF16, M=16, K=64, codes=P, codes_stride=64, scale=P)
+    for name, t in (("x", real), ("codes", word), ("scale", half), ("rows_end", wide)):
+        _refused("moe_quantise_rows", m.MOE_E_INVALID, **{**rows, name: t})
