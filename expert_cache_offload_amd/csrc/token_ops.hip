@@ -598,6 +598,16 @@ constexpr int kMaxCols = 1 << 20;
 int block_tokens(int k) { return kChunkIds / k; }
 int block_count(int T, int k) { return (T + block_tokens(k) - 1) / block_tokens(k); }
 
+// The move kernel of a launch.  Rows below 16 bytes (V = 1) are never streamed as codes (2^24 rows of 7
+// stay below kStreamBytes), nor where tokens are few enough for WIDE.
+template <class E, int V, bool I8, bool WIDE>
+auto move_kernel(bool self, bool stream) {
+  if (self) return sort_move_kernel<E, V, I8, WIDE, false, true>;
+  if constexpr (V > 1 || !(I8 || WIDE))
+    if (stream) return sort_move_kernel<E, V, I8, WIDE, true, false>;
+  return sort_move_kernel<E, V, I8, WIDE, false, false>;
+}
+
 template <class E, int V, bool I8>
 hipError_t launch_sort_by(SortArgs& a, hipStream_t s) {
   const int nc = a.x ? chunk_count<V>(a.H) : 0;
@@ -621,12 +631,8 @@ hipError_t launch_sort_by(SortArgs& a, hipStream_t s) {
   // and where few choices make for few ids per token, as many as leave 1024 workgroups
   if (a.T > 1024 * kSubTokens) sub = std::max(sub, std::min(a.T / 1024, kSubIds / 2 / a.k));
   const bool stream = (int64_t)a.N * a.H * (I8 ? 1 : (int)sizeof(E)) > kStreamBytes;
-  const auto kernel = self ? wide ? sort_move_kernel<E, V, I8, true, false, true>
-                                  : sort_move_kernel<E, V, I8, false, false, true>
-                      : wide ? stream ? sort_move_kernel<E, V, I8, true, true, false>
-                                      : sort_move_kernel<E, V, I8, true, false, false>
-                             : stream ? sort_move_kernel<E, V, I8, false, true, false>
-                                      : sort_move_kernel<E, V, I8, false, false, false>;
+  const auto kernel = wide ? move_kernel<E, V, I8, true>(self, stream)
+                           : move_kernel<E, V, I8, false>(self, stream);
   const int subs = (a.tok_blk + sub - 1) / sub;
   return launch_kernel(kernel, dim3(a.nblk * subs), dim3(TOK_T), (size_t)kChunkWaves * a.E * 2, s, a,
                        sub, subs);
@@ -639,6 +645,14 @@ hipError_t launch_sort(SortArgs& a, hipStream_t s) {
                                   : launch_sort_by<E, 1, I8>(a, s);
 }
 
+// A row of 16 bytes at least may have a wave to itself (uni), a shorter one never has.
+template <class E, int V, bool W>
+auto combine_kernel_for(bool uni, bool stream) {
+  if constexpr (V > 1)
+    if (uni) return stream ? combine_kernel<E, V, W, true, true> : combine_kernel<E, V, W, true, false>;
+  return combine_kernel<E, V, W, false, false>;
+}
+
 template <class E, int V>
 hipError_t launch_combine_by(CombineArgs& a, hipStream_t s) {
   const int nc = chunk_count<V>(a.H);
@@ -649,12 +663,8 @@ hipError_t launch_combine_by(CombineArgs& a, hipStream_t s) {
                   (unsigned)((nc + (1 << a.tpt_log) - 1) >> a.tpt_log));
   const bool uni = a.tpt_log >= 6;
   const bool stream = (int64_t)a.T * a.k * a.H * (int)sizeof(E) > kStreamBytes;
-  const auto kernel = a.w ? uni ? stream ? combine_kernel<E, V, true, true, true>
-                                         : combine_kernel<E, V, true, true, false>
-                                : combine_kernel<E, V, true, false, false>
-                          : uni ? stream ? combine_kernel<E, V, false, true, true>
-                                         : combine_kernel<E, V, false, true, false>
-                                : combine_kernel<E, V, false, false, false>;
+  const auto kernel = a.w ? combine_kernel_for<E, V, true>(uni, stream)
+                          : combine_kernel_for<E, V, false>(uni, stream);
   return launch_kernel(kernel, grid, dim3(TOK_T), 0, s, a);
 }
 template <class E>

@@ -1,5 +1,7 @@
 """What the operators launch, and what they answer when a launch fails, seen without a GPU: the
 runtime's launches are replaced (hip_stub.py)."""
+import re
+
 import pytest
 
 import hip_stub
@@ -21,7 +23,7 @@ def calls(tmp_path_factory):
         """Each wanted call as (name, arguments[, settings])."""
         out, kernels = hip_stub.run(lib, [[w[0], w[1], w[2] if len(w) > 2 else {}]
                                           for w in wanted])
-        assert len(kernels) > 100
+        run.kernels = kernels
         return out
     return run
 
@@ -106,3 +108,66 @@ def test_lds_limit_of_a_kernel_is_one_for_all_calls(calls):
         assert lds <= limit[key]
     assert len(limit) == 4  # one kernel for each of the two, whatever the groups, on two devices
     assert len(set(limit.values())) == 2
+
+
+def _variant_calls():
+    """Every case of ops_variants as a call, with the tile it is there for."""
+    import ops_variants as v
+    for tile, per_gpu, any_, counts, N, K, pad, at in v.TILES:
+        for kind in v.KINDS:
+            for swiglu in (False, True):
+                yield "moe_product_i8", v.product_args(counts, N, K, pad, at, kind, swiglu), \
+                    (tile, per_gpu, any_, counts, N)
+    for counts, N, K, pad, at in v.FEW:
+        for kind in v.KINDS:
+            for swiglu in (False, True):
+                yield "moe_product_i8", v.product_args(counts, N, K, pad, at, kind, swiglu), None
+    for kind in v.KINDS:
+        for T, k, E, _, H, pad, at in v.SORTS:
+            for rows in (kind, "i8"):
+                yield "moe_sort_tokens", v.sort_args(T, k, E, H, pad, at, kind, rows), None
+        T, k, E, _, H, pad, at = v.SORTS_SHORT_STREAMED[kind == "fp32"]
+        yield "moe_sort_tokens", v.sort_args(T, k, E, H, pad, at, kind, kind), None
+        for T, k, _, H, pad, at in v.COMBINES:
+            args = v.combine_args(T, k, H, pad, at, kind)
+            yield "moe_combine_tokens", args, None
+            yield "moe_sort_tokens_grad", dict(
+                drows=args["rows"], drows_stride=args["rows_stride"], n_rows=args["n_rows"],
+                type=args["type"], place=P, T=T, top_k=k, hidden=H, dx=P, dx_stride=H), None
+            yield "moe_combine_tokens_grad", dict(
+                dout=P, dout_stride=H, rows=args["rows"], rows_stride=args["rows_stride"],
+                n_rows=args["n_rows"], type=args["type"], place=P, weights=P, T=T, top_k=k,
+                hidden=H, drows=P, drows_stride=H, dweights=P), None
+        for M, K in v.quantises(kind):
+            yield "moe_quantise_rows", v.quantise_args(M, K, kind), None
+
+
+def test_variants_reach_every_kernel(calls):
+    """The cases that the GPU tests run launch every kernel of the operators, and every tile kernel
+    with more tiles than workgroups, so that a workgroup goes on to a second tile."""
+    wanted = list(_variant_calls())
+    out = calls(*[(name, args) for name, args, _ in wanted])
+    reached, second = set(), set()
+    for (name, args, tile), r in zip(wanted, out):
+        assert r["status"] == OK, (name, args)
+        reached |= {launch[0] for launch in r["launches"]}
+        if tile is None:
+            continue
+        (rows, channels, sets), per_gpu, any_, counts, N = tile
+        kernel, grid = r["launches"][0][:2]
+        shape = re.search(r"product_tile_kernelI.*Lb[01]ELb([01])ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)"
+                          r"ELi(\d+)ELi(\d+)EEE", kernel)
+        assert shape, (kernel, args)
+        free, wm, wn, mi, ni, ks, per_cu = map(int, shape.groups())
+        assert (32 * wm * mi, 32 * wn * ni, ks, 256 * per_cu, bool(free)) == (
+            rows, channels, sets, per_gpu, any_), args
+        groups = [counts] if isinstance(counts, int) else counts
+        tiles = sum(-(-c // rows) for c in groups) * -(-N // channels)
+        assert tiles > grid == per_gpu, (args, tiles, grid)
+        second.add(kernel)
+    kernels = {k for k in calls.kernels if re.search(r"\d(sort|combine|quantise|product)_", k)
+               and not k.endswith("7FfnArgsE")}  # the layer step's own combine
+    assert len(kernels) > 100
+    assert {k for k in kernels if "product_tile_kernel" in k} == second
+    missed = sorted(kernels - reached)
+    assert not missed, (len(missed), missed)
