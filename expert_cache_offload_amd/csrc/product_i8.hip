@@ -319,23 +319,23 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
 // goes through registers, fetched one stage before it is put into LDS.
 //
 // What bounds the large dense shapes is power: 8192 x 8192 x 8192 runs at 2.37 to 2.46 POP/s with
-// normally distributed codes and at 3.48 with zeros; with the former the clock falls to 1.6 GHz of 2.4
-// while the matrix units are 67% busy (a vendor library's plain 8-bit product: 2.08, zeros 3.26).
+// normally distributed codes and at 3.48 with zeros; with the former the clock falls to 1.6 GHz of
+// 2.4 while the matrix units are 67% busy (a vendor library's plain 8-bit product: 2.08, zeros 3.26).
 // Stages of 64 bytes four deep, 128 x 128 per wave, four waves of 64 x 64 per SIMD and fixed
 // orders of reads and products were within 15% of this or slower.  With few stages per tile it is
 // what lies outside them: 131072 rows over 128 experts x 1536 channels, SwiGLU, bf16 out take 104,
-// 181, 272 and 455 us at K = 128, 512, 1024 and 2048 (437 to 482 by the box), 23 us for each stage and
-// 90 besides; x 2048 channels, plain, 168 and 338 at K = 128 and 768, 34 for each stage and 134
-// besides.  There a tile's stores hold up the next one's first product: every stage's barrier
+// 181, 272 and 455 us at K = 128, 512, 1024 and 2048 (437 to 482 by the box), 23 us for each stage
+// and 90 besides; x 2048 channels, plain, 168 and 338 at K = 128 and 768, 34 for each stage and
+// 134 besides.  There a tile's stores hold up the next one's first product: every stage's barrier
 // waits for all that is outstanding, stores too.
 // Registers: the 256 x 320 kernels spill 45 to 51 vector registers (184 to 208 bytes a lane, mostly
 // in taking up a tile and in the epilogue), of those for any alignment (ANY, with a 64-bit address
 // for each load) 128 x 128 spills 22 to 25 and 64 x 64 over two or four sets of waves 11 to 16.
 constexpr int LK = 128;
 
-// 16 bytes per lane from base + off to the LDS bytes from lds + 16 * lane on.  The instruction takes the
-// LDS address from m0: an operand of the statement, so the compiler writes the register and knows
-// what it holds (a wait state has to lie between that and the load).
+// 16 bytes per lane from base + off to the LDS bytes from lds + 16 * lane on.  The instruction takes
+// the LDS address from m0: an operand of the statement, so the compiler writes the register and
+// knows what it holds (a wait state has to lie between that and the load).
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, const int8_t* base) {
   asm volatile(
       "s_nop 0\n\t"
@@ -711,10 +711,10 @@ hipError_t launch_product(const ProdArgs& a, hipStream_t s) {
   const bool aligned = !(((uintptr_t)a.a | (uintptr_t)a.w | (uintptr_t)a.as | (uintptr_t)a.ws |
                           (uintptr_t)a.K) & 15) &&
                        a.as < (1 << 22) && a.ws < (1 << 22);  // a tile's offsets: 31 bits
-  // Few rows: the streaming kernel takes 16 of them nearly as fast as one (x 5000 channels x 4096: 8.0
-  // and 9.3 us); with more the tiles win (17 rows 11.6, 64 rows 13.0 against 22.8 us) where
-  // alignment allows them, and for 128 rows of 128 groups the two are equal (42.0 and 42.5 us, the
-  // weights' bytes).
+  // Few rows: the streaming kernel takes 16 of them nearly as fast as one (x 5000 channels x 4096:
+  // 8.0 and 9.3 us); with more the tiles win (64 rows: 13.0 against 22.8 us) where alignment
+  // allows them, and for 128 rows of 128 groups the two are equal (42.0 and 42.5 us, the weights'
+  // bytes).
   if (a.M <= 16 || (a.M <= 64 && (a.offsets || !aligned))) {
     const int nf = (a.N + FN - 1) / FN;
     if (a.offsets || a.M <= 16)

@@ -34,8 +34,8 @@ constexpr int kMaxRows = (1 << 24) - 1;  // a workgroup each stays a launch's si
 // not be there any more for whoever reads it next, and the chip moves it faster so (16384 tokens
 // of 8 rows, 2048 bf16: sort 137 -> 116 us, combine 118 -> 102, its gradient 226 -> 207, 131072 rows
 // of 768 quantised 54.7 -> 52.0; a gradient over 34 MB, which stays in the 256 MB cache, got slower
-// so, 13.7 -> 15.4 us).  Two exceptions: combine below a wave per token, and sorts whose launch counts for
-// itself (up to 16 chunks, 16384 assignments), never stream.
+// so, 13.7 -> 15.4 us).  Two exceptions: combine below a wave per token, and sorts whose last launch
+// adds up the counts itself (up to 16 chunks, 16384 assignments), never stream.
 constexpr int64_t kStreamBytes = 128 << 20;
 constexpr int kScanExperts = 16, kScanSegs = 64;  // of a workgroup of the scan
 constexpr int SCAN_T = kScanExperts * kScanSegs;

@@ -472,9 +472,9 @@ moe_status moe_quantise_rows(const void* x, int64_t x_stride, int32_t type, int3
  * M rows; else device words [groups + 1], rows offsets[g] .. offsets[g + 1] - 1 belong to group
  * g (ascending, within [0, M]; what lies outside is cut off), and the rows of out that belong
  * to no group are left as they were.  The integer sum is exact, its scaling in fp32 from the left
- * (sum * a_scale has to be within its range).  The sizes of the groups are not known on the host: how the
- * work is tiled goes by all M rows in equal groups, the result does not.  A down weight has a
- * channel per row, [H][I]; the WdT [I][H] of an expert blob is its transpose.
+ * (sum * a_scale has to be within its range).  The sizes of the groups are not known on the host:
+ * how the work is tiled goes by all M rows in equal groups, the result does not.  A down weight
+ * has a channel per row, [H][I]; the WdT [I][H] of an expert blob is its transpose.
  * epilogue MOE_EPI_NONE: out [M][N] = c.  MOE_EPI_SWIGLU (N even): channels 2i and 2i + 1 are
  * gate and up (the order of an expert blob's rows), out [M][N/2] = silu(c[2i]) * c[2i + 1].
  * out_type bf16, fp16 or fp32.  M 0..16777215, N 1..1048576, K 1..131071 (a longer sum could
