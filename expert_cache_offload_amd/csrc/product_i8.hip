@@ -324,7 +324,7 @@ __global__ __launch_bounds__(FT) void product_few_kernel(ProdArgs a) {
 // Stages of 64 bytes four deep, 128 x 128 per wave, four waves of 64 x 64 per SIMD and fixed
 // orders of reads and products were within 15% of this or slower.  With few stages per tile it is
 // what lies outside them: 131072 rows over 128 experts x 1536 channels, SwiGLU, bf16 out take 104,
-// 181, 272 and 455 us at K = 128, 512, 1024 and 2048 (437 to 482 by the box), 23 us for each stage
+// 181, 272 and 455 us at K = 128, 512, 1024 and 2048 (437 to 482 by the card), 23 us for each stage
 // and 90 besides; x 2048 channels, plain, 168 and 338 at K = 128 and 768, 34 for each stage and
 // 134 besides.  There a tile's stores hold up the next one's first product: every stage's barrier
 // waits for all that is outstanding, stores too.
