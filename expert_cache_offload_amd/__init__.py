@@ -74,6 +74,7 @@ _PROF_KINDS = ("route", "fill", "gate_up", "down")
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 _SIGS = {
     "moe_blob_bytes": (_i64, [_i32, _i32, _i32]),
     "moe_workspace_bytes": (_sz, [ctypes.POINTER(MoeShape), _i32]),
@@ -130,6 +131,11 @@ _SIGS = {
     "moe_quantise_rows": (_i32, [_vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]),
     "moe_product_i8": (_i32, [_vp, _i64, _vp, _i32, _i32, _vp, _i64, _vp, _i32, _i32, _vp, _i32,
                               _vp, _i64, _i32, _vp]),
+    "moe_norm_rows": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _f32, _vp, _i64, _vp,
+                             _i64, _vp, _i64, _vp, _vp]),
+    "moe_norm_grad_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_norm_rows_grad": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _f32,
+                                  _vp, _i64, _vp, _vp, _sz, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_i32]),
     "moe_last_hip_error": (_i32, [_vp]),
 }
@@ -512,6 +518,35 @@ def moe_product_i8(a, a_stride: int, a_scale, M: int, K: int, w, w_stride: int, 
                              _b(out, _T_BYTES.get(out_type)), out_stride, out_type, stream)
     if st:
         _check(st, "moe_product_i8")
+
+
+def moe_norm_rows(x, x_stride: int, residual, residual_stride: int, type: int, M: int, K: int,
+                  weight, eps: float, sum, sum_stride: int, y, y_stride: int, codes=None,
+                  codes_stride: int = 0, scale=None, stream: int = 0) -> None:
+    """Norm of the rows of x + residual, rounded and in 8 bits (see the header)."""
+    size = _T_BYTES.get(type)
+    st = _lib.moe_norm_rows(_b(x, size), x_stride, _b(residual, size), residual_stride, type, M, K,
+                            _b(weight, size), eps, _b(sum, size), sum_stride, _b(y, size), y_stride,
+                            _b(codes, 1), codes_stride, _b(scale, 4), stream)
+    if st:
+        _check(st, "moe_norm_rows")
+
+
+def moe_norm_grad_workspace_bytes(M: int, K: int) -> int:
+    return int(_lib.moe_norm_grad_workspace_bytes(M, K))
+
+
+def moe_norm_rows_grad(dy, dy_stride: int, dsum, dsum_stride: int, sum, sum_stride: int, type: int,
+                       M: int, K: int, weight, eps: float, dx, dx_stride: int, dweight=None,
+                       workspace=None, workspace_bytes: int = 0, stream: int = 0) -> None:
+    """Gradients of moe_norm_rows for its rows and its weight (see the header)."""
+    size = _T_BYTES.get(type)
+    st = _lib.moe_norm_rows_grad(_b(dy, size), dy_stride, _b(dsum, size), dsum_stride,
+                                 _b(sum, size), sum_stride, type, M, K, _b(weight, size), eps,
+                                 _b(dx, size), dx_stride, _b(dweight, 4), _b(workspace, None),
+                                 workspace_bytes, stream)
+    if st:
+        _check(st, "moe_norm_rows_grad")
 
 
 def moe_status_string(status: int) -> str:

@@ -1,0 +1,450 @@
+// Root-mean-square norm of rows with the residual's addition, in the rows' type and in 8 bits, and
+// its gradient.
+//
+// h = x + r rounded to the rows' type, q = 1 / sqrt(mean(h^2) + eps), y = q h w.  The 8-bit codes are
+// those of the unrounded y: code = 127 y / max |y| = 127 p / max |p| with p = h w, where q cancels,
+// so they are exact; scale = max |p| q / 127.  Gradient: with S = sum_k w dy h,
+// dx = dsum + q w dy - h q^3 S / K, and dw = sum over the rows of q dy h.
+//
+// A row is read once and held in registers between its sums and its outputs, so both directions
+// are bound by the bytes of the matrices.  Sums over a row are held in 64 bits: fp64 is as fast as
+// unpacked fp32 here, and squares of any element stay in range.
+#include <algorithm>
+#include <type_traits>
+
+#include "row_ops.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxNormCols = 16384;  // a row is held by a workgroup
+constexpr int HELD = 4;              // chunks of it that a lane holds
+
+struct NormArgs {
+  const void* x;
+  int64_t xs;
+  const void* res;  // may be null
+  int64_t res_s;
+  int M, K;
+  const void* w;
+  float eps;
+  void* sum;  // may be null, x or res
+  int64_t sum_s;
+  void* y;  // may be null, x or res
+  int64_t ys;
+  int8_t* codes;  // may be null
+  int64_t cs;
+  float* scale;
+};
+
+// A row is held by G lanes (beyond 64: by the whole workgroup).
+constexpr int norm_threads(int G) { return G < 256 ? 256 : G; }
+
+template <int G, class T, class Join>
+__device__ __forceinline__ T row_join(T v, T* s_part, Join&& join) {
+#pragma unroll
+  for (int s = (G < 64 ? G : 64) / 2; s > 0; s >>= 1) v = join(v, __shfl_xor(v, s));
+  if constexpr (G > 64) {
+    __syncthreads();  // what an earlier sum left has been read
+    if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s_part[0];
+#pragma unroll
+    for (int i = 1; i < G / 64; ++i) v = join(v, s_part[i]);
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ double row_sum(double v, double* s_part) {
+  return row_join<G>(v, s_part, [](double a, double b) { return a + b; });
+}
+// The larger one; a NaN stays.
+__device__ __forceinline__ double max_nan(double a, double b) { return a > b || a != a ? a : b; }
+template <int G>
+__device__ __forceinline__ double row_max(double v, double* s_part) {
+  return row_join<G>(v, s_part, [](double a, double b) { return max_nan(a, b); });
+}
+
+// The exact code of p beside the row's largest magnitude m: p and m are products of two numbers of 24
+// bits and exact in 64; the quotient's rounding is that of 64 bits.
+__device__ __forceinline__ uint32_t code_f64(double p, double m) {
+  return __float_as_uint((float)rint(127.0 * p / m) + 12582912.0f);
+}
+
+// Codes of a chunk of p = h w.  Where every |p| that matters is far inside fp32's range (`plain`):
+// 16-bit types have their products exact in fp32, and those of bf16 have 16 bits, so that 127 p is
+// exact too and quant_bits' 16-bit form holds: a quotient 127 P 2^e / M that is no tie (P and M of 16
+// bits) is 2^e / 2^17 from one at least, and the corrected quotient is right to half a step, below
+// 2^(e - 18) where P <= M, and for e < 0 (P up to 2 M) 2^(e - 17) beside 2^e / 2^16.  fp32
+// products have 48 bits: the fp32 quotient, off by less than 127 * 2^-21, decides unless it is within
+// 2^-12 of a tie, and 64 bits do there.
+template <class E, int V>
+__device__ __forceinline__ Codes<E, V> norm_codes(const Chunk<E, V>& h, const Chunk<E, V>& w,
+                                                  const RowQuant& r, double m, bool plain) {
+  Codes<E, V> o;
+  uint32_t b[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float hf = to_f32(h.e[i]), wf = to_f32(w.e[i]);
+    if (!plain) {
+      b[i] = code_f64((double)hf * (double)wf, m);
+    } else if constexpr (__is_same(E, bf16_t)) {
+      b[i] = quant_bits<bf16_t>(hf * wf, r);
+    } else if constexpr (sizeof(E) == 2) {
+      b[i] = quant_bits<float>(hf * wf, r);
+    } else {
+      const float q = r.k * (hf * wf) * r.inv, n = rintf(q);
+      b[i] = __float_as_uint(n + 12582912.0f);
+      if (fabsf(q - n) > 0.5f - 0x1p-12f) b[i] = code_f64((double)hf * (double)wf, m);
+    }
+  }
+  if constexpr (V == 1) {
+    o.w[0] = r.live ? b[0] : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const uint32_t lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x04000c0cu);
+      o.w[i] = r.live ? lo | hi : 0u;
+    }
+  }
+  return o;
+}
+
+template <class E, int V, int G>
+__global__ __launch_bounds__(norm_threads(G)) void norm_rows_kernel(NormArgs a) {
+  constexpr int THR = norm_threads(G), ROWS = THR / G;
+  __shared__ double s_part[2][THR / 64];
+  const int lane = threadIdx.x % G;
+  const int nc = chunk_count<V>(a.K);
+  Chunk<E, V> w[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (lane + i * G < nc) w[i] = load_chunk<V>((const E*)a.w + chunk_at<V>(lane + i * G, a.K));
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / G; row < a.M;
+       row += (int64_t)gridDim.x * ROWS) {
+    const E* const x = (const E*)a.x + row * a.xs;
+    Chunk<E, V> h[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (lane + i * G < nc) h[i] = load_chunk<V>(x + chunk_at<V>(lane + i * G, a.K));
+    if (a.res) {
+      const E* const res = (const E*)a.res + row * a.res_s;
+      Chunk<E, V> r[HELD];
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (lane + i * G < nc) r[i] = load_chunk<V>(res + chunk_at<V>(lane + i * G, a.K));
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) {
+        float f[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = to_f32(h[i].e[e]) + to_f32(r[i].e[e]);
+        h[i] = round_chunk<E, V>(f);
+      }
+    }
+    double sq = 0.0, m = 0.0;
+    float m32 = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (lane + i * G >= nc) continue;
+      const int c = lane + i * G, twice = c * V - chunk_at<V>(c, a.K);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const double f = to_f32(h[i].e[e]);
+        sq = e >= twice ? fma(f, f, sq) : sq;
+        if (!a.codes) continue;
+        if constexpr (sizeof(E) == 2) {
+          const float p = fabsf(to_f32(h[i].e[e]) * to_f32(w[i].e[e]));
+          m32 = fmaxf(m32, p);
+          nan |= p != p;
+        } else {
+          m = max_nan(m, fabs(f * (double)to_f32(w[i].e[e])));
+        }
+      }
+    }
+    if constexpr (sizeof(E) == 2) m = nan ? __builtin_nan("") : (double)m32;
+    const double q = rsqrt(row_sum<G>(sq, s_part[0]) / a.K + (double)a.eps);
+    const float qf = (float)q;
+    if (a.sum) {
+      E* const sum = (E*)a.sum + row * a.sum_s;
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (lane + i * G < nc) store_chunk(sum + chunk_at<V>(lane + i * G, a.K), h[i]);
+    }
+    if (a.y) {
+      E* const y = (E*)a.y + row * a.ys;
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) {
+        if (lane + i * G >= nc) continue;
+        float f[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = to_f32(h[i].e[e]) * qf * to_f32(w[i].e[e]);
+        store_chunk(y + chunk_at<V>(lane + i * G, a.K), round_chunk<E, V>(f));
+      }
+    }
+    if (a.codes) {
+      m = row_max<G>(m, s_part[1]);
+      const bool plain = m >= 0x1p-60 && m <= 0x1p60;
+      if (sizeof(E) == 2 && !plain) {  // products that fp32 may have lost
+        m = 0.0;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+          if (lane + i * G < nc)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+              m = max_nan(m, fabs((double)to_f32(h[i].e[e]) * (double)to_f32(w[i].e[e])));
+        m = row_max<G>(m, s_part[1]);
+      }
+      RowQuant r = row_quant(__float_as_uint((float)m));
+      r.live = m > 0.0 && m < __builtin_inf();
+      int8_t* const codes = a.codes + row * a.cs;
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (lane + i * G < nc)
+          store_codes(codes + chunk_at<V>(lane + i * G, a.K), norm_codes(h[i], w[i], r, m, plain));
+      if (lane == 0)
+        a.scale[row] = m < __builtin_inf() ? (float)(m * q / 127.0) : __uint_as_float(0x7fc00000u);
+    }
+  }
+}
+
+struct NormGradArgs {
+  const void* dy;
+  int64_t dys;
+  const void* dsum;  // may be null
+  int64_t dsum_s;
+  const void* h;
+  int64_t hs;
+  int M, K;
+  const void* w;
+  float eps;
+  void* dx;  // may be null, dy or dsum
+  int64_t dxs;
+  float* part;  // [workgroups][K] sums of q dy h over a workgroup's rows; null: no dweight
+};
+
+// dx of the workgroup's rows, one after the other, and the part of dw that they give: each lane adds up
+// its own columns in fp32 over its rows, the row groups of the workgroup are joined in LDS.
+template <class E, int V, int G>
+__global__ __launch_bounds__(norm_threads(G)) void norm_rows_grad_kernel(NormGradArgs a) {
+  constexpr int THR = norm_threads(G), ROWS = THR / G;
+  __shared__ double s_part[2][THR / 64];
+  extern __shared__ __align__(16) float s_dw[];  // [ROWS][K], where ROWS > 1
+  const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  const int nc = chunk_count<V>(a.K);
+  Chunk<E, V> w[HELD];
+  float dw[HELD][V];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    if (lane + i * G < nc) w[i] = load_chunk<V>((const E*)a.w + chunk_at<V>(lane + i * G, a.K));
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[i][e] = 0.f;
+  }
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + group; row < a.M;
+       row += (int64_t)gridDim.x * ROWS) {
+    Chunk<E, V> h[HELD], g[HELD], d[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (lane + i * G >= nc) continue;
+      const int at = chunk_at<V>(lane + i * G, a.K);
+      h[i] = load_chunk<V>((const E*)a.h + row * a.hs + at);
+      g[i] = load_chunk<V>((const E*)a.dy + row * a.dys + at);
+      if (a.dsum && a.dx) d[i] = load_chunk<V>((const E*)a.dsum + row * a.dsum_s + at);
+    }
+    double sq = 0.0, dot = 0.0;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (lane + i * G >= nc) continue;
+      const int c = lane + i * G, twice = c * V - chunk_at<V>(c, a.K);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const double f = to_f32(h[i].e[e]);
+        const float wg = to_f32(w[i].e[e]) * to_f32(g[i].e[e]);
+        sq = e >= twice ? fma(f, f, sq) : sq;
+        dot = e >= twice ? fma(f, (double)wg, dot) : dot;
+      }
+    }
+    const double q = rsqrt(row_sum<G>(sq, s_part[0]) / a.K + (double)a.eps);
+    const float qf = (float)q;
+    const float cf = (float)(q * q * q * row_sum<G>(dot, s_part[1]) / a.K);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (lane + i * G >= nc) continue;
+      float f[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float hf = to_f32(h[i].e[e]), gf = to_f32(g[i].e[e]);
+        dw[i][e] = fmaf(gf, hf * qf, dw[i][e]);
+        const float own = a.dsum ? to_f32(d[i].e[e]) : 0.f;
+        f[e] = fmaf(-hf, cf, fmaf(qf, to_f32(w[i].e[e]) * gf, own));
+      }
+      if (a.dx)
+        store_chunk((E*)a.dx + row * a.dxs + chunk_at<V>(lane + i * G, a.K),
+                    round_chunk<E, V>(f));
+    }
+  }
+  if (!a.part) return;
+  float* const part = a.part + (int64_t)blockIdx.x * a.K;
+  float* const own = ROWS > 1 ? s_dw + group * a.K : part;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    if (lane + i * G >= nc) continue;
+    const int at = chunk_at<V>(lane + i * G, a.K);
+#pragma unroll
+    for (int e = 0; e < V; ++e) own[at + e] = dw[i][e];  // an overlap twice, with the same value
+  }
+  if constexpr (ROWS > 1) {
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.K; k += THR) {
+      float sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) sum += s_dw[r * a.K + k];
+      part[k] = sum;
+    }
+  }
+}
+
+// dw[k] = sum of the workgroups' parts, in 64 bits: a workgroup takes 32 columns, each of its 32 half
+// waves a share of the parts.  parts = 0: zeros.
+constexpr int PART_COLS = 32, PART_SHARES = 32;
+__global__ __launch_bounds__(PART_COLS * PART_SHARES) void norm_rows_parts_kernel(
+    const float* part, int parts, int K, float* dw) {
+  __shared__ double s_sum[PART_SHARES][PART_COLS];
+  const int col = threadIdx.x % PART_COLS, share = threadIdx.x / PART_COLS;
+  const int k = blockIdx.x * PART_COLS + col;
+  double sum = 0.0;
+  if (k < K) {
+#pragma unroll 4
+    for (int p = share; p < parts; p += PART_SHARES) sum += part[(int64_t)p * K + k];
+  }
+  s_sum[share][col] = sum;
+  __syncthreads();
+  if (share == 0 && k < K) {
+#pragma unroll
+    for (int s = 1; s < PART_SHARES; ++s) sum += s_sum[s][col];
+    dw[k] = (float)sum;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+// As few lanes per row as hold it: f(elements of a chunk, lanes).
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <class E, class F>
+auto by_width(int K, F&& f) {
+  constexpr int V = kChunk<E>;
+  const int nc = chunk_count<V>(K);
+  if (K < V) return f(Int<1>{}, Int<16>{});
+  if (nc <= 16 * HELD) return f(Int<V>{}, Int<16>{});
+  if (nc <= 64 * HELD) return f(Int<V>{}, Int<64>{});
+  if (nc <= 256 * HELD) return f(Int<V>{}, Int<256>{});
+  return f(Int<V>{}, Int<kMaxNormCols / V / HELD>{});
+}
+
+// Workgroups of a launch over M rows, `rows` at a time each.
+int norm_grid(int M, int rows, int most) { return std::min((M + rows - 1) / rows, most); }
+
+template <class E>
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  return by_width<E>(a.K, [&](auto v, auto g) {
+    constexpr int V = decltype(v)::value, G = decltype(g)::value, THR = norm_threads(G);
+    return launch_kernel(norm_rows_kernel<E, V, G>,
+                         dim3((unsigned)norm_grid(a.M, THR / G, 256 * 8)), dim3(THR), 0, s, a);
+  });
+}
+
+// Parts of dw (workgroups of the gradient's launch).
+constexpr int kMaxParts = 512;
+template <class E>
+int grad_parts(int M, int K) {
+  return by_width<E>(K, [&](auto, auto g) {
+    constexpr int G = decltype(g)::value;
+    return norm_grid(M, norm_threads(G) / G, G > 256 ? 256 : kMaxParts);
+  });
+}
+
+template <class E>
+hipError_t launch_norm_grad(NormGradArgs& a, float* dweight, float* ws, hipStream_t s) {
+  const int parts = grad_parts<E>(a.M, a.K);
+  if (dweight) a.part = parts == 1 ? dweight : ws;
+  hipError_t e = hipSuccess;
+  if (parts > 0)
+    e = by_width<E>(a.K, [&](auto v, auto g) {
+      constexpr int V = decltype(v)::value, G = decltype(g)::value, THR = norm_threads(G);
+      const size_t lds = THR > G && dweight ? sizeof(float) * (THR / G) * a.K : 0;
+      return launch_kernel(norm_rows_grad_kernel<E, V, G>,
+                           dim3((unsigned)parts), dim3(THR), lds, s, a);
+    });
+  if (e != hipSuccess || !dweight || parts == 1) return e;
+  return launch_kernel(norm_rows_parts_kernel, dim3((unsigned)((a.K + PART_COLS - 1) / PART_COLS)),
+                       dim3(PART_COLS * PART_SHARES), 0, s, (const float*)ws, parts, a.K, dweight);
+}
+
+bool norm_ok(int type, int M, int K, float eps) {
+  return float_type(type) && M >= 0 && M <= kMaxRows && K >= 1 && K <= kMaxNormCols && eps > 0.f &&
+         eps < __builtin_inff();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_norm_rows(const void* x, int64_t x_stride, const void* residual,
+                         int64_t residual_stride, int32_t type, int32_t M, int32_t K,
+                         const void* weight, float eps, void* sum, int64_t sum_stride, void* y,
+                         int64_t y_stride, int8_t* codes, int64_t codes_stride, float* scale,
+                         void* stream) {
+  if (!norm_ok(type, M, K, eps)) return MOE_E_INVALID;
+  if (M == 0) return MOE_OK;  // before the pointers: empty buffers have none
+  if (!rows_ok(x, x_stride, K, type) || !rows_ok(weight, K, K, type) ||
+      (residual && !rows_ok(residual, residual_stride, K, type)) || (!y && !codes) ||
+      (sum && (!residual || !rows_ok(sum, sum_stride, K, type))) ||
+      (y && !rows_ok(y, y_stride, K, type)) ||
+      (codes && (!rows_ok(codes, codes_stride, K, MOE_T_I8) || !scale || !aligned4(scale))) ||
+      !on_current_device(x))
+    return MOE_E_INVALID;
+  NormArgs a{x,   x_stride,   residual, residual_stride, M,     K,            weight, eps,
+             sum, sum_stride, y,        y_stride,        codes, codes_stride, scale};
+  const hipStream_t s = (hipStream_t)stream;
+  if (type == MOE_T_BF16) return launched(launch_norm<bf16_t>(a, s));
+  if (type == MOE_T_FP16) return launched(launch_norm<fp16_t>(a, s));
+  return launched(launch_norm<float>(a, s));
+}
+
+size_t moe_norm_grad_workspace_bytes(int32_t M, int32_t K) {
+  if (!norm_ok(MOE_T_FP32, M, K, 1.f)) return 0;
+  const int parts = std::max(grad_parts<float>(M, K), grad_parts<bf16_t>(M, K));
+  return parts > 1 ? sizeof(float) * (size_t)parts * (size_t)K : 0;
+}
+
+moe_status moe_norm_rows_grad(const void* dy, int64_t dy_stride, const void* dsum,
+                              int64_t dsum_stride, const void* sum, int64_t sum_stride,
+                              int32_t type, int32_t M, int32_t K, const void* weight, float eps,
+                              void* dx, int64_t dx_stride, float* dweight, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!norm_ok(type, M, K, eps) || !aligned4(dweight)) return MOE_E_INVALID;
+  if (M == 0 && !dweight) return MOE_OK;
+  if (M > 0 && (!rows_ok(dy, dy_stride, K, type) || !rows_ok(sum, sum_stride, K, type) ||
+                !rows_ok(weight, K, K, type) || (!dx && !dweight) ||
+                (dsum && !rows_ok(dsum, dsum_stride, K, type)) ||
+                (dx && !rows_ok(dx, dx_stride, K, type))))
+    return MOE_E_INVALID;
+  const size_t need = dweight ? moe_norm_grad_workspace_bytes(M, K) : 0;
+  if (need && (!workspace || !aligned4(workspace))) return MOE_E_INVALID;
+  if (workspace_bytes < need) return MOE_E_SCRATCH;
+  if (!on_current_device(M > 0 ? dy : dweight)) return MOE_E_INVALID;
+  NormGradArgs a{dy, dy_stride, dsum, dsum_stride, sum, sum_stride, M, K, weight, eps,
+                 dx, dx_stride, nullptr};
+  const hipStream_t s = (hipStream_t)stream;
+  float* const ws = (float*)workspace;
+  if (type == MOE_T_BF16) return launched(launch_norm_grad<bf16_t>(a, dweight, ws, s));
+  if (type == MOE_T_FP16) return launched(launch_norm_grad<fp16_t>(a, dweight, ws, s));
+  return launched(launch_norm_grad<float>(a, dweight, ws, s));
+}
+
+}  // extern "C"

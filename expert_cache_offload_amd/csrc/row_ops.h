@@ -247,6 +247,10 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
   return v;
 }
 
+inline bool float_type(int type) { return type >= MOE_T_BF16 && type <= MOE_T_FP32; }
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
+constexpr int kMaxRows = (1 << 24) - 1;  // a workgroup each stays a launch's size
+constexpr int kMaxCols = 1 << 20;
 inline size_t elem_bytes(int type) {
   return type == MOE_T_FP32 ? 4 : type == MOE_T_I8 ? 1 : 2;
 }

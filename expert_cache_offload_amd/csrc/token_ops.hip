@@ -29,7 +29,6 @@ constexpr int kSubTokens = 16;      // tokens a workgroup of the move kernel sor
 constexpr int kSubIds = 256;        // and the most assignments
 constexpr int kSelfChunks = 16;     // most chunks whose counts the move kernel adds up itself
 constexpr int kMaxT = 1 << 20;
-constexpr int kMaxRows = (1 << 24) - 1;  // a workgroup each stays a launch's size
 // A rows matrix above this is streamed past the caches (non-temporal loads and stores): it would
 // not be there any more for whoever reads it next, and the chip moves it faster so (16384 tokens
 // of 8 rows, 2048 bf16: sort 137 -> 116 us, combine 118 -> 102, its gradient 226 -> 207, 131072 rows
@@ -593,9 +592,6 @@ __global__ __launch_bounds__(TOK_T) void quantise_kernel(QuantArgs a) {
 bool tokens_ok(int T, int k, int E) {
   return T >= 0 && T <= kMaxT && k >= 1 && k <= kMaxTopK && E >= 1 && E <= kMaxExperts;
 }
-bool float_type(int type) { return type >= MOE_T_BF16 && type <= MOE_T_FP32; }
-bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
-constexpr int kMaxCols = 1 << 20;
 
 int block_tokens(int k) { return kChunkIds / k; }
 int block_count(int T, int k) { return (T + block_tokens(k) - 1) / block_tokens(k); }

@@ -74,7 +74,7 @@ typedef int32_t moe_status;
 #define MOE_E_NOMEM (-5)    /* pinned host allocation failed */
 #define MOE_E_HYBRID (-6)   /* hybrid decode: the host did not answer a step within ~2 s */
 #define MOE_E_SCRATCH (-7)  /* workspace above the static workspace (moe_cache_create_static),
-                            * or below what the call needs (moe_sort_tokens) */
+                            * or below what the call needs (operators) */
 
 #define MOE_FMT_BF16 0
 #define MOE_FMT_FP8_E4M3_K128 1
@@ -388,7 +388,7 @@ moe_status moe_probe_copy(const void* src, void* dst, uint64_t bytes, int32_t re
 
 /* ---------------------------------------------------------------- operators on device buffers
  *
- * The expert layer's token movement and an 8-bit integer product, as calls of their own: for
+ * The expert layer's norm, token movement and an 8-bit integer product, as calls of their own: for
  * experts that live outside a handle (kept resident, in 8-bit integers, or in training).  They
  * need no handle and keep nothing between calls.  Conventions as above, and:
  *  - a matrix is a pointer to its first element and the distance of its rows in elements (at
@@ -485,6 +485,42 @@ moe_status moe_product_i8(const int8_t* a, int64_t a_stride, const float* a_scal
                           int32_t K, const int8_t* w, int64_t w_stride, const float* w_scale,
                           int32_t N, int32_t groups, const int32_t* offsets, int32_t epilogue,
                           void* out, int64_t out_stride, int32_t out_type, void* stream);
+
+/* Root-mean-square norm of M rows of K elements, with the residual's addition in front.
+ *   h = x + residual, rounded to `type` (residual NULL: h = x); written to sum (may be NULL; only
+ *     with a residual);
+ *   y = h * weight / sqrt(mean(h^2) + eps) (may be NULL), rounded once more;
+ *   codes, scale (both or neither): y, unrounded, in 8 bits as moe_quantise_rows gives them: with
+ *     p = h * weight and m the row's largest |p| the code is 127 p / m to the nearest integer, ties to
+ *     even, exactly (fp32 inputs: with the quotient in 64 bits), the scale m / 127 times the
+ *     row's factor.  A row of zeros has scale 0, one with a NaN or an infinity in p scale NaN,
+ *     both codes 0.
+ * At least one of y and codes.  weight: [K] of `type`.  eps above 0.  sum and y may be x or residual
+ * themselves (the same rows), not both the same.  The mean is held in 64 bits.
+ * M 0..16777215, K 1..16384, type bf16, fp16 or fp32. */
+moe_status moe_norm_rows(const void* x, int64_t x_stride, const void* residual,
+                         int64_t residual_stride, int32_t type, int32_t M, int32_t K,
+                         const void* weight, float eps, void* sum, int64_t sum_stride, void* y,
+                         int64_t y_stride, int8_t* codes, int64_t codes_stride, float* scale,
+                         void* stream);
+
+/* Workspace bytes of moe_norm_rows_grad, of any type (0: none needed, or unsupported sizes); used as
+ * the sort's is. */
+size_t moe_norm_grad_workspace_bytes(int32_t M, int32_t K);
+
+/* Gradients of moe_norm_rows (of y; codes have none).  sum: the rows h that were normalised (the
+ * forward pass's sum, or x without a residual); dy: the gradient of y; dsum: what reaches h by
+ * other ways (may be NULL).  With q = 1 / sqrt(mean(h^2) + eps):
+ *   dx = dsum + q * weight * dy - h * q^3 * mean(weight * dy * h), the gradient of x and of residual
+ *     alike; dx may be dy or dsum itself;
+ *   dweight [K] fp32 = sum over the rows of q * dy * h (M = 0: zeros).
+ * dx or dweight may be NULL; without dweight no workspace is needed.  Sizes as moe_norm_rows.
+ * MOE_E_SCRATCH when workspace_bytes is below moe_norm_grad_workspace_bytes. */
+moe_status moe_norm_rows_grad(const void* dy, int64_t dy_stride, const void* dsum,
+                              int64_t dsum_stride, const void* sum, int64_t sum_stride,
+                              int32_t type, int32_t M, int32_t K, const void* weight, float eps,
+                              void* dx, int64_t dx_stride, float* dweight, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 const char* moe_status_string(moe_status s);
 
