@@ -22,6 +22,7 @@ MOE_E_HYBRID, MOE_E_SCRATCH = -6, -7
 MOE_FMT_BF16, MOE_FMT_FP8_E4M3_K128, MOE_FMT_MXFP4_K32 = 0, 1, 2
 MOE_T_BF16, MOE_T_FP16, MOE_T_FP32, MOE_T_I8 = 0, 1, 2, 3
 MOE_EPI_NONE, MOE_EPI_SWIGLU = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 # PyTorch ships its own HIP runtime with the same soname (libamdhip64.so.7).  Loading torch
 # first makes the library's HIP dependency resolve to that already-loaded runtime, so device
@@ -136,6 +137,10 @@ _SIGS = {
     "moe_norm_grad_workspace_bytes": (_sz, [_i32, _i32]),
     "moe_norm_rows_grad": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _f32,
                                   _vp, _i64, _vp, _vp, _sz, _vp]),
+    "moe_route_tokens": (_i32, [_vp, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32,
+                                _i32, _f32, _vp, _vp, _vp]),
+    "moe_route_tokens_grad": (_i32, [_vp, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32, _vp,
+                                     _vp, _i64, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_i32]),
     "moe_last_hip_error": (_i32, [_vp]),
 }
@@ -547,6 +552,29 @@ def moe_norm_rows_grad(dy, dy_stride: int, dsum, dsum_stride: int, sum, sum_stri
                                  workspace_bytes, stream)
     if st:
         _check(st, "moe_norm_rows_grad")
+
+
+def moe_route_tokens(logits, logits_stride: int, type: int, T: int, experts: int, score: int, bias,
+                     groups: int, group_best: int, top_groups: int, top_k: int, renormalise: bool,
+                     scale: float, topk_idx, topk_w, stream: int = 0) -> None:
+    """Experts and routing weights of tokens from their logits (see the header)."""
+    st = _lib.moe_route_tokens(_b(logits, _T_BYTES.get(type)), logits_stride, type, T, experts,
+                               score, _b(bias, 4), groups, group_best, top_groups, top_k,
+                               renormalise, scale, _b(topk_idx, 4), _b(topk_w, 4), stream)
+    if st:
+        _check(st, "moe_route_tokens")
+
+
+def moe_route_tokens_grad(logits, logits_stride: int, type: int, T: int, experts: int, score: int,
+                          topk_idx, top_k: int, renormalise: bool, scale: float, dweights, dlogits,
+                          dlogits_stride: int, stream: int = 0) -> None:
+    """Gradient of the routing weights for the logits (see the header)."""
+    size = _T_BYTES.get(type)
+    st = _lib.moe_route_tokens_grad(_b(logits, size), logits_stride, type, T, experts, score,
+                                    _b(topk_idx, 4), top_k, renormalise, scale, _b(dweights, 4),
+                                    _b(dlogits, size), dlogits_stride, stream)
+    if st:
+        _check(st, "moe_route_tokens_grad")
 
 
 def moe_status_string(status: int) -> str:

@@ -1,0 +1,520 @@
+// Experts and routing weights of tokens from their logits, and the gradient for the logits.
+//
+// Scores s = softmax(z) or 1 / (1 + exp(-z)); an expert is chosen by its choice value, c = s + bias or,
+// without a bias, z itself (which orders the scores).  Of G groups of neighbouring experts the best
+// `kept` by the sum of their one or two largest choice values (scores without a bias) stay;
+// of their experts the k largest c are chosen, ties to the lower id.  Weights: s of the chosen,
+// divided by their sum or not, times a factor.
+//
+// A wave takes a token; a lane holds NPL neighbouring experts, so that among equal values the first
+// lane of a ballot has the lowest id.  One read of the logits, k rounds of a wave-wide maximum:
+// bound by instructions, not by bytes.
+#include <algorithm>
+
+#include "row_ops.h"
+
+namespace moe {
+namespace {
+
+constexpr int RT_T = 256;  // threads, a wave per token
+constexpr int kMaxChoices = 16;
+constexpr int kMaxRouted = 1024;
+constexpr int kMaxRouteGroups = 64;
+constexpr int kMaxRouteT = 1 << 20;
+
+struct RouteArgs {
+  const void* z;
+  int64_t zs;
+  int T, E, score;
+  const float* bias;  // may be null
+  int G, best, kept, k, renorm;
+  float scale;
+  int* idx;
+  float* w;
+};
+
+// Keys that order as numbers do (without NaN); 0 is below every number's.
+__device__ __forceinline__ uint32_t key_of(float f) {
+  const uint32_t b = __float_as_uint(f + 0.f);  // -0 as 0
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t key_of(double f) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, f + 0.0);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+
+// The wave's largest, in every lane (an SGPR).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  const auto with = [&](uint32_t o) { v = v > o ? v : o; };
+  with(__builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr:1, 2, 4, 8
+  with(__builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // row_bcast:15, 31
+  with(__builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+  const uint32_t hi = wave_max((uint32_t)(v >> 32));
+  const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+template <class R>
+__device__ __forceinline__ R shfl_sum(R v, int width) {
+  for (int s = width / 2; s > 0; s >>= 1) v += __shfl_xor(v, s);
+  return v;
+}
+__device__ __forceinline__ float fmax_all(float v, int width) {
+  for (int s = width / 2; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
+  return v;
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  return __shfl(v, lane);
+}
+
+__device__ __forceinline__ float exp_fast(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504f);
+}
+__device__ __forceinline__ double exp_fast(double x) { return exp(x); }
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
+
+// Scores of the lane's experts (zmax: the largest logit, of softmax).
+template <class R, int NPL>
+__device__ __forceinline__ void route_scores(R (&s)[NPL], const float (&z)[NPL], int score,
+                                             float zmax) {
+  if (score == MOE_SCORE_SOFTMAX) {
+    R sum = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      s[i] = exp_fast((R)z[i] - (R)zmax);
+      sum += s[i];
+    }
+    const R inv = inverse(shfl_sum(sum, 64));
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) s[i] *= inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) s[i] = inverse((R)1 + exp_fast(-(R)z[i]));
+  }
+}
+
+// What a fp32 choice value may be off by: scores are off by less than 2^-20 (two roundings of exp's
+// argument, the sum, the reciprocal), the bias' addition adds half a step of c.
+__device__ __forceinline__ float choice_error(float c) { return 0x1p-19f * (1.f + fabsf(c)); }
+
+struct Chosen {
+  int idx;    // of lane j: choice j (j < found)
+  int found;  // uniform
+  bool sure;  // fp32: no two values that decide are closer than their errors
+};
+
+// Groups kept, as bits at each group's first lane: 64 / G2 lanes share a group, G2 = 2^g_log >= G.
+// c: [E] in LDS, -inf where an expert is not to be had.
+template <class R>
+__device__ __forceinline__ uint64_t kept_groups(const R* c, int E, int G, int g_log, int best,
+                                                int kept, int lane, bool& sure) {
+  const R none = -__builtin_inff();
+  const int per = 64 >> g_log, g = lane / per, size = E / G;
+  R m1 = none, m2 = none;
+  if (g < G)
+    for (int t = lane % per; t < size; t += per) {
+      const R v = c[g * size + t];
+      m2 = v > m1 ? m1 : v > m2 ? v : m2;
+      m1 = v > m1 ? v : m1;
+    }
+  for (int s = 1; s < per; s <<= 1) {
+    const R o1 = __shfl_xor(m1, s), o2 = __shfl_xor(m2, s);
+    const R low = m1 < o1 ? m1 : o1, up = m2 > o2 ? m2 : o2;
+    m1 = m1 > o1 ? m1 : o1;
+    m2 = low > up ? low : up;
+  }
+  R value = m1;
+  if (best == 2 && m2 > none) value += m2;
+  int rank = 0;
+  for (int o = 0; o < G; ++o) {
+    const R other = __shfl(value, o * per);
+    rank += other > value || (other == value && o < g);
+  }
+  const bool keep = g < G && rank < kept;
+  if constexpr (sizeof(R) == 4) {
+    float off = m1 > none ? choice_error(m1) : 0.f;
+    if (best == 2 && m2 > none) off += choice_error(m2);
+    const float low = keep ? value - off : __builtin_inff();
+    const float high = !keep && g < G ? value + off : none;
+    const float worst = -fmax_all(-low, 64), next = fmax_all(high, 64);
+    sure = kept >= G || worst > next;
+  }
+  return __ballot(keep && lane % per == 0);
+}
+
+// c: choice values, v: what groups are ranked by; out: experts that are not to be had.
+template <class R, int NPL>
+__device__ __forceinline__ Chosen choose(const RouteArgs& a, const R (&c)[NPL], const R (&v)[NPL],
+                                         const bool (&out)[NPL], R* s_c, int g_log,
+                                         const int (&group_lane)[NPL], int lane, bool check) {
+  Chosen r{-1, 0, true};
+  uint64_t groups = ~0ull;
+  if (a.G > 1) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (lane * NPL + i < a.E) s_c[lane * NPL + i] = out[i] ? (R)-__builtin_inff() : v[i];
+    asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
+    groups = kept_groups(s_c, a.E, a.G, g_log, a.best, a.kept, lane, r.sure);
+    asm volatile("" ::: "memory");
+  }
+  using Key = decltype(key_of(R()));
+  Key key[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    key[i] = out[i] || !(groups >> group_lane[i] & 1) ? 0 : key_of(c[i]);
+  Key own = 0, last = 0;
+  for (int j = 0; j <= a.k; ++j) {
+    Key m = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) {
+      at = key[i] > m ? i : at;
+      m = key[i] > m ? key[i] : m;
+    }
+    const Key top = wave_max(m);
+    if (j == a.k || top == 0) {
+      last = top;
+      break;
+    }
+    const int win = __builtin_ctzll(__ballot(m == top));
+    const int e = win * NPL + __builtin_amdgcn_readlane(at, win);
+    if (lane == j) {
+      r.idx = e;
+      own = top;
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (lane * NPL + i == e) key[i] = 0;
+    r.found = j + 1;
+  }
+  if constexpr (sizeof(R) == 4)
+    if (check) {
+      Key next = __shfl_down(own, 1);
+      next = lane == r.found - 1 ? last : next;
+      const float hi = value_of(own), lo = value_of(next);
+      const bool open = lane < r.found && next != 0 &&
+                        !(hi - lo > choice_error(hi) + choice_error(lo));
+      r.sure = r.sure && __ballot(open) == 0;
+    }
+  return r;
+}
+
+template <class E, int NPL>
+__device__ __forceinline__ void load_logits(float (&z)[NPL], const E* row, int lane, int n,
+                                            float fill) {
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) z[i] = fill;
+  if (lane * NPL >= n) return;
+  constexpr int B = NPL * (int)sizeof(E);
+  if (lane * NPL + NPL <= n && B >= 4) {
+    if constexpr (B >= 16) {
+      constexpr int V = kChunk<E>;
+#pragma unroll
+      for (int q = 0; q < NPL / V; ++q) {
+        const Chunk<E> c = load_chunk<V>(row + lane * NPL + q * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[q * V + i] = to_f32(c.e[i]);
+      }
+    } else if constexpr (B >= 4) {
+      struct Part {
+        E e[NPL];
+      };
+      typedef uint32_t part_t __attribute__((ext_vector_type(B / 4)));
+      typedef part_t part_any __attribute__((aligned(1)));
+      const Part p = __builtin_bit_cast(Part, (part_t) * (const part_any*)(row + lane * NPL));
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) z[i] = to_f32(p.e[i]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (lane * NPL + i < n) z[i] = to_f32(row[lane * NPL + i]);
+}
+
+// Logit of choice e; 64-bit score arithmetic on the few chosen.
+template <class E>
+__device__ __forceinline__ double sigmoid_f64(E z) {
+  return 1.0 / (1.0 + exp(-(double)z));
+}
+
+template <class E, int NPL>
+__global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a) {
+  __shared__ double s_choice[RT_T / 64][NPL * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float none = -__builtin_inff();
+  int g_log = 0;
+  while ((1 << g_log) < a.G) ++g_log;
+  float bias[NPL];
+  int group_lane[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = lane * NPL + i;
+    bias[i] = e >= a.E ? none : a.bias ? a.bias[e] : 0.f;
+    group_lane[i] = a.G > 1 && e < a.E ? e / (a.E / a.G) * (64 >> g_log) : 0;
+  }
+  const bool by_score = a.bias || (a.G > 1 && a.best == 2);
+  for (int t = blockIdx.x * (RT_T / 64) + wave; t < a.T; t += gridDim.x * (RT_T / 64)) {
+    const E* const row = (const E*)a.z + (int64_t)t * a.zs;
+    float z[NPL];
+    load_logits(z, row, lane, a.E, none);
+    float zmax = none;
+    bool out[NPL], nan = false;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      out[i] = z[i] == none || bias[i] == none;
+      zmax = fmaxf(zmax, z[i]);
+      nan |= z[i] != z[i] && (!out[i] || a.score == MOE_SCORE_SOFTMAX);
+      nan |= bias[i] != bias[i] && !out[i];
+      nan |= z[i] == __builtin_inff() && a.score == MOE_SCORE_SOFTMAX;
+    }
+    if (__ballot(nan)) {
+      if (lane < a.k) {
+        a.idx[(int64_t)t * a.k + lane] = lane;
+        a.w[(int64_t)t * a.k + lane] = __uint_as_float(0x7fc00000u);
+      }
+      continue;
+    }
+    if (a.score == MOE_SCORE_SOFTMAX) zmax = fmax_all(zmax, 64);
+    Chosen r;
+    if (by_score) {
+      float c[NPL], v[NPL];
+      route_scores(v, z, a.score, zmax);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        v[i] += bias[i];
+        c[i] = a.bias ? v[i] : z[i];
+      }
+      r = choose(a, c, v, out, (float*)s_choice[wave], g_log, group_lane, lane, a.bias != nullptr);
+      if (!r.sure) {  // values too close for fp32: 64 bits decide
+        double cd[NPL], vd[NPL];
+        route_scores(vd, z, a.score, zmax);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          vd[i] += (double)bias[i];
+          cd[i] = a.bias ? vd[i] : (double)z[i];
+        }
+        r = choose(a, cd, vd, out, s_choice[wave], g_log, group_lane, lane, false);
+      }
+    } else {
+      r = choose(a, z, z, out, (float*)s_choice[wave], g_log, group_lane, lane, false);
+    }
+    // the weights, in 64 bits: few enough
+    const bool has = lane < r.found;
+    const float zc = has ? to_f32(row[r.idx]) : none;
+    double w;
+    if (a.score == MOE_SCORE_SOFTMAX) {
+      double sum;
+      if (a.renorm) {
+        const float top = fmax_all(zc, kMaxChoices);
+        w = has ? exp((double)zc - (double)top) : 0.0;
+        sum = shfl_sum(w, kMaxChoices);
+      } else {
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) sum += exp((double)z[i] - (double)zmax);
+        sum = shfl_sum(sum, 64);
+        w = has ? exp((double)zc - (double)zmax) : 0.0;
+      }
+      w /= sum;
+    } else {
+      w = has ? sigmoid_f64(zc) : 0.0;
+      if (a.renorm) {
+        const double sum = shfl_sum(w, kMaxChoices);
+        w = sum > 0.0 ? w / sum : 0.0;
+      }
+    }
+    if (lane < a.k) {
+      a.idx[(int64_t)t * a.k + lane] = has ? r.idx : -1;
+      a.w[(int64_t)t * a.k + lane] = has ? (float)(w * (double)a.scale) : 0.f;
+    }
+  }
+}
+
+struct RouteGradArgs {
+  const void* z;
+  int64_t zs;
+  int T, E, score;
+  const int* idx;
+  int k, renorm;
+  float scale;
+  const float* dw;
+  void* dz;
+  int64_t dzs;
+};
+
+// With W the chosen scores divided by their sum and D = sum_j W_j dw_j: softmax renormalised
+// dz_j = f W_j (dw_j - D); sigmoid renormalised the same times (1 - s_j); sigmoid
+// dz_j = f s_j (1 - s_j) dw_j; softmax dz_e = f p_e (dw_e - sum_j p_j dw_j) for every expert (dw_e = 0
+// where e was not chosen), otherwise 0.  The chosen are few: 64 bits.  A wave per token writes its
+// row; the logits of the others are read where softmax needs them.
+template <class E, int NPL>
+__global__ __launch_bounds__(RT_T) void route_tokens_grad_kernel(RouteGradArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float none = -__builtin_inff();
+  const bool all = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
+  for (int t = blockIdx.x * (RT_T / 64) + wave; t < a.T; t += gridDim.x * (RT_T / 64)) {
+    const E* const row = (const E*)a.z + (int64_t)t * a.zs;
+    const int64_t at = (int64_t)t * a.k + lane;
+    const int e = lane < a.k ? a.idx[at] : -1;
+    const bool has = (unsigned)e < (unsigned)a.E;
+    const float zc = has ? to_f32(row[e]) : none;
+    const double dw = has ? (double)a.dw[at] * (double)a.scale : 0.0;
+    float dz[NPL];
+    double own;
+    if (a.score == MOE_SCORE_SOFTMAX) {
+      double w, along;
+      if (all) {
+        float z[NPL];
+        load_logits(z, row, lane, a.E, none);
+        float zmax = none;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) zmax = fmaxf(zmax, z[i]);
+        zmax = fmax_all(zmax, 64);
+        double p[NPL], sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          p[i] = z[i] == none ? 0.0 : exp((double)z[i] - (double)zmax);
+          sum += p[i];
+        }
+        sum = shfl_sum(sum, 64);
+        sum = sum == 0.0 ? 0.0 : 1.0 / sum;  // no expert at all: zeros
+        w = has ? exp((double)zc - (double)zmax) * sum : 0.0;
+        along = shfl_sum(w * dw, 64);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) dz[i] = (float)(-p[i] * sum * along);
+        own = w * (dw - along);
+      } else {
+        const float top = fmax_all(zc, 64);
+        w = has ? exp((double)zc - (double)top) : 0.0;
+        w /= shfl_sum(w, 64);
+        along = shfl_sum(w * dw, 64);
+        own = w * (dw - along);
+      }
+    } else {
+      const double s = has ? sigmoid_f64(zc) : 0.0, rest = has ? sigmoid_f64(-zc) : 0.0;
+      double w = s, along = 0.0;
+      if (a.renorm) {
+        const double sum = shfl_sum(s, 64);
+        w = sum > 0.0 ? s / sum : 0.0;
+        along = shfl_sum(w * dw, 64);
+      }
+      own = w * rest * (dw - along);
+    }
+    if (!all)
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) dz[i] = 0.f;
+    const float mine = (float)own;
+    for (int j = 0; j < a.k; ++j) {
+      const int ej = __builtin_amdgcn_readlane(e, j);
+      const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j));
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) dz[i] = lane * NPL + i == ej ? v : dz[i];
+    }
+    E* const out = (E*)a.dz + (int64_t)t * a.dzs + lane * NPL;
+    const int n = a.E - lane * NPL;
+    if constexpr (NPL >= kChunk<E>) {
+      if (n >= NPL) {
+#pragma unroll
+        for (int q = 0; q < NPL; q += kChunk<E>)
+          store_chunk(out + q, round_chunk<E, kChunk<E>>(dz + q));
+        continue;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (i < n) out[i] = from_f32<E>(dz[i]);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+constexpr int kRouteGrid = 256 * 8;
+unsigned route_grid(int T) {
+  return (unsigned)std::min((T + RT_T / 64 - 1) / (RT_T / 64), kRouteGrid);
+}
+
+template <class E>
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  const auto kernel = a.E <= 64    ? route_tokens_kernel<E, 1>
+                      : a.E <= 128 ? route_tokens_kernel<E, 2>
+                      : a.E <= 256 ? route_tokens_kernel<E, 4>
+                      : a.E <= 512 ? route_tokens_kernel<E, 8>
+                                   : route_tokens_kernel<E, 16>;
+  return launch_kernel(kernel, dim3(route_grid(a.T)), dim3(RT_T), 0, s, a);
+}
+template <class E>
+hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t s) {
+  const auto kernel = a.E <= 64    ? route_tokens_grad_kernel<E, 1>
+                      : a.E <= 128 ? route_tokens_grad_kernel<E, 2>
+                      : a.E <= 256 ? route_tokens_grad_kernel<E, 4>
+                      : a.E <= 512 ? route_tokens_grad_kernel<E, 8>
+                                   : route_tokens_grad_kernel<E, 16>;
+  return launch_kernel(kernel, dim3(route_grid(a.T)), dim3(RT_T), 0, s, a);
+}
+
+bool route_ok(int type, int T, int E, int score, int k, float scale) {
+  return float_type(type) && T >= 0 && T <= kMaxRouteT && E >= 1 && E <= kMaxRouted &&
+         (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID) && k >= 1 &&
+         k <= std::min(E, kMaxChoices) && scale - scale == 0.f;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_route_tokens(const void* logits, int64_t logits_stride, int32_t type, int32_t T,
+                            int32_t experts, int32_t score, const float* bias, int32_t groups,
+                            int32_t group_best, int32_t top_groups, int32_t top_k,
+                            int32_t renormalise, float scale, int32_t* topk_idx, float* topk_w,
+                            void* stream) {
+  if (!route_ok(type, T, experts, score, top_k, scale) || !aligned4(bias) || groups < 1 ||
+      groups > kMaxRouteGroups || experts % groups != 0 || group_best < 1 || group_best > 2 ||
+      top_groups < 1 || top_groups > groups)
+    return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;  // before the pointers: empty buffers have none
+  if (!rows_ok(logits, logits_stride, experts, type) || !topk_idx || !topk_w ||
+      !aligned4(topk_idx) || !aligned4(topk_w) || !on_current_device(topk_idx))
+    return MOE_E_INVALID;
+  // where every group stays there is nothing to rank
+  const int G = top_groups == groups ? 1 : groups;
+  RouteArgs a{logits, logits_stride, T, experts, score, bias, G, group_best, top_groups,
+              top_k, renormalise, scale, topk_idx, topk_w};
+  const hipStream_t s = (hipStream_t)stream;
+  if (type == MOE_T_BF16) return launched(launch_route<bf16_t>(a, s));
+  if (type == MOE_T_FP16) return launched(launch_route<fp16_t>(a, s));
+  return launched(launch_route<float>(a, s));
+}
+
+moe_status moe_route_tokens_grad(const void* logits, int64_t logits_stride, int32_t type,
+                                 int32_t T, int32_t experts, int32_t score,
+                                 const int32_t* topk_idx, int32_t top_k, int32_t renormalise,
+                                 float scale, const float* dweights, void* dlogits,
+                                 int64_t dlogits_stride, void* stream) {
+  if (!route_ok(type, T, experts, score, top_k, scale)) return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;  // before the pointers: empty buffers have none
+  if (!rows_ok(logits, logits_stride, experts, type) || !topk_idx || !dweights ||
+      !aligned4(topk_idx) || !aligned4(dweights) ||
+      !rows_ok(dlogits, dlogits_stride, experts, type) || !on_current_device(dlogits))
+    return MOE_E_INVALID;
+  RouteGradArgs a{logits, logits_stride, T, experts, score, topk_idx, top_k,
+                  renormalise, scale, dweights, dlogits, dlogits_stride};
+  const hipStream_t s = (hipStream_t)stream;
+  if (type == MOE_T_BF16) return launched(launch_route_grad<bf16_t>(a, s));
+  if (type == MOE_T_FP16) return launched(launch_route_grad<fp16_t>(a, s));
+  return launched(launch_route_grad<float>(a, s));
+}
+
+}  // extern "C"

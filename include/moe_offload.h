@@ -522,6 +522,39 @@ moe_status moe_norm_rows_grad(const void* dy, int64_t dy_stride, const void* dsu
                               void* dx, int64_t dx_stride, float* dweight, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* Experts and routing weights of T tokens from their logits [T][experts], for moe_sort_tokens.
+ * Scores s: MOE_SCORE_SOFTMAX over the row, or MOE_SCORE_SIGMOID of each logit.  The choice value c of
+ * an expert is s + bias ([experts] fp32, in 64 bits; it has no part in the weights) or, with
+ * bias NULL, its logit.  A logit or a bias of -infinity keeps the expert from being chosen.
+ * groups > 1 (it divides experts): of the groups of experts / groups neighbours only the top_groups
+ * with the largest sums of their group_best (1 or 2) largest choice values (scores, with bias
+ * NULL) stay; ties to the lower group.  Chosen are the top_k largest c, ties to the lower expert:
+ *   topk_idx [T][top_k]: the experts by descending c; -1 where fewer are to be had (the sort drops
+ *     these);
+ *   topk_w [T][top_k]: s of each, divided by their sum if renormalise (0 where the sum is 0), times
+ *     scale; 0 beside -1.
+ * Scores and weights are accurate to fp32, choices as in 64 bits.  A token with a NaN among its
+ * choice values (softmax: in its row, or an infinity of positive sign) has experts 0 .. top_k - 1 and
+ * weights NaN, so that what is computed from it is NaN.
+ * T 0..1048576, experts 1..1024, groups 1..64, top_k 1..min(16, experts); logits bf16, fp16, fp32. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+moe_status moe_route_tokens(const void* logits, int64_t logits_stride, int32_t type, int32_t T,
+                            int32_t experts, int32_t score, const float* bias, int32_t groups,
+                            int32_t group_best, int32_t top_groups, int32_t top_k,
+                            int32_t renormalise, float scale, int32_t* topk_idx, float* topk_w,
+                            void* stream);
+
+/* Gradient of moe_route_tokens' weights for the logits, dlogits [T][experts] of `type` (the choice
+ * itself has none): the logits and options of the forward call and the experts it chose; an id
+ * outside [0, experts) has no part, and a token's others have to be distinct.  With renormalise or
+ * sigmoid scores only the chosen logits have a gradient, the others get zeros. */
+moe_status moe_route_tokens_grad(const void* logits, int64_t logits_stride, int32_t type,
+                                 int32_t T, int32_t experts, int32_t score,
+                                 const int32_t* topk_idx, int32_t top_k, int32_t renormalise,
+                                 float scale, const float* dweights, void* dlogits,
+                                 int64_t dlogits_stride, void* stream);
+
 const char* moe_status_string(moe_status s);
 
 /* The hipError_t of the last MOE_E_HIP returned on this handle (0 if none). */
