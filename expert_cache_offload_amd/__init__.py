@@ -141,6 +141,8 @@ _SIGS = {
                                 _i32, _f32, _vp, _vp, _vp]),
     "moe_route_tokens_grad": (_i32, [_vp, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _f32, _vp,
                                      _vp, _i64, _vp]),
+    "moe_adapt_rows": (_i32, [_vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _vp,
+                              _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_i32]),
     "moe_last_hip_error": (_i32, [_vp]),
 }
@@ -575,6 +577,19 @@ def moe_route_tokens_grad(logits, logits_stride: int, type: int, T: int, experts
                                     _b(dlogits, size), dlogits_stride, stream)
     if st:
         _check(st, "moe_route_tokens_grad")
+
+
+def moe_adapt_rows(x, x_stride: int, type: int, M: int, K: int, a, a_stride: int, b, b_stride: int,
+                   N: int, rank: int, scale, adapters: int, offsets, order, base, base_stride: int,
+                   out, out_stride: int, stream: int = 0) -> None:
+    """Low-rank adapters of rows sorted by adapter, added to a shared projection (see the header)."""
+    size = _T_BYTES.get(type)
+    st = _lib.moe_adapt_rows(_b(x, size), x_stride, type, M, K, _b(a, size), a_stride, _b(b, size),
+                             b_stride, N, rank, _b(scale, 4), adapters, _b(offsets, 4),
+                             _b(order, 4), _b(base, size), base_stride, _b(out, size), out_stride,
+                             stream)
+    if st:
+        _check(st, "moe_adapt_rows")
 
 
 def moe_status_string(status: int) -> str:

@@ -555,6 +555,26 @@ moe_status moe_route_tokens_grad(const void* logits, int64_t logits_stride, int3
                                  float scale, const float* dweights, void* dlogits,
                                  int64_t dlogits_stride, void* stream);
 
+/* Low-rank adapters of many requests at once, added beside a projection that all rows share (a
+ * product's out): over rows sorted by adapter
+ *   out[m] = base[m] + scale[g] * (x[m] A_g^T) B_g^T
+ * x: [M][K]; a: [adapters][rank][K], a_stride from row to row (adapter g at a + g * rank * a_stride);
+ * b: [adapters][N][rank] likewise; an adapter of a lower rank has zeros behind it.  scale [adapters]
+ * fp32 (NULL: 1).  offsets: device words [adapters + 1], sorted rows offsets[g] .. offsets[g + 1] - 1
+ * have adapter g (ascending, within [0, M]; what lies outside is cut off); NULL: one adapter (adapters
+ * = 1) for all M rows.  order: the row of x, base and out of each sorted row (distinct; what lies
+ * outside [0, M) is left out); NULL: the rows lie sorted.  Both as moe_sort_tokens writes them with
+ * top_k = 1 from a row's adapter, an id outside [0, adapters) for none.
+ * base: [M][N], out itself, or NULL (nothing is added to).  Rows without an adapter are left as they
+ * were.  All matrices are of `type` (bf16, fp16 or fp32); x A^T is held in fp32 (16-bit types: 16 bits
+ * of it at least enter the second product).
+ * M 0..16777215, K and N 1..1048576, rank 1..128, adapters 1..1024. */
+moe_status moe_adapt_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
+                          const void* a, int64_t a_stride, const void* b, int64_t b_stride,
+                          int32_t N, int32_t rank, const float* scale, int32_t adapters,
+                          const int32_t* offsets, const int32_t* order, const void* base,
+                          int64_t base_stride, void* out, int64_t out_stride, void* stream);
+
 const char* moe_status_string(moe_status s);
 
 /* The hipError_t of the last MOE_E_HIP returned on this handle (0 if none). */
