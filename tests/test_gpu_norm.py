@@ -65,8 +65,10 @@ def _check(env, x, r, w, kind, o, eps=EPS):
     wide, got = o["y"]
     if got is not None:
         ref = h.double() * q * w.double()
-        # the factor and two products in fp32, then the output's own rounding (fp16's subnormal step)
-        tol = ref.abs() * (u + 4 * U32) + (2.0 ** -25 if kind == "fp16" else 2.0 ** -126)
+        # the factor and two products in fp32, then the output's own rounding (fp16's subnormal step);
+        # 16-bit rows add up eight squares at a time in fp32, four additions in sequence of two exact
+        # products each: 2^-22 of the sum, half of that of its root
+        tol = ref.abs() * (u + 6 * U32) + (2.0 ** -25 if kind == "fp16" else 2.0 ** -126)
         ok = (got.double() - ref).abs() <= tol
         ok |= torch.isnan(ref) & torch.isnan(got)
         assert bool(ok.all()), torch.nonzero(~ok)[:4].tolist()
@@ -77,7 +79,8 @@ def _check(env, x, r, w, kind, o, eps=EPS):
         assert torch.equal(got, codes), torch.nonzero(got != codes)[:4].tolist()
         assert _untouched(wide, M, K)
         ref = big * q[:, 0] / 127
-        torch.testing.assert_close(o["scale"][:M].double(), ref, rtol=2 * U32, atol=2.0 ** -149,
+        # 64 bits rounded once, and the sum's 2 U32 as above
+        torch.testing.assert_close(o["scale"][:M].double(), ref, rtol=4 * U32, atol=2.0 ** -149,
                                    equal_nan=True)
         assert float(o["scale"][M]) == 77
 
@@ -139,6 +142,25 @@ def test_norm_values(env, kind):
     keep = [i for i in range(64) if i not in (4, 9)]  # an infinite row is 0 but for its infinities
     o = _run(env, x[keep].contiguous(), None, w, kind)
     _check(env, x[keep].contiguous(), None, w, kind, o)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_norm_subnormals(env, kind):
+    """Rows whose sum of squares is made of subnormal numbers."""
+    torch, m, types, tid = env
+    K, t = 512, types[kind]
+    tiny = torch.finfo(t).smallest_normal
+    g = _gen(torch, 3)
+    x = torch.full((6, K), tiny / 2, dtype=torch.float64, device="cuda")
+    x[1, 5] = tiny
+    x[2] = tiny * torch.rand(K, generator=g, device="cuda")
+    x[3, ::2] = -tiny * 2
+    x[4, 0] = tiny * 64
+    x[5] /= 4
+    x = x.to(t)
+    w = torch.ones(K, device="cuda", dtype=t)
+    for eps in (1e-30, 1e-6):
+        _check(env, x, None, w, kind, _run(env, x, None, w, kind, eps=eps), eps)
 
 
 @pytest.mark.parametrize("kind", KINDS)
