@@ -42,27 +42,10 @@ constexpr int64_t kNormStreamBytes = 128 << 20;
 // A row is held by G lanes (beyond 64: by the whole workgroup).
 constexpr int norm_threads(int G) { return G < 256 ? 256 : G; }
 
-// A value of the lane's neighbour in a group of 2, 4, 8 or 16 lanes (each step joins groups that hold
-// equal values already, so mirrored lanes serve as well as exchanged ones).
-template <int CTRL, class T>
-__device__ __forceinline__ T dpp_neighbour(T v) {
-  if constexpr (sizeof(T) == 8) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_mov_dpp((uint32_t)b, CTRL, 0xf, 0xf, true);
-    const uint32_t hi = __builtin_amdgcn_mov_dpp((uint32_t)(b >> 32), CTRL, 0xf, 0xf, true);
-    return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
-  } else {
-    return __builtin_bit_cast(
-        T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(uint32_t, v), CTRL, 0xf, 0xf, true));
-  }
-}
 // v joined over the lanes of a row, in all of them.
 template <int G, class T, class Join>
 __device__ __forceinline__ T row_join(T v, T* s_part, Join&& join) {
-  v = join(v, dpp_neighbour<0xb1>(v));   // quad_perm 1, 0, 3, 2
-  v = join(v, dpp_neighbour<0x4e>(v));   // quad_perm 2, 3, 0, 1
-  v = join(v, dpp_neighbour<0x141>(v));  // row_half_mirror
-  v = join(v, dpp_neighbour<0x140>(v));  // row_mirror
+  v = join16(v, join);
 #pragma unroll
   for (int s = 16; s < (G < 64 ? G : 64); s <<= 1) v = join(v, __shfl_xor(v, s));
   if constexpr (G > 64) {

@@ -62,17 +62,21 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return (uint64_t)hi << 32 | lo;
 }
-template <class R>
-__device__ __forceinline__ R shfl_sum(R v, int width) {
-  for (int s = width / 2; s > 0; s >>= 1) v += __shfl_xor(v, s);
+// Over W neighbouring lanes (16 or 64), in all of them.
+template <int W, class T, class Join>
+__device__ __forceinline__ T join_lanes(T v, Join&& join) {
+  v = join16(v, join);
+#pragma unroll
+  for (int s = 16; s < W; s <<= 1) v = join(v, __shfl_xor(v, s));
   return v;
 }
-__device__ __forceinline__ float fmax_all(float v, int width) {
-  for (int s = width / 2; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
-  return v;
+template <int W, class R>
+__device__ __forceinline__ R sum_lanes(R v) {
+  return join_lanes<W>(v, [](R a, R b) { return a + b; });
 }
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  return __shfl(v, lane);
+template <int W>
+__device__ __forceinline__ float max_lanes(float v) {
+  return join_lanes<W>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 __device__ __forceinline__ float exp_fast(float x) {
@@ -93,7 +97,7 @@ __device__ __forceinline__ void route_scores(R (&s)[NPL], const float (&z)[NPL],
       s[i] = exp_fast((R)z[i] - (R)zmax);
       sum += s[i];
     }
-    const R inv = inverse(shfl_sum(sum, 64));
+    const R inv = inverse(sum_lanes<64>(sum));
 #pragma unroll
     for (int i = 0; i < NPL; ++i) s[i] *= inv;
   } else {
@@ -145,7 +149,7 @@ __device__ __forceinline__ uint64_t kept_groups(const R* c, int E, int G, int g_
     if (best == 2 && m2 > none) off += choice_error(m2);
     const float low = keep ? value - off : __builtin_inff();
     const float high = !keep && g < G ? value + off : none;
-    const float worst = -fmax_all(-low, 64), next = fmax_all(high, 64);
+    const float worst = -max_lanes<64>(-low), next = max_lanes<64>(high);
     sure = kept >= G || worst > next;
   }
   return __ballot(keep && lane % per == 0);
@@ -247,46 +251,71 @@ __device__ __forceinline__ double sigmoid_f64(E z) {
   return 1.0 / (1.0 + exp(-(double)z));
 }
 
-template <class E, int NPL>
-__global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a) {
-  __shared__ double s_choice[RT_T / 64][NPL * 64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// Choice `lane` of a token (has: there is one), by 16 neighbouring lanes: its weight in 64 bits, the
+// chosen being few.  zmax and sum: of softmax that is not renormalised.
+template <class E>
+__device__ __forceinline__ void write_choice(const RouteArgs& a, const E* row, int64_t at, int lane,
+                                             bool has, int e, float zmax, double sum) {
+  const float zc = has ? to_f32(row[e]) : -__builtin_inff();
+  double w;
+  if (a.score == MOE_SCORE_SOFTMAX) {
+    const float top = a.renorm ? max_lanes<kMaxChoices>(zc) : zmax;
+    w = has ? exp((double)zc - (double)top) : 0.0;
+    if (a.renorm) sum = sum_lanes<kMaxChoices>(w);
+    w /= sum;
+  } else {
+    w = has ? sigmoid_f64(zc) : 0.0;
+    if (a.renorm) {
+      sum = sum_lanes<kMaxChoices>(w);
+      w = sum > 0.0 ? w / sum : 0.0;
+    }
+  }
+  if (lane < a.k) {
+    a.idx[at] = has ? e : -1;
+    a.w[at] = has ? (float)(w * (double)a.scale) : 0.f;
+  }
+}
+
+// Choice values are scores (with a bias or not), not the logits alone.
+__device__ __forceinline__ bool by_score(const RouteArgs& a) {
+  return a.bias || (a.G > 1 && a.best == 2);
+}
+
+// Token t by a whole wave, each choice exact: fp32 (TRY) where no two values that decide are closer than
+// their errors, else 64 bits.  s_choice: NPL * 64 numbers of the wave's own.
+template <class E, int NPL, bool TRY>
+__device__ void route_exact(const RouteArgs& a, int t, double* s_choice, int lane) {
   const float none = -__builtin_inff();
+  const E* const row = (const E*)a.z + (int64_t)t * a.zs;
   int g_log = 0;
   while ((1 << g_log) < a.G) ++g_log;
-  float bias[NPL];
+  float z[NPL], bias[NPL], zmax = none;
   int group_lane[NPL];
+  load_logits(z, row, lane, a.E, none);
+  bool out[NPL], nan = false;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int e = lane * NPL + i;
     bias[i] = e >= a.E ? none : a.bias ? a.bias[e] : 0.f;
     group_lane[i] = a.G > 1 && e < a.E ? e / (a.E / a.G) * (64 >> g_log) : 0;
+    out[i] = z[i] == none || bias[i] == none;
+    zmax = fmaxf(zmax, z[i]);
+    nan |= z[i] != z[i] && (!out[i] || a.score == MOE_SCORE_SOFTMAX);
+    nan |= bias[i] != bias[i] && !out[i];
+    nan |= z[i] == __builtin_inff() && a.score == MOE_SCORE_SOFTMAX;
   }
-  const bool by_score = a.bias || (a.G > 1 && a.best == 2);
-  for (int t = blockIdx.x * (RT_T / 64) + wave; t < a.T; t += gridDim.x * (RT_T / 64)) {
-    const E* const row = (const E*)a.z + (int64_t)t * a.zs;
-    float z[NPL];
-    load_logits(z, row, lane, a.E, none);
-    float zmax = none;
-    bool out[NPL], nan = false;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      out[i] = z[i] == none || bias[i] == none;
-      zmax = fmaxf(zmax, z[i]);
-      nan |= z[i] != z[i] && (!out[i] || a.score == MOE_SCORE_SOFTMAX);
-      nan |= bias[i] != bias[i] && !out[i];
-      nan |= z[i] == __builtin_inff() && a.score == MOE_SCORE_SOFTMAX;
+  const int64_t at = (int64_t)t * a.k + lane;
+  if (__ballot(nan)) {
+    if (lane < a.k) {
+      a.idx[at] = lane;
+      a.w[at] = __uint_as_float(0x7fc00000u);
     }
-    if (__ballot(nan)) {
-      if (lane < a.k) {
-        a.idx[(int64_t)t * a.k + lane] = lane;
-        a.w[(int64_t)t * a.k + lane] = __uint_as_float(0x7fc00000u);
-      }
-      continue;
-    }
-    if (a.score == MOE_SCORE_SOFTMAX) zmax = fmax_all(zmax, 64);
-    Chosen r;
-    if (by_score) {
+    return;
+  }
+  if (a.score == MOE_SCORE_SOFTMAX) zmax = max_lanes<64>(zmax);
+  Chosen r;
+  if (by_score(a)) {
+    if constexpr (TRY) {
       float c[NPL], v[NPL];
       route_scores(v, z, a.score, zmax);
 #pragma unroll
@@ -294,50 +323,229 @@ __global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a) {
         v[i] += bias[i];
         c[i] = a.bias ? v[i] : z[i];
       }
-      r = choose(a, c, v, out, (float*)s_choice[wave], g_log, group_lane, lane, a.bias != nullptr);
-      if (!r.sure) {  // values too close for fp32: 64 bits decide
-        double cd[NPL], vd[NPL];
-        route_scores(vd, z, a.score, zmax);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          vd[i] += (double)bias[i];
-          cd[i] = a.bias ? vd[i] : (double)z[i];
-        }
-        r = choose(a, cd, vd, out, s_choice[wave], g_log, group_lane, lane, false);
-      }
-    } else {
-      r = choose(a, z, z, out, (float*)s_choice[wave], g_log, group_lane, lane, false);
+      r = choose(a, c, v, out, (float*)s_choice, g_log, group_lane, lane, a.bias != nullptr);
     }
-    // the weights, in 64 bits: few enough
-    const bool has = lane < r.found;
-    const float zc = has ? to_f32(row[r.idx]) : none;
-    double w;
+    if (!TRY || !r.sure) {
+      double cd[NPL], vd[NPL];
+      route_scores(vd, z, a.score, zmax);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        vd[i] += (double)bias[i];
+        cd[i] = a.bias ? vd[i] : (double)z[i];
+      }
+      r = choose(a, cd, vd, out, s_choice, g_log, group_lane, lane, false);
+    }
+  } else {
+    r = choose(a, z, z, out, (float*)s_choice, g_log, group_lane, lane, false);
+  }
+  double sum = 0.0;
+  if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) sum += exp((double)z[i] - (double)zmax);
+    sum = sum_lanes<64>(sum);
+  }
+  const bool has = lane < r.found;
+  write_choice(a, row, at, lane, has, r.idx, zmax, sum);
+}
+
+// A wave to every token, for sizes that the kernel below does not take.
+template <class E, int NPL>
+__global__ __launch_bounds__(RT_T) void route_tokens_wave_kernel(RouteArgs a) {
+  __shared__ double s_choice[RT_T / 64][NPL * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int t = blockIdx.x * (RT_T / 64) + wave; t < a.T; t += gridDim.x * (RT_T / 64))
+    route_exact<E, NPL, true>(a, t, s_choice[wave], lane);
+}
+
+// The nearest integer below, 0 for what is negative or no number.
+__device__ __forceinline__ uint32_t steps_of(float f) {
+  uint32_t u;
+  asm("v_cvt_u32_f32 %0, %1" : "=v"(u) : "v"(f));
+  return u;
+}
+
+// Four neighbouring elements of a row (the experts are a multiple of four and four of them a piece
+// of 8 or 16 bytes), or those that there are.
+template <class E>
+__device__ __forceinline__ void load_four(float* f, const E* p, int n, bool fours, float fill) {
+  if (fours) {
+    typedef uint32_t part_t __attribute__((ext_vector_type(sizeof(E))));
+    typedef part_t part_any __attribute__((aligned(1)));
+    struct Part {
+      E e[4];
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = fill;
+    if (n > 0) {
+      const Part q = __builtin_bit_cast(Part, (part_t) * (const part_any*)p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = to_f32(q.e[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = j < n ? to_f32(p[j]) : fill;
+  }
+}
+
+// Four tokens to a wave, 16 lanes each, a lane with n_lane (up to NE, a multiple of 4) neighbouring
+// experts.  A choice value becomes a number of up to 31 bits with the expert's id, inverted, in the
+// low ones: keys are distinct, the largest is the best choice, the next the largest below it, which
+// is the largest of key - last in 32 bits' arithmetic (keys above wrap to the lower half).
+// 16-bit logits go in whole and are exact.  Others go in as fixed-point distances from the row's
+// largest: equal or, of scores, too close ones (and NaN, and tokens with fewer experts than choices)
+// are left to route_exact; with values as they come about one token in a hundred.
+template <class E, int NE>
+__global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a, int n_lane, int id_bits,
+                                                            int group_lanes) {
+  constexpr int NPL = NE / 4;
+  // fixed point: with 9 bits of an id below 2^31; the largest is kTop, whose rounding leaves it inside
+  constexpr float kTop = (1 << 22) - (1 << 12);
+  __shared__ double s_choice[RT_T / 64][NPL * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane & 15;
+  const float none = -__builtin_inff(), inf = __builtin_inff();
+  const bool scores = by_score(a), whole = sizeof(E) == 2 && !a.bias, fours = a.E % 4 == 0;
+  const uint32_t id_mask = (1u << id_bits) - 1;
+  const int first = l * n_lane, mine = min(n_lane, a.E - first);  // this lane's experts
+  const int t = (blockIdx.x * (RT_T / 64) + wave) * 4 + (lane >> 4);
+  const E* const row = (const E*)a.z + (int64_t)min(t, a.T - 1) * a.zs;
+  float z[NE], v[NE];  // logits; scores, with the bias
+  uint32_t key[NE];
+#pragma unroll
+  for (int i = 0; i < NE; i += 4) load_four(z + i, row + first + i, mine - i, fours, none);
+  bool rest = false;  // left to route_exact
+  float zmax = none;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    rest |= !(z[i] < inf);
+    zmax = fmaxf(zmax, z[i]);
+  }
+  zmax = max_lanes<16>(zmax);
+  if (scores) {
     if (a.score == MOE_SCORE_SOFTMAX) {
-      double sum;
-      if (a.renorm) {
-        const float top = fmax_all(zc, kMaxChoices);
-        w = has ? exp((double)zc - (double)top) : 0.0;
-        sum = shfl_sum(w, kMaxChoices);
-      } else {
-        sum = 0.0;
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) sum += exp((double)z[i] - (double)zmax);
-        sum = shfl_sum(sum, 64);
-        w = has ? exp((double)zc - (double)zmax) : 0.0;
+      for (int i = 0; i < NE; ++i) {
+        v[i] = exp_fast(z[i] - zmax);
+        sum += v[i];
       }
-      w /= sum;
+      const float inv = inverse(sum_lanes<16>(sum));
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] *= inv;
     } else {
-      w = has ? sigmoid_f64(zc) : 0.0;
-      if (a.renorm) {
-        const double sum = shfl_sum(w, kMaxChoices);
-        w = sum > 0.0 ? w / sum : 0.0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = inverse(1.f + exp_fast(-z[i]));
+    }
+    float vmax = none;
+#pragma unroll
+    for (int i = 0; i < NE; i += 4) {
+      float bias[4] = {0.f, 0.f, 0.f, 0.f};
+      if (a.bias) load_four(bias, a.bias + first + i, mine - i, fours, none);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[i + j] = z[i + j] > none ? v[i + j] + bias[j] : none;
+        rest |= !(v[i + j] < inf);
+        vmax = fmaxf(vmax, v[i + j]);
       }
     }
-    if (lane < a.k) {
-      a.idx[(int64_t)t * a.k + lane] = has ? r.idx : -1;
-      a.w[(int64_t)t * a.k + lane] = has ? (float)(w * (double)a.scale) : 0.f;
+    if (a.bias) zmax = max_lanes<16>(vmax);
+  }
+  // values down to `far` below the largest in steps; twice the error of scores that near, in steps,
+  // and the roundings to these; a largest whose own steps are not exact enough is left too
+  const float far = a.bias ? 2.f : 32.f, step = 0x1p22f / far;
+  rest |= !(fabsf(zmax) < 1024.f);
+  const uint32_t close =
+      a.bias ? (uint32_t)(2.f * choice_error(fabsf(zmax) + 2.f) * step + 4.f) : 0u;
+  float top_step = kTop - zmax * step;
+  bool keep = true;
+  if (a.G > 1) {
+    // the groups' one or two largest: of group_lanes lanes each
+    float m1 = none, m2 = none;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const float c = scores ? v[i] : z[i];
+      m2 = __builtin_amdgcn_fmed3f(m1, m2, c);
+      m1 = fmaxf(m1, c);
+    }
+    for (int s = 1; s < group_lanes; s <<= 1) {
+      const float o1 = __shfl_xor(m1, s), o2 = __shfl_xor(m2, s);
+      m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+      m1 = fmaxf(m1, o1);
+    }
+    float value = m1, off = 0.f;
+    if (scores) {
+      off = choice_error(m1);
+      if (a.best == 2) {
+        value += m2 > none ? m2 : 0.f;
+        off += m2 > none ? choice_error(m2) : 0.f;
+      }
+    }
+    const int g = l / group_lanes;
+    int rank = 0;
+    for (int o = 0; o < a.G; ++o) {
+      const float other = __shfl(value, (lane & 48) + o * group_lanes);
+      rank += other > value || (other == value && o < g);
+    }
+    const bool in = g < a.G;
+    keep = in && rank < a.kept;
+    if (scores) {
+      const float low = -max_lanes<16>(keep ? off - value : none);
+      const float high = max_lanes<16>(in && !keep ? value + off : none);
+      rest |= !(low > high);
     }
   }
+  const uint32_t id0 = id_mask - (uint32_t)first;
+  if (whole) {
+    constexpr int DROP = __is_same(E, bf16_t) ? 16 : 13;  // bits that these types leave zero
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      key[i] = keep ? (((key_of(z[i]) >> DROP) - (key_of(none) >> DROP)) << id_bits) +
+                          (id0 - i & id_mask)
+                    : 0u;
+  } else {
+    if (!keep) top_step = none;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      key[i] = (steps_of(fmaf(a.bias ? v[i] : z[i], step, top_step)) << id_bits) +
+               (id0 - i & id_mask);
+  }
+  uint32_t top = 1u << 31, own = 0;
+  for (int j = 0; j <= a.k; ++j) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) m = max(m, key[i] - top);
+    top += join16(m, [](uint32_t x, uint32_t y) { return max(x, y); });
+    own = l == j ? top : own;  // k = 16: the one behind the last stays in top
+  }
+  // where the keys ran out (id bits alone) all that follows does not count
+  const uint64_t out = __ballot(own <= id_mask) >> (lane & 48) & 0xffff;
+  const bool has = l < a.k && (out & ((2u << l) - 1)) == 0;
+  if (!whole) {
+    uint32_t next = __shfl_down(own, 1);
+    next = l == 15 ? top : next;
+    rest |= l < a.k && (!has || (own >> id_bits) - (next >> id_bits) <= close);
+  }
+  const uint64_t left = __ballot(rest);
+  const bool fast = (left >> (lane & 48) & 0xffff) == 0 && t < a.T;
+  double sum = 0.0;
+  if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
+    if (a.bias) {  // zmax is the choice values' now
+      zmax = none;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) zmax = fmaxf(zmax, z[i]);
+      zmax = max_lanes<16>(zmax);
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) sum += exp((double)z[i] - (double)zmax);
+    sum = sum_lanes<16>(sum);
+  }
+  write_choice(a, row, (int64_t)t * a.k + l, fast ? l : 16, has && fast,
+               (int)(id_mask - (own & id_mask)), zmax, sum);
+  for (int q = 0; q < 4; ++q)
+    if (left >> (16 * q) & 0xffff) {
+      const int tq = (blockIdx.x * (RT_T / 64) + wave) * 4 + q;
+      if (tq < a.T) route_exact<E, NPL, false>(a, tq, s_choice[wave], lane);
+    }
 }
 
 struct RouteGradArgs {
@@ -379,34 +587,34 @@ __global__ __launch_bounds__(RT_T) void route_tokens_grad_kernel(RouteGradArgs a
         float zmax = none;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) zmax = fmaxf(zmax, z[i]);
-        zmax = fmax_all(zmax, 64);
+        zmax = max_lanes<64>(zmax);
         double p[NPL], sum = 0.0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
           p[i] = z[i] == none ? 0.0 : exp((double)z[i] - (double)zmax);
           sum += p[i];
         }
-        sum = shfl_sum(sum, 64);
+        sum = sum_lanes<64>(sum);
         sum = sum == 0.0 ? 0.0 : 1.0 / sum;  // no expert at all: zeros
         w = has ? exp((double)zc - (double)zmax) * sum : 0.0;
-        along = shfl_sum(w * dw, 64);
+        along = sum_lanes<64>(w * dw);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) dz[i] = (float)(-p[i] * sum * along);
         own = w * (dw - along);
       } else {
-        const float top = fmax_all(zc, 64);
+        const float top = max_lanes<64>(zc);
         w = has ? exp((double)zc - (double)top) : 0.0;
-        w /= shfl_sum(w, 64);
-        along = shfl_sum(w * dw, 64);
+        w /= sum_lanes<64>(w);
+        along = sum_lanes<64>(w * dw);
         own = w * (dw - along);
       }
     } else {
       const double s = has ? sigmoid_f64(zc) : 0.0, rest = has ? sigmoid_f64(-zc) : 0.0;
       double w = s, along = 0.0;
       if (a.renorm) {
-        const double sum = shfl_sum(s, 64);
+        const double sum = sum_lanes<64>(s);
         w = sum > 0.0 ? s / sum : 0.0;
-        along = shfl_sum(w * dw, 64);
+        along = sum_lanes<64>(w * dw);
       }
       own = w * rest * (dw - along);
     }
@@ -445,11 +653,31 @@ unsigned route_grid(int T) {
 
 template <class E>
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  const auto kernel = a.E <= 64    ? route_tokens_kernel<E, 1>
-                      : a.E <= 128 ? route_tokens_kernel<E, 2>
-                      : a.E <= 256 ? route_tokens_kernel<E, 4>
-                      : a.E <= 512 ? route_tokens_kernel<E, 8>
-                                   : route_tokens_kernel<E, 16>;
+  // experts of a lane: with groups, so many that a group has 1, 2, 4, 8 or 16 lanes
+  int n_lane = (a.E + 63) / 64 * 4, group_lanes = 1;
+  if (a.G > 1) {
+    const int size = a.E / a.G;
+    n_lane = 0;
+    for (group_lanes = 16; group_lanes > 1; group_lanes >>= 1)
+      if (size % (4 * group_lanes) == 0 && a.G * group_lanes <= 16) break;
+    if (size % (4 * group_lanes) == 0 && a.G * group_lanes <= 16) n_lane = size / group_lanes;
+  }
+  int id_bits = 1;
+  while ((1 << id_bits) < a.E) ++id_bits;
+  if (n_lane > 0 && n_lane <= 32) {
+    const auto kernel = n_lane <= 4    ? route_tokens_kernel<E, 4>
+                        : n_lane <= 8  ? route_tokens_kernel<E, 8>
+                        : n_lane <= 16 ? route_tokens_kernel<E, 16>
+                                       : route_tokens_kernel<E, 32>;
+    constexpr int tokens = RT_T / 16;
+    return launch_kernel(kernel, dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(RT_T), 0, s, a,
+                         n_lane, id_bits, group_lanes);
+  }
+  const auto kernel = a.E <= 64    ? route_tokens_wave_kernel<E, 1>
+                      : a.E <= 128 ? route_tokens_wave_kernel<E, 2>
+                      : a.E <= 256 ? route_tokens_wave_kernel<E, 4>
+                      : a.E <= 512 ? route_tokens_wave_kernel<E, 8>
+                                   : route_tokens_wave_kernel<E, 16>;
   return launch_kernel(kernel, dim3(route_grid(a.T)), dim3(RT_T), 0, s, a);
 }
 template <class E>

@@ -236,6 +236,29 @@ __device__ __forceinline__ uint32_t chunk_max_bits(const Chunk<E, V>& c, uint32_
   return m;
 }
 
+// A value of the lane's neighbour in a group of 2, 4, 8 or 16 lanes (each step joins groups that hold
+// equal values already, so mirrored lanes serve as well as exchanged ones).
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp_neighbour(T v) {
+  if constexpr (sizeof(T) == 8) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((uint32_t)b, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((uint32_t)(b >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+  } else {
+    return __builtin_bit_cast(
+        T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(uint32_t, v), CTRL, 0xf, 0xf, true));
+  }
+}
+// v joined over 16 neighbouring lanes, in all of them.
+template <class T, class Join>
+__device__ __forceinline__ T join16(T v, Join&& join) {
+  v = join(v, dpp_neighbour<0xb1>(v));      // quad_perm 1, 0, 3, 2
+  v = join(v, dpp_neighbour<0x4e>(v));      // quad_perm 2, 3, 0, 1
+  v = join(v, dpp_neighbour<0x141>(v));     // row_half_mirror
+  return join(v, dpp_neighbour<0x140>(v));  // row_mirror
+}
+
 // The largest of m over groups of G neighbouring lanes (G <= 64).
 template <int G>
 __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {

@@ -84,7 +84,9 @@ ROUTES = [  # T, E, k, groups, kept, padding, share masked
     (1000, 60, 4, 6, 2, 1, 0.0), (5, 1024, 16, 16, 3, 0, 0.0), (33, 65, 3, 5, 2, 3, 0.3),
     (700, 257, 8, 1, 1, 0, 0.2), (100, 512, 10, 64, 7, 8, 0.9), (20001, 8, 2, 4, 1, 0, 0.0),
     (300, 384, 6, 3, 1, 0, 0.1), (64, 16, 16, 16, 16, 5, 0.5), (50, 130, 5, 13, 12, 0, 0.0),
-    (3, 1000, 7, 50, 9, 1, 0.05), (9000, 128, 8, 2, 1, 0, 0.0)]
+    (3, 1000, 7, 50, 9, 1, 0.05), (9000, 128, 8, 2, 1, 0, 0.0),
+    (3001, 160, 6, 8, 3, 0, 0.0), (2050, 256, 8, 8, 4, 3, 0.1), (77, 64, 12, 4, 2, 0, 0.2),
+    (130, 96, 4, 1, 1, 0, 0.0), (9, 512, 16, 16, 4, 0, 0.0)]
 
 
 @pytest.mark.parametrize("T,E,k,G,kept,pad,masked", ROUTES)
