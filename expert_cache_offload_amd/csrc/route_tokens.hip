@@ -106,9 +106,14 @@ __device__ __forceinline__ void route_scores(R (&s)[NPL], const float (&z)[NPL],
   }
 }
 
-// What a fp32 choice value may be off by: scores are off by less than 2^-20 (two roundings of exp's
-// argument, the sum, the reciprocal), the bias' addition adds half a step of c.
-__device__ __forceinline__ float choice_error(float c) { return 0x1p-19f * (1.f + fabsf(c)); }
+// What a fp32 choice value may be off by, in units of 1 + |c|.  exp's argument x is off by 1.5 |x| 2^-24
+// (2.5 below the row's largest), exp and the reciprocal by 2^-23 of themselves.  A sigmoid's
+// s (1 - s) |x| and s (1 - s) stay below 1 / 4, so it is off by less than 2^-22; softmax has its sum in
+// fp32 over up to 22 additions in sequence, less than 2^-19, or in 64 bits, less than 2^-21.  The
+// bias' addition adds half a step of c.
+__device__ __forceinline__ float error_unit(int score, bool sum_f64) {
+  return score == MOE_SCORE_SIGMOID ? 0x1p-22f : sum_f64 ? 0x1p-21f : 0x1p-19f;
+}
 
 struct Chosen {
   int idx;    // of lane j: choice j (j < found)
@@ -120,7 +125,7 @@ struct Chosen {
 // c: [E] in LDS, -inf where an expert is not to be had.
 template <class R>
 __device__ __forceinline__ uint64_t kept_groups(const R* c, int E, int G, int g_log, int best,
-                                                int kept, int lane, bool& sure) {
+                                                int kept, int lane, float unit, bool& sure) {
   const R none = -__builtin_inff();
   const int per = 64 >> g_log, g = lane / per, size = E / G;
   R m1 = none, m2 = none;
@@ -145,8 +150,8 @@ __device__ __forceinline__ uint64_t kept_groups(const R* c, int E, int G, int g_
   }
   const bool keep = g < G && rank < kept;
   if constexpr (sizeof(R) == 4) {
-    float off = m1 > none ? choice_error(m1) : 0.f;
-    if (best == 2 && m2 > none) off += choice_error(m2);
+    float off = m1 > none ? unit * (1.f + fabsf(m1)) : 0.f;
+    if (best == 2 && m2 > none) off += unit * (1.f + fabsf(m2));
     const float low = keep ? value - off : __builtin_inff();
     const float high = !keep && g < G ? value + off : none;
     const float worst = -max_lanes<64>(-low), next = max_lanes<64>(high);
@@ -167,7 +172,8 @@ __device__ __forceinline__ Chosen choose(const RouteArgs& a, const R (&c)[NPL], 
     for (int i = 0; i < NPL; ++i)
       if (lane * NPL + i < a.E) s_c[lane * NPL + i] = out[i] ? (R)-__builtin_inff() : v[i];
     asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
-    groups = kept_groups(s_c, a.E, a.G, g_log, a.best, a.kept, lane, r.sure);
+    groups = kept_groups(s_c, a.E, a.G, g_log, a.best, a.kept, lane,
+                         error_unit(a.score, false), r.sure);
     asm volatile("" ::: "memory");
   }
   using Key = decltype(key_of(R()));
@@ -206,7 +212,7 @@ __device__ __forceinline__ Chosen choose(const RouteArgs& a, const R (&c)[NPL], 
       next = lane == r.found - 1 ? last : next;
       const float hi = value_of(own), lo = value_of(next);
       const bool open = lane < r.found && next != 0 &&
-                        !(hi - lo > choice_error(hi) + choice_error(lo));
+                        !(hi - lo > error_unit(a.score, false) * (2.f + fabsf(hi) + fabsf(lo)));
       r.sure = r.sure && __ballot(open) == 0;
     }
   return r;
@@ -267,7 +273,7 @@ __device__ __forceinline__ void write_choice(const RouteArgs& a, const E* row, i
     w = has ? sigmoid_f64(zc) : 0.0;
     if (a.renorm) {
       sum = sum_lanes<kMaxChoices>(w);
-      w = sum > 0.0 ? w / sum : 0.0;
+      w = sum == 0.0 ? 0.0 : w / sum;
     }
   }
   if (lane < a.k) {
@@ -387,13 +393,44 @@ __device__ __forceinline__ void load_four(float* f, const E* p, int n, bool four
   }
 }
 
+// Rank among the G groups of a token's 16 lanes, group_lanes each, by their one or two largest values:
+// of this lane's group.  m1 >= m2: the lane's own two largest.
+template <class R>
+__device__ __forceinline__ int group_rank(R& m1, R& m2, const RouteArgs& a, int group_lanes,
+                                          int lane) {
+  const R none = -__builtin_inff();
+  for (int s = 1; s < group_lanes; s <<= 1) {
+    const R o1 = __shfl_xor(m1, s), o2 = __shfl_xor(m2, s);
+    const R low = m1 < o1 ? m1 : o1, up = m2 > o2 ? m2 : o2;
+    m1 = m1 > o1 ? m1 : o1;
+    m2 = low > up ? low : up;
+  }
+  const R value = a.best == 2 && m2 > none ? m1 + m2 : m1;
+  const int g = (lane & 15) / group_lanes;
+  int rank = 0;
+  for (int o = 0; o < a.G; ++o) {
+    const R other = __shfl(value, (lane & 48) + o * group_lanes);
+    rank += other > value || (other == value && o < g);
+  }
+  return rank;
+}
+
+// A choice value in 64 bits (zmax, sum: of softmax).
+__device__ __forceinline__ double choice_f64(const RouteArgs& a, float z, int e, float zmax,
+                                             double sum) {
+  const double s = a.score == MOE_SCORE_SOFTMAX ? exp((double)z - (double)zmax) / sum
+                                                : sigmoid_f64(z);
+  return s + (a.bias ? (double)a.bias[e] : 0.0);
+}
+
 // Four tokens to a wave, 16 lanes each, a lane with n_lane (up to NE, a multiple of 4) neighbouring
 // experts.  A choice value becomes a number of up to 31 bits with the expert's id, inverted, in the
 // low ones: keys are distinct, the largest is the best choice, the next the largest below it, which
 // is the largest of key - last in 32 bits' arithmetic (keys above wrap to the lower half).
 // 16-bit logits go in whole and are exact.  Others go in as fixed-point distances from the row's
-// largest: equal or, of scores, too close ones (and NaN, and tokens with fewer experts than choices)
-// are left to route_exact; with values as they come about one token in a hundred.
+// largest; where some of the k + 1 best are equal or, of scores, too close, these are ranked in 64
+// bits, and so are groups that are too close.  What else may be wrong (the border among more than two
+// experts, NaN, fewer experts than choices) is left to route_exact.
 template <class E, int NE>
 __global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a, int n_lane, int id_bits,
                                                             int group_lanes) {
@@ -421,17 +458,19 @@ __global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a, int n_l
     zmax = fmaxf(zmax, z[i]);
   }
   zmax = max_lanes<16>(zmax);
+  float cmax = zmax;  // the largest of what is ranked
+  double sum = 1.0;
+  if (a.score == MOE_SCORE_SOFTMAX && (scores || !a.renorm)) {
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) sum += exp((double)z[i] - (double)zmax);
+    sum = sum_lanes<16>(sum);
+  }
   if (scores) {
     if (a.score == MOE_SCORE_SOFTMAX) {
-      float sum = 0.f;
+      const float inv = (float)(1.0 / sum);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        v[i] = exp_fast(z[i] - zmax);
-        sum += v[i];
-      }
-      const float inv = inverse(sum_lanes<16>(sum));
-#pragma unroll
-      for (int i = 0; i < NE; ++i) v[i] *= inv;
+      for (int i = 0; i < NE; ++i) v[i] = exp_fast(z[i] - zmax) * inv;
     } else {
 #pragma unroll
       for (int i = 0; i < NE; ++i) v[i] = inverse(1.f + exp_fast(-z[i]));
@@ -448,18 +487,11 @@ __global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a, int n_l
         vmax = fmaxf(vmax, v[i + j]);
       }
     }
-    if (a.bias) zmax = max_lanes<16>(vmax);
+    if (a.bias) cmax = max_lanes<16>(vmax);
   }
-  // values down to `far` below the largest in steps; twice the error of scores that near, in steps,
-  // and the roundings to these; a largest whose own steps are not exact enough is left too
-  const float far = a.bias ? 2.f : 32.f, step = 0x1p22f / far;
-  rest |= !(fabsf(zmax) < 1024.f);
-  const uint32_t close =
-      a.bias ? (uint32_t)(2.f * choice_error(fabsf(zmax) + 2.f) * step + 4.f) : 0u;
-  float top_step = kTop - zmax * step;
+  const float unit = error_unit(a.score, true);
   bool keep = true;
   if (a.G > 1) {
-    // the groups' one or two largest: of group_lanes lanes each
     float m1 = none, m2 = none;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
@@ -467,33 +499,36 @@ __global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a, int n_l
       m2 = __builtin_amdgcn_fmed3f(m1, m2, c);
       m1 = fmaxf(m1, c);
     }
-    for (int s = 1; s < group_lanes; s <<= 1) {
-      const float o1 = __shfl_xor(m1, s), o2 = __shfl_xor(m2, s);
-      m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-      m1 = fmaxf(m1, o1);
-    }
-    float value = m1, off = 0.f;
+    const bool in = l < a.G * group_lanes;
+    keep = group_rank(m1, m2, a, group_lanes, lane) < a.kept && in;
     if (scores) {
-      off = choice_error(m1);
-      if (a.best == 2) {
-        value += m2 > none ? m2 : 0.f;
-        off += m2 > none ? choice_error(m2) : 0.f;
+      float value = m1, off = unit * (1.f + fabsf(m1));
+      if (a.best == 2 && m2 > none) {
+        value += m2;
+        off += unit * (1.f + fabsf(m2));
       }
-    }
-    const int g = l / group_lanes;
-    int rank = 0;
-    for (int o = 0; o < a.G; ++o) {
-      const float other = __shfl(value, (lane & 48) + o * group_lanes);
-      rank += other > value || (other == value && o < g);
-    }
-    const bool in = g < a.G;
-    keep = in && rank < a.kept;
-    if (scores) {
       const float low = -max_lanes<16>(keep ? off - value : none);
       const float high = max_lanes<16>(in && !keep ? value + off : none);
-      rest |= !(low > high);
+      if (__ballot(!(low > high))) {
+        double d1 = none, d2 = none;
+#pragma unroll 4
+        for (int i = 0; i < mine; ++i) {
+          const float zi = to_f32(row[first + i]);
+          double c = choice_f64(a, zi, first + i, zmax, sum);
+          c = zi > none ? c : (double)none;
+          const double low = d1 < c ? d1 : c;
+          d2 = d2 > low ? d2 : low;
+          d1 = d1 > c ? d1 : c;
+        }
+        keep = group_rank(d1, d2, a, group_lanes, lane) < a.kept && in;
+      }
     }
   }
+  // values down to 2 (logits: 32) below the largest in steps; twice the error of scores that near, in
+  // steps, and the roundings to these; a largest whose own steps are not exact enough is left
+  const float step = a.bias ? 0x1p21f : 0x1p17f;
+  rest |= !(fabsf(cmax) < 1024.f);
+  const uint32_t close = a.bias ? (uint32_t)(2.f * unit * (3.f + fabsf(cmax)) * step + 4.f) : 0u;
   const uint32_t id0 = id_mask - (uint32_t)first;
   if (whole) {
     constexpr int DROP = __is_same(E, bf16_t) ? 16 : 13;  // bits that these types leave zero
@@ -503,44 +538,50 @@ __global__ __launch_bounds__(RT_T) void route_tokens_kernel(RouteArgs a, int n_l
                           (id0 - i & id_mask)
                     : 0u;
   } else {
-    if (!keep) top_step = none;
+    const float top_step = keep ? kTop - cmax * step : none;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       key[i] = (steps_of(fmaf(a.bias ? v[i] : z[i], step, top_step)) << id_bits) +
                (id0 - i & id_mask);
   }
-  uint32_t top = 1u << 31, own = 0;
-  for (int j = 0; j <= a.k; ++j) {
+  uint32_t top = 1u << 31, own = 0;  // own: lane j's the j-th best
+  for (int j = 0; j <= a.k + 1; ++j) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < NE; ++i) m = max(m, key[i] - top);
     top += join16(m, [](uint32_t x, uint32_t y) { return max(x, y); });
-    own = l == j ? top : own;  // k = 16: the one behind the last stays in top
+    own = l == j ? top : own;
   }
   // where the keys ran out (id bits alone) all that follows does not count
   const uint64_t out = __ballot(own <= id_mask) >> (lane & 48) & 0xffff;
-  const bool has = l < a.k && (out & ((2u << l) - 1)) == 0;
+  const bool valid = l <= a.k && (out & ((2u << l) - 1)) == 0;
+  const int e = (int)(id_mask - (own & id_mask));
+  int place = l;
   if (!whole) {
-    uint32_t next = __shfl_down(own, 1);
-    next = l == 15 ? top : next;
-    rest |= l < a.k && (!has || (own >> id_bits) - (next >> id_bits) <= close);
+    const uint32_t f = own >> id_bits, next = __shfl_down(own, 1) >> id_bits;
+    rest |= l < a.k && !valid;
+    // the one behind the k + 1 best, which are ranked below, is far enough from the k-th
+    rest |= l == a.k - 1 && f - (top >> id_bits) <= close;
+    const bool next_valid = (out & ((4u << l) - 1)) == 0;
+    if (__ballot(l < a.k && valid && next_valid && f - next <= close)) {
+      double c = none;
+      if (valid) {
+        const float zc = to_f32(row[e]);
+        c = a.bias ? choice_f64(a, zc, e, zmax, sum) : (double)zc;
+      }
+      int rank = 0;
+      for (int j = 0; j <= a.k; ++j) {
+        const double oc = __shfl(c, (lane & 48) + j);
+        const int oe = __shfl(e, (lane & 48) + j);
+        rank += oc > c || (oc == c && oe < e);
+      }
+      place = l <= a.k ? rank : l;
+    }
   }
   const uint64_t left = __ballot(rest);
   const bool fast = (left >> (lane & 48) & 0xffff) == 0 && t < a.T;
-  double sum = 0.0;
-  if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
-    if (a.bias) {  // zmax is the choice values' now
-      zmax = none;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) zmax = fmaxf(zmax, z[i]);
-      zmax = max_lanes<16>(zmax);
-    }
-#pragma unroll
-    for (int i = 0; i < NE; ++i) sum += exp((double)z[i] - (double)zmax);
-    sum = sum_lanes<16>(sum);
-  }
-  write_choice(a, row, (int64_t)t * a.k + l, fast ? l : 16, has && fast,
-               (int)(id_mask - (own & id_mask)), zmax, sum);
+  const bool has = valid && place < a.k && fast;
+  write_choice(a, row, (int64_t)t * a.k + place, fast ? place : 16, has, e, zmax, sum);
   for (int q = 0; q < 4; ++q)
     if (left >> (16 * q) & 0xffff) {
       const int tq = (blockIdx.x * (RT_T / 64) + wave) * 4 + q;
@@ -563,84 +604,99 @@ struct RouteGradArgs {
 // With W the chosen scores divided by their sum and D = sum_j W_j dw_j: softmax renormalised
 // dz_j = f W_j (dw_j - D); sigmoid renormalised the same times (1 - s_j); sigmoid
 // dz_j = f s_j (1 - s_j) dw_j; softmax dz_e = f p_e (dw_e - sum_j p_j dw_j) for every expert (dw_e = 0
-// where e was not chosen), otherwise 0.  The chosen are few: 64 bits.  A wave per token writes its
-// row; the logits of the others are read where softmax needs them.
-template <class E, int NPL>
-__global__ __launch_bounds__(RT_T) void route_tokens_grad_kernel(RouteGradArgs a) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// where e was not chosen), otherwise 0.  The chosen are few: 64 bits, four tokens to a wave, 16 lanes
+// each.  A token's row is put together in LDS (the logits of the others are read where softmax needs
+// them, their exponentials held there in fp32) and written in 16-byte pieces.
+template <class E>
+__global__ __launch_bounds__(RT_T) void route_tokens_grad_kernel(RouteGradArgs a, int pitch) {
+  constexpr int V = kChunk<E>;
+  extern __shared__ __align__(16) float s_rows[];  // [RT_T / 16][pitch], pitch a multiple of V
+  const int l = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const float none = -__builtin_inff();
   const bool all = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
-  for (int t = blockIdx.x * (RT_T / 64) + wave; t < a.T; t += gridDim.x * (RT_T / 64)) {
-    const E* const row = (const E*)a.z + (int64_t)t * a.zs;
-    const int64_t at = (int64_t)t * a.k + lane;
-    const int e = lane < a.k ? a.idx[at] : -1;
-    const bool has = (unsigned)e < (unsigned)a.E;
-    const float zc = has ? to_f32(row[e]) : none;
-    const double dw = has ? (double)a.dw[at] * (double)a.scale : 0.0;
-    float dz[NPL];
-    double own;
-    if (a.score == MOE_SCORE_SOFTMAX) {
-      double w, along;
-      if (all) {
-        float z[NPL];
-        load_logits(z, row, lane, a.E, none);
-        float zmax = none;
+  const int tokens = RT_T / 16, t = min(blockIdx.x * tokens + slot, (unsigned)a.T - 1);
+  // behind the last token its lanes do the last one's work again, and write nothing
+  const bool live = blockIdx.x * tokens + slot < (unsigned)a.T;
+  const E* const row = (const E*)a.z + (int64_t)t * a.zs;
+  float* const s_row = s_rows + slot * pitch;
+  const int64_t at = (int64_t)t * a.k + l;
+  const int e = l < a.k ? a.idx[at] : -1;
+  const bool has = (unsigned)e < (unsigned)a.E;
+  const float zc = has ? to_f32(row[e]) : none;
+  const double dw = has ? (double)a.dw[at] * (double)a.scale : 0.0;
+  double own;
+  if (all) {
+    float zmax = none;
+    for (int c = l * V; c < a.E; c += 16 * V) {
+      float f[V];
+      if (c + V <= a.E) {
+        const Chunk<E> q = load_chunk<V>(row + c);
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) zmax = fmaxf(zmax, z[i]);
-        zmax = max_lanes<64>(zmax);
-        double p[NPL], sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          p[i] = z[i] == none ? 0.0 : exp((double)z[i] - (double)zmax);
-          sum += p[i];
-        }
-        sum = sum_lanes<64>(sum);
-        sum = sum == 0.0 ? 0.0 : 1.0 / sum;  // no expert at all: zeros
-        w = has ? exp((double)zc - (double)zmax) * sum : 0.0;
-        along = sum_lanes<64>(w * dw);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) dz[i] = (float)(-p[i] * sum * along);
-        own = w * (dw - along);
+        for (int i = 0; i < V; ++i) f[i] = to_f32(q.e[i]);
       } else {
-        const float top = max_lanes<64>(zc);
-        w = has ? exp((double)zc - (double)top) : 0.0;
-        w /= sum_lanes<64>(w);
-        along = sum_lanes<64>(w * dw);
-        own = w * (dw - along);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = c + i < a.E ? to_f32(row[c + i]) : none;
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        zmax = fmaxf(zmax, f[i]);
+        s_row[c + i] = f[i];
+      }
+    }
+    zmax = max_lanes<16>(zmax);
+    double sum = 0.0;
+    for (int c = l * V; c < a.E; c += 16 * V)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float z = s_row[c + i];
+        const double p = z == none ? 0.0 : exp((double)z - (double)zmax);
+        sum += p;
+        s_row[c + i] = (float)p;
+      }
+    sum = sum_lanes<16>(sum);
+    sum = sum == 0.0 ? 0.0 : 1.0 / sum;  // no expert at all: zeros
+    const double w = has ? exp((double)zc - (double)zmax) * sum : 0.0;
+    const double along = sum_lanes<16>(w * dw);
+    own = w * (dw - along);
+    const double by = -sum * along;
+    for (int c = l * V; c < a.E; c += 16 * V)
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_row[c + i] = (float)((double)s_row[c + i] * by);
+  } else {
+    for (int c = l * 4; c < pitch; c += 64) *(float4*)(s_row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.score == MOE_SCORE_SOFTMAX) {
+      const float top = max_lanes<16>(zc);
+      double w = has ? exp((double)zc - (double)top) : 0.0;
+      w /= sum_lanes<16>(w);
+      own = w * (dw - sum_lanes<16>(w * dw));
     } else {
-      const double s = has ? sigmoid_f64(zc) : 0.0, rest = has ? sigmoid_f64(-zc) : 0.0;
+      // 1 - s without its cancellation: s(-z) = exp(-z) s(z), with the smaller of the exponentials
+      const double f = exp(-fabs((double)zc)), big = 1.0 / (1.0 + f), small = f * big;
+      const double s = !has ? 0.0 : zc < 0.f ? small : big;
       double w = s, along = 0.0;
       if (a.renorm) {
-        const double sum = sum_lanes<64>(s);
-        w = sum > 0.0 ? s / sum : 0.0;
-        along = sum_lanes<64>(w * dw);
+        const double sum = sum_lanes<16>(s);
+        w = sum == 0.0 ? 0.0 : s / sum;
+        along = sum_lanes<16>(w * dw);
       }
-      own = w * rest * (dw - along);
+      own = w * (zc < 0.f ? big : small) * (dw - along);
+      if (zc != zc) own = zc;
     }
-    if (!all)
+  }
+  asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
+  if (has) s_row[e] = (float)own;
+  asm volatile("" ::: "memory");
+  if (!live) return;
+  E* const out = (E*)a.dz + (int64_t)t * a.dzs;
+  for (int c = l * V; c < a.E; c += 16 * V) {
+    const Chunk<E> q = round_chunk<E, V>(s_row + c);
+    if (c + V <= a.E) {
+      store_chunk(out + c, q);
+    } else {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) dz[i] = 0.f;
-    const float mine = (float)own;
-    for (int j = 0; j < a.k; ++j) {
-      const int ej = __builtin_amdgcn_readlane(e, j);
-      const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j));
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) dz[i] = lane * NPL + i == ej ? v : dz[i];
+      for (int i = 0; i < V; ++i)
+        if (c + i < a.E) out[c + i] = q.e[i];
     }
-    E* const out = (E*)a.dz + (int64_t)t * a.dzs + lane * NPL;
-    const int n = a.E - lane * NPL;
-    if constexpr (NPL >= kChunk<E>) {
-      if (n >= NPL) {
-#pragma unroll
-        for (int q = 0; q < NPL; q += kChunk<E>)
-          store_chunk(out + q, round_chunk<E, kChunk<E>>(dz + q));
-        continue;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (i < n) out[i] = from_f32<E>(dz[i]);
   }
 }
 
@@ -664,7 +720,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   }
   int id_bits = 1;
   while ((1 << id_bits) < a.E) ++id_bits;
-  if (n_lane > 0 && n_lane <= 32) {
+  if (n_lane > 0 && n_lane <= 32 && a.k < 16) {
     const auto kernel = n_lane <= 4    ? route_tokens_kernel<E, 4>
                         : n_lane <= 8  ? route_tokens_kernel<E, 8>
                         : n_lane <= 16 ? route_tokens_kernel<E, 16>
@@ -682,12 +738,10 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
 }
 template <class E>
 hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t s) {
-  const auto kernel = a.E <= 64    ? route_tokens_grad_kernel<E, 1>
-                      : a.E <= 128 ? route_tokens_grad_kernel<E, 2>
-                      : a.E <= 256 ? route_tokens_grad_kernel<E, 4>
-                      : a.E <= 512 ? route_tokens_grad_kernel<E, 8>
-                                   : route_tokens_grad_kernel<E, 16>;
-  return launch_kernel(kernel, dim3(route_grid(a.T)), dim3(RT_T), 0, s, a);
+  constexpr int tokens = RT_T / 16;
+  const int pitch = (a.E + 7) / 8 * 8;
+  return launch_kernel(route_tokens_grad_kernel<E>, dim3((unsigned)((a.T + tokens - 1) / tokens)),
+                       dim3(RT_T), sizeof(float) * tokens * pitch, s, a, pitch);
 }
 
 bool route_ok(int type, int T, int E, int score, int k, float scale) {
