@@ -19,10 +19,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int AD_T = 256, AD_W = AD_T / 64;  // threads, waves
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 1024;
-constexpr int NT = 4, NB = 16 * NT;  // channel tiles of a block, its channels
+constexpr int AD_W = 4;  // waves
 
 struct AdaptArgs {
   const void* x;
@@ -88,218 +87,355 @@ __device__ __forceinline__ u32x4 load_tail(const E* p, int n, int len) {
 struct Tile {
   int g, m0, end;  // adapter, first sorted row, end of the adapter's rows
 };
-// Row tile `tile` of BM rows, counted over the adapters, by every wave for itself (64 adapters at a
-// time); g = -1 behind the last.
+// The row tile (of BM rows, counted over the adapters) of workgroup column b, by every wave for itself,
+// 64 adapters at a time; g = -1 where there is none.  Workgroups go round the eight dies, so each
+// die is given a run of neighbouring tiles: its L2 then holds the one or two adapters that they
+// share (16384 rows, 11 adapters of 512 KiB: NNN us, 93 with tiles dealt out in order).
+constexpr int kDies = 8;
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const AdaptArgs& a, int tile, int lane) {
-  if (!a.offsets) return tile * BM < a.M ? Tile{0, tile * BM, a.M} : Tile{-1, 0, 0};
-  for (int g0 = 0; g0 < a.adapters; g0 += 64) {
-    int lo = 0, hi = 0;
-    if (g0 + lane < a.adapters) {
-      lo = min(max(a.offsets[g0 + lane], 0), a.M);
-      hi = min(max(a.offsets[g0 + lane + 1], lo), a.M);
+__device__ __forceinline__ Tile find_tile(const AdaptArgs& a, int b, int lane) {
+  int2 rows = make_int2(0, 0);  // this lane's adapter's, of the 64 from g0 on
+  int inc = 0, n = 0;           // tiles up to and with it; its own
+  const auto look = [&](int g0) {
+    rows = make_int2(0, 0);
+    if (!a.offsets) {
+      if (lane == 0) rows.y = a.M;
+    } else if (g0 + lane < a.adapters) {
+      rows.x = min(max(a.offsets[g0 + lane], 0), a.M);
+      rows.y = min(max(a.offsets[g0 + lane + 1], rows.x), a.M);
     }
-    const int n = (hi - lo + BM - 1) / BM;
-    int inc = n;
+    n = inc = (rows.y - rows.x + BM - 1) / BM;
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
       const int o = __shfl_up(inc, s);
       if (lane >= s) inc += o;
     }
-    const uint64_t past = __ballot(inc > tile);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int first = __builtin_amdgcn_readlane(inc - n, l);
-      return Tile{g0 + l, __builtin_amdgcn_readlane(lo, l) + (tile - first) * BM,
-                  __builtin_amdgcn_readlane(hi, l)};
+    return __builtin_amdgcn_readlane(inc, 63);
+  };
+  int total = look(0);
+  for (int g0 = 64; g0 < a.adapters; g0 += 64) total += look(g0);
+  const int per = (total + kDies - 1) / kDies;
+  int tile = b % kDies * per + b / kDies;
+  if (b / kDies >= per || tile >= total) return Tile{-1, 0, 0};
+  for (int g0 = 0; g0 < a.adapters; g0 += 64) {
+    const int here = a.adapters > 64 ? look(g0) : total;
+    if (tile < here) {
+      const int l = __builtin_ctzll(__ballot(inc > tile));
+      const int before = __builtin_amdgcn_readlane(inc - n, l);
+      return Tile{g0 + l, __builtin_amdgcn_readlane(rows.x, l) + (tile - before) * BM,
+                  __builtin_amdgcn_readlane(rows.y, l)};
     }
-    tile -= __builtin_amdgcn_readlane(inc, 63);
+    tile -= here;
   }
   return Tile{-1, 0, 0};
 }
 
-// A tile of 16 MT rows, ranks up to 16 RT.
-template <class E, int RT, int MT>
-__global__ __launch_bounds__(AD_T) void adapt_rows_kernel(AdaptArgs a) {
-  constexpr int V = kChunk<E>, BM = 16 * MT, UNIT = 8 * V;  // elements of 128 bytes
+// A wave's LDS accesses execute in order; this keeps the compiler, which sees one lane's only, from
+// reordering or merging them where lanes read what others wrote.
+__device__ __forceinline__ void wave_lds_order() { asm volatile("" ::: "memory"); }
+
+// 16-byte chunks of a row of UC in LDS are dealt by the row's number, so that the sixteen rows of an
+// operand do not meet in the same banks.
+template <int UC>
+__device__ __forceinline__ int dealt(int chunk, int row) {
+  return UC == 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+}
+
+// A tile of 16 MT rows, ranks up to 16 RT, UC 16-byte chunks of a row's contraction at a time.
+// Neighbouring lanes load neighbouring chunks (a lane per row, as the matrix instruction has them,
+// costs an access of the cache for each lane: 93 us where this takes NNN), which go through the
+// wave's own part of LDS into the instruction's order, and its results back the same way.  Both
+// products have the loads of their next step under way in registers.
+template <class E, int RT, int MT, int UC>
+__global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
+  constexpr int V = kChunk<E>, BM = 16 * MT, UNIT = UC * V;
   constexpr bool SPLIT = sizeof(E) == 2;
-  constexpr int PITCH = 16 * RT + 4;                 // of a row of h, in floats
+  constexpr int PARTS = SPLIT ? 2 : 1;
+  constexpr int RPL = 64 / UC;                        // rows of a load of all lanes
+  constexpr int NX = BM / RPL, NA = 16 * RT / RPL;    // loads of a step
+  constexpr int BATCH = NX + NA <= 4 ? 4 : NX + NA <= 8 ? 2 : 1;  // steps under way
+  constexpr int PITCH = 16 * RT + 4;                  // of a row of h, in floats
   constexpr int R = RT == 1 && SPLIT ? 32 : 16 * RT;  // contraction of the second product, padded
-  constexpr int RK = R / (4 * V);
-  constexpr int HP = R + V;  // pitch of its operand
-  __shared__ __align__(16) float s_part[AD_W][BM][PITCH];
-  __shared__ __align__(16) E s_h[SPLIT ? 2 : 1][BM][HP];
+  constexpr int RC = R / V, RK = RC / 4;              // its chunks, and steps
+  constexpr int HP = R + V;                           // pitch of its operands
+  constexpr int NT = RC <= 8 ? 4 : RC <= 16 ? 2 : 1;  // channel tiles of a block
+  constexpr int NB = 16 * NT, CPR = NB / V;           // channels, chunks of a row of the output
+  constexpr int NBL = NB * RC / 64;                   // loads of a block's B
+  constexpr int RPO = 64 / CPR, NO = BM / RPO;        // rows of a load of the base; loads
+  constexpr int OP = NB + 4;                          // pitch of the results
+  // the wave's LDS: a step's operands, or its part of h, or a block's B and results
+  constexpr int STEP_B = (BM + 16 * RT) * UC * 16, PART_B = BM * PITCH * 4;
+  constexpr int BLOCK_B = NB * HP * (int)sizeof(E), RESULT_B = 16 * OP * 4;
+  constexpr int WAVE_B = (STEP_B > PART_B ? STEP_B : PART_B) > BLOCK_B + RESULT_B
+                             ? (STEP_B > PART_B ? STEP_B : PART_B)
+                             : BLOCK_B + RESULT_B;
+  static_assert(WAVE_B % 16 == 0 && BLOCK_B % 16 == 0 && NX * RPL == BM && NA * RPL == 16 * RT);
+  __shared__ __align__(16) uint8_t s_wave[AD_W][WAVE_B];
+  __shared__ __align__(16) E s_h[PARTS][BM][HP];
   __shared__ float s_back[BM];  // powers of two that fp16's parts were divided by
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const Tile t = find_tile<BM>(a, blockIdx.x, lane);
   if (t.g < 0) return;
-  // this lane's rows; -1: none
-  int row[MT];
-  const E* x[MT];
+  uint8_t* const mem = s_wave[wave];
+  const auto row_of = [&](int m) {
+    const int p = t.m0 + m;
+    const int r = p >= t.end ? -1 : a.order ? a.order[p] : p;
+    return (unsigned)r < (unsigned)a.M ? r : -1;
+  };
+  const E* src[NX + NA];  // this lane's chunk of its rows of x, and of A (behind the rank: the last)
+  const int lr = lane / UC, lc = lane % UC;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int p = t.m0 + 16 * i + col;
-    row[i] = p >= t.end ? -1 : a.order ? a.order[p] : p;
-    if ((unsigned)row[i] >= (unsigned)a.M) row[i] = -1;
-    x[i] = (const E*)a.x + max(row[i], 0) * a.xs + quad * 2 * V;
-  }
-  const E* w[RT];  // rows of A; those behind the rank repeat the last
+  for (int i = 0; i < NX; ++i)
+    src[i] = (const E*)a.x + max(row_of(lr + RPL * i), 0) * a.xs + lc * V;
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-    w[i] = (const E*)a.a + ((int64_t)t.g * a.rank + min(16 * i + col, a.rank - 1)) * a.as +
-           quad * 2 * V;
+  for (int i = 0; i < NA; ++i)
+    src[NX + i] = (const E*)a.a +
+                  ((int64_t)t.g * a.rank + min(lr + RPL * i, a.rank - 1)) * a.as + lc * V;
+
   f32x4 acc[RT][MT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int units = a.K / UNIT;
-#pragma unroll 2
-  for (int u = wave; u < units; u += AD_W) {
-    u32x4 xv[MT][2], wv[RT][2];
+  struct Step {
+    u32x4 q[NX + NA];
+  };
+  const auto load_step = [&](Step& k, int u) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int i = 0; i < NX + NA; ++i) k.q[i] = load_full(src[i] + u * UNIT);
+  };
+  const auto use_step = [&](const Step& k) {
+    wave_lds_order();
 #pragma unroll
-      for (int i = 0; i < MT; ++i) xv[i][s] = load_full(x[i] + u * UNIT + s * V);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) wv[r][s] = load_full(w[r] + u * UNIT + s * V);
+    for (int i = 0; i < NX + NA; ++i) {
+      const int row = lr + RPL * i;
+      *(u32x4*)(mem + (row * UC + dealt<UC>(lc, row)) * 16) = k.q[i];
     }
+    wave_lds_order();
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < UC / 4; ++s) {
+      const auto frag = [&](int row) {
+        return *(const u32x4*)(mem + (row * UC + dealt<UC>(4 * s + quad, row)) * 16);
+      };
+      u32x4 xf[MT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) mma<E>(acc[r][i], wv[r][s], xv[i][s]);
-  }
-  if (units * UNIT < a.K && units % AD_W == wave) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int k = units * UNIT + s * V, left = a.K - k - quad * 2 * V;
-      u32x4 xv[MT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) xv[i] = load_tail(x[i] + k, left, a.K);
+      for (int i = 0; i < MT; ++i) xf[i] = frag(16 * i + col);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const u32x4 wv = load_tail(w[r] + k, left, a.K);
+        const u32x4 wf = frag(BM + 16 * r + col);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) mma<E>(acc[r][i], wv, xv[i]);
+        for (int i = 0; i < MT; ++i) mma<E>(acc[r][i], wf, xf[i]);
       }
     }
+  };
+
+  // A block of channels: its rows of B, a lane a chunk of NBL of them, and the base's chunks
+  const int blocks = (a.N + NB - 1) / NB, step = gridDim.y * AD_W;
+  const bool short_rank = a.rank < V;
+  // whole blocks; the others (the last where N is no multiple, all where the rank is below 16
+  // bytes) go element by element
+  const int whole = short_rank ? 0 : a.N / NB;
+  const int bc = lane % RC * V;  // first element of this lane's chunk of a row of B
+  const E* const bg = (const E*)a.b + (int64_t)t.g * a.N * a.bs;
+  const int oc = lane % CPR * V;
+  int orow[NO];
+  const E* base[NO];
+#pragma unroll
+  for (int i = 0; i < NO; ++i) {
+    orow[i] = row_of(lane / CPR + RPO * i);
+    // without a base any 16 bytes of the output's row serve: nothing takes them
+    base[i] = a.base ? (const E*)a.base + max(orow[i], 0) * a.base_s + oc
+                     : (const E*)a.out + max(orow[i], 0) * a.os;
   }
+  const int base_n = a.base ? -1 : 0;
+  struct Block {
+    u32x4 b[NBL];
+    Chunk<E> base[NO];
+  };
+  const auto load_block = [&](Block& k, int nb) {
+#pragma unroll
+    for (int i = 0; i < NBL; ++i)
+      k.b[i] = load_full(bg + (nb * NB + (i * 64 + lane) / RC) * a.bs + min(bc, a.rank - V));
+#pragma unroll
+    for (int i = 0; i < NO; ++i) k.base[i] = load_chunk<V>(base[i] + (nb * NB & base_n));
+  };
+
+  const int units = a.K / UNIT, batches = units / BATCH;
+  Block blk[2];
+  const int ib = blockIdx.y * AD_W + wave;
+  {
+    Step k[2][BATCH];  // in turn; behind the last the last is loaded again
+    const auto load_batch = [&](Step(&k)[BATCH], int i) {
+      const int u = min(i, batches - 1) * BATCH;
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) load_step(k[j], u + j);
+    };
+    const auto use_batch = [&](const Step(&k)[BATCH]) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) use_step(k[j]);
+    };
+    if (wave < batches) load_batch(k[0], wave);
+    if (ib < whole) load_block(blk[0], ib);
+    for (int i = wave; i < batches; i += 2 * AD_W) {
+      load_batch(k[1], i + AD_W);
+      use_batch(k[0]);
+      if (i + AD_W >= batches) break;
+      load_batch(k[0], i + 2 * AD_W);
+      use_batch(k[1]);
+    }
+    static_assert(BATCH - 1 <= AD_W);
+    if (BATCH > 1 && batches * BATCH + wave < units) {  // steps short of a batch, one each
+      load_step(k[0][0], batches * BATCH + wave);
+      use_step(k[0][0]);
+    }
+    if (units * UNIT < a.K && wave == AD_W - 1) {
+      const int n = a.K - units * UNIT - lc * V;
+#pragma unroll
+      for (int i = 0; i < NX + NA; ++i) k[0][0].q[i] = load_tail(src[i] + units * UNIT, n, a.K);
+      use_step(k[0][0]);
+    }
+  }
+  wave_lds_order();
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      *(f32x4*)&s_part[wave][16 * i + col][16 * r + 4 * quad] = acc[r][i];
+      *(f32x4*)(mem + ((16 * i + col) * PITCH + 16 * r + 4 * quad) * 4) = acc[r][i];
   __syncthreads();
   {  // the waves' parts joined, scaled and laid out as an operand
-    constexpr int PER = AD_T / BM;  // threads of a row
-    const int m = tid / PER;
+    constexpr int PER = 16;  // threads of a row
     const float f = a.scale ? a.scale[t.g] : 1.f;
-    float h[R / PER], big = 0.f;
 #pragma unroll
-    for (int i = 0; i < R / PER; ++i) {
-      // the rank's last chunk ends with it and holds zeros where the one before has been
-      const int q = tid % PER + i * PER, c = q / V * V;
-      const int r = c + V <= a.rank || a.rank < V ? q : a.rank - V + q % V;
-      const bool in = c < a.rank && r >= c && r < a.rank;
-      h[i] = 0.f;
-      if (in) {
+    for (int m = tid / PER; m < BM; m += 64 * AD_W / PER) {
+      float h[R / PER], big = 0.f;
 #pragma unroll
-        for (int p = 0; p < AD_W; ++p) h[i] += s_part[p][m][r];
-        h[i] *= f;
+      for (int i = 0; i < R / PER; ++i) {
+        // the rank's last chunk ends with it and holds zeros where the one before has been
+        const int q = tid % PER + i * PER, c = q / V * V;
+        const int r = c + V <= a.rank || a.rank < V ? q : a.rank - V + q % V;
+        const bool in = c < a.rank && r >= c && r < a.rank;
+        h[i] = 0.f;
+        if (in) {
+#pragma unroll
+          for (int p = 0; p < AD_W; ++p) h[i] += ((const float*)s_wave[p])[m * PITCH + r];
+          h[i] *= f;
+        }
+        big = fmaxf(big, fabsf(h[i]));
       }
-      big = fmaxf(big, fabsf(h[i]));
-    }
-    float by = 1.f;
-    if constexpr (__is_same(E, fp16_t)) {
+      float by = 1.f;
+      if constexpr (__is_same(E, fp16_t)) {
+        big = join16(big, [](float p, float q) { return fmaxf(p, q); });
+        // the row's largest in [1, 2), inside the normal numbers' exponents
+        const int e = (int)(__float_as_uint(big) >> 23) - 127;
+        if (e > -126 && e < 127) by = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (tid % PER == 0) s_back[m] = 1.f / by;
+      }
 #pragma unroll
-      for (int s = 1; s < PER; s <<= 1) big = fmaxf(big, __shfl_xor(big, s));
-      // the row's largest in [1, 2), inside the normal numbers' exponents
-      const int e = (int)(__float_as_uint(big) >> 23) - 127;
-      if (e > -126 && e < 127) by = __uint_as_float((uint32_t)(127 - e) << 23);
-      if (tid % PER == 0) s_back[m] = 1.f / by;
-    }
-#pragma unroll
-    for (int i = 0; i < R / PER; ++i) {
-      const int q = tid % PER + i * PER;
-      const float v = h[i] * by;
-      const E hi = from_f32<E>(v);
-      s_h[0][m][q] = hi;
-      if constexpr (SPLIT) {
-        const float rest = v - to_f32(hi);
-        s_h[1][m][q] = from_f32<E>(rest - rest == 0.f ? rest : 0.f);  // an infinity has none
+      for (int i = 0; i < R / PER; ++i) {
+        const int q = tid % PER + i * PER;
+        const float v = h[i] * by;
+        const E hi = from_f32<E>(v);
+        s_h[0][m][q] = hi;
+        if constexpr (SPLIT) {
+          const float rest = v - to_f32(hi);
+          s_h[1][m][q] = from_f32<E>(rest - rest == 0.f ? rest : 0.f);  // an infinity has none
+        }
       }
     }
   }
   __syncthreads();
-  u32x4 h[MT][RK][SPLIT ? 2 : 1];
-  float back[MT];
+  u32x4 h[MT][RK][PARTS];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    back[i] = __is_same(E, fp16_t) ? s_back[16 * i + col] : 1.f;
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int s = 0; s < RK; ++s)
 #pragma unroll
-      for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
+      for (int p = 0; p < PARTS; ++p)
         h[i][s][p] = *(const u32x4*)&s_h[p][16 * i + col][(s * 4 + quad) * V];
-  }
-  // row 4 q + i of channel tile t is channel 4 (NT q + t) + i of the block: a lane's results are
-  // 4 NT neighbouring channels
-  const int blocks = (a.N + NB - 1) / NB;
-  const E* const bg = (const E*)a.b + (int64_t)t.g * a.N * a.bs;
-  for (int nb = blockIdx.y * AD_W + wave; nb < blocks; nb += gridDim.y * AD_W) {
-    f32x4 o[MT][NT];
+
+  const bool cut = !short_rank && a.rank != R;
+  const auto use_block = [&](Block& k, int nb, bool all) {
+    wave_lds_order();
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const int n = min(nb * NB + 4 * (NT * (col >> 2) + c) + (col & 3), a.N - 1);
-      const E* const b = bg + n * a.bs;
-      u32x4 bv[RK];
+    for (int i = 0; i < NBL; ++i) {
+      if (cut) {  // zeros behind the rank and, in its last chunk, where the one before has been
+        Chunk<E> c;
+        c.q = k.b[i];
+        const int gone = bc - min(bc, a.rank - V);
 #pragma unroll
-      for (int s = 0; s < RK; ++s) {
-        const int r = (s * 4 + quad) * V;
-        bv[s] = r + V <= a.rank ? load_full(b + r) : load_tail(b + r, a.rank - r, a.rank);
+        for (int e = 0; e < V; ++e) c.e[e] = e < gone ? E{} : c.e[e];
+        k.b[i] = c.q;
       }
+      *(u32x4*)(mem + ((i * 64 + lane) / RC * HP + bc) * (int)sizeof(E)) = k.b[i];
+    }
+    wave_lds_order();
+    u32x4 bf[NT][RK];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        o[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int s = 0; s < RK; ++s)
+        bf[c][s] = *(const u32x4*)(mem + ((16 * c + col) * HP + (s * 4 + quad) * V) * (int)sizeof(E));
+    float* const res = (float*)(mem + BLOCK_B);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      wave_lds_order();
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < RK; ++s)
 #pragma unroll
-          for (int p = SPLIT ? 1 : 0; p >= 0; --p) mma<E>(o[i][c], bv[s], h[i][s][p]);
+          for (int p = PARTS - 1; p >= 0; --p) mma<E>(o, bf[c][s], h[i][s][p]);
+        *(f32x4*)(res + col * OP + 16 * c + 4 * quad) = o;
       }
-    }
-    const int n0 = nb * NB + 4 * NT * quad;
+      wave_lds_order();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (row[i] < 0) continue;
-      const E* const base = (const E*)a.base + row[i] * a.base_s;
-      E* const out = (E*)a.out + row[i] * a.os;
-#pragma unroll
-      for (int q = 0; q < 4 * NT; q += V) {
-        const int n = n0 + q, left = a.N - n;
-        if (left <= 0) continue;
-        Chunk<E> v;
+      for (int j = 0; j < 16 / RPO; ++j) {
+        const int at = i * (16 / RPO) + j, m = lane / CPR + RPO * j;
         float f[V];
-        if (a.base) {
-          if (left >= V)
-            v = load_chunk<V>(base + n);
-          else
-            for (int e = 0; e < V; ++e)
-              if (e < left) v.e[e] = base[n + e];
-        }
+#pragma unroll
+        for (int e = 0; e < V; e += 4) *(f32x4*)(f + e) = *(const f32x4*)(res + m * OP + oc + e);
+        const float back = __is_same(E, fp16_t) ? s_back[16 * i + m] : 1.f;
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          f[e] = fmaf(o[i][(q + e) / 4][(q + e) % 4], back[i], a.base ? to_f32(v.e[e]) : 0.f);
-        v = round_chunk<E, V>(f);
-        if (left >= V)
-          store_chunk(out + n, v);
-        else
+          f[e] = fmaf(f[e], back, a.base ? to_f32(k.base[at].e[e]) : 0.f);
+        const Chunk<E> v = round_chunk<E, V>(f);
+        if (orow[at] < 0) continue;
+        const int n = nb * NB + oc;
+        E* const out = (E*)a.out + orow[at] * a.os + n;
+        if (all) {
+          store_chunk(out, v);
+        } else {
+#pragma unroll
           for (int e = 0; e < V; ++e)
-            if (e < left) out[n + e] = v.e[e];
+            if (n + e < a.N) out[e] = v.e[e];
+        }
       }
     }
+  };
+  const auto block_at = [&](int i) { return min(i, whole - 1); };
+  for (int nb = ib; nb < whole; nb += 2 * step) {
+    load_block(blk[1], block_at(nb + step));
+    use_block(blk[0], nb, true);
+    if (nb + step >= whole) break;
+    load_block(blk[0], block_at(nb + 2 * step));
+    use_block(blk[1], nb + step, true);
+  }
+  for (int nb = ib; nb < blocks; nb += step) {
+    if (nb < whole) continue;
+#pragma unroll
+    for (int i = 0; i < NBL; ++i) {
+      const E* const b = bg + min(nb * NB + (i * 64 + lane) / RC, a.N - 1) * a.bs;
+      blk[0].b[i] = short_rank ? load_tail(b + bc, a.rank - bc, a.rank)
+                               : load_full(b + min(bc, a.rank - V));
+    }
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        blk[0].base[i].e[e] = a.base && nb * NB + oc + e < a.N ? base[i][nb * NB + e] : E{};
+    use_block(blk[0], nb, false);
   }
 }
 
@@ -307,25 +443,27 @@ __global__ __launch_bounds__(AD_T) void adapt_rows_kernel(AdaptArgs a) {
 
 // Row tiles are counted for the worst split of the rows over the adapters; workgroups behind the last
 // tile return.  The channels are shared out until there are two workgroups for a CU.
-template <class E, int RT, int MT>
+template <class E, int RT, int MT, int UC>
 hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
   constexpr int BM = 16 * MT;
   const int groups = a.offsets ? std::min(a.adapters, a.M) : 1;
-  const int tiles = std::min(a.M, a.M / BM + groups);
-  const int blocks = (a.N + NB - 1) / NB;
+  const int tiles = (std::min(a.M, a.M / BM + groups) + kDies - 1) / kDies * kDies;
   const int full = std::max(1, a.M / BM);
-  const int shares = std::max(1, std::min((blocks + AD_W - 1) / AD_W, 512 / full));
-  return launch_kernel(adapt_rows_kernel<E, RT, MT>, dim3((unsigned)tiles, (unsigned)shares),
-                       dim3(AD_T), 0, s, a);
+  const int shares = std::max(1, std::min((a.N + 255) / 256, 512 / full));
+  return launch_kernel(adapt_rows_kernel<E, RT, MT, UC>, dim3((unsigned)tiles, (unsigned)shares),
+                       dim3(64 * AD_W), 0, s, a);
 }
 template <class E>
 hipError_t launch_adapt(const AdaptArgs& a, hipStream_t s) {
   // 32 rows a tile where the adapters have so many
   const bool wide = a.M >= 32 * (a.offsets ? a.adapters : 1);
-  if (a.rank <= 16) return wide ? launch_adapt_by<E, 1, 2>(a, s) : launch_adapt_by<E, 1, 1>(a, s);
-  if (a.rank <= 32) return wide ? launch_adapt_by<E, 2, 2>(a, s) : launch_adapt_by<E, 2, 1>(a, s);
-  if (a.rank <= 64) return wide ? launch_adapt_by<E, 4, 2>(a, s) : launch_adapt_by<E, 4, 1>(a, s);
-  return launch_adapt_by<E, 8, 1>(a, s);
+  if (a.rank <= 16)
+    return wide ? launch_adapt_by<E, 1, 2, 8>(a, s) : launch_adapt_by<E, 1, 1, 8>(a, s);
+  if (a.rank <= 32)
+    return wide ? launch_adapt_by<E, 2, 2, 8>(a, s) : launch_adapt_by<E, 2, 1, 8>(a, s);
+  if (a.rank <= 64)
+    return wide ? launch_adapt_by<E, 4, 2, 8>(a, s) : launch_adapt_by<E, 4, 1, 8>(a, s);
+  return launch_adapt_by<E, 8, 1, 4>(a, s);
 }
 
 }  // namespace
