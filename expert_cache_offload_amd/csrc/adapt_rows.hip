@@ -9,6 +9,7 @@
 // h is held in fp32.  16-bit inputs multiply it as two 16-bit parts, which keep 16 bits of bf16 and
 // 22 (of the row's largest) of fp16: its rounding stays far inside the output's.
 #include <algorithm>
+#include <type_traits>
 
 #include "row_ops.h"
 
@@ -22,6 +23,9 @@ typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 1024;
 constexpr int AD_W = 4;  // waves
+// Calls whose x, base and out are more than this together pass the caches by: they would push out the
+// adapters (16384 rows of 2048 to 2048 of rank 64: 67 us without, 59 with).
+constexpr int64_t kAdaptStreamBytes = 128 << 20;
 
 struct AdaptArgs {
   const void* x;
@@ -64,6 +68,10 @@ template <class E>
 __device__ __forceinline__ u32x4 load_full(const E* p) {
   return *(const u32x4_any*)p;
 }
+template <bool STREAM, class E>
+__device__ __forceinline__ u32x4 load_x(const E* p) {
+  return load_chunk<kChunk<E>, STREAM>(p).q;
+}
 // 16 bytes of a contraction from p on, where n elements of a row of `len` are left: all, or (len at
 // least 16 bytes) the row's last 16 bytes with what lies before p zeroed, or the elements of a
 // shorter row one by one; zeros behind the end.  Both operands agree in which is which.
@@ -90,7 +98,8 @@ struct Tile {
 // The row tile (of BM rows, counted over the adapters) of workgroup column b, by every wave for itself,
 // 64 adapters at a time; g = -1 where there is none.  Workgroups go round the eight dies, so each
 // die is given a run of neighbouring tiles: its L2 then holds the one or two adapters that they
-// share (16384 rows, 11 adapters of 512 KiB: NNN us, 93 with tiles dealt out in order).
+// share (16384 rows over 11 adapters of 512 KiB read 144 MB from behind the L2, 185 with the tiles dealt
+// out in order).
 constexpr int kDies = 8;
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const AdaptArgs& a, int b, int lane) {
@@ -143,10 +152,10 @@ __device__ __forceinline__ int dealt(int chunk, int row) {
 
 // A tile of 16 MT rows, ranks up to 16 RT, UC 16-byte chunks of a row's contraction at a time.
 // Neighbouring lanes load neighbouring chunks (a lane per row, as the matrix instruction has them,
-// costs an access of the cache for each lane: 93 us where this takes NNN), which go through the
+// costs an access of the cache for each lane: 93 us where this took 67), which go through the
 // wave's own part of LDS into the instruction's order, and its results back the same way.  Both
 // products have the loads of their next step under way in registers.
-template <class E, int RT, int MT, int UC>
+template <class E, int RT, int MT, int UC, bool STREAM>
 __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   constexpr int V = kChunk<E>, BM = 16 * MT, UNIT = UC * V;
   constexpr bool SPLIT = sizeof(E) == 2;
@@ -178,16 +187,22 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   const Tile t = find_tile<BM>(a, blockIdx.x, lane);
   if (t.g < 0) return;
   uint8_t* const mem = s_wave[wave];
-  const auto row_of = [&](int m) {
-    const int p = t.m0 + m;
-    const int r = p >= t.end ? -1 : a.order ? a.order[p] : p;
-    return (unsigned)r < (unsigned)a.M ? r : -1;
-  };
+  // The tile's rows, a lane each.  Behind the adapter's last row, and where a place is no row, another
+  // row of the tile is computed and written again, so that no store depends on its lane: a wait for a
+  // load would otherwise count on none of the stores after it, and wait for these too.
+  int mine = t.m0 + lane % BM;
+  if (mine >= t.end) mine = t.end - 1;
+  if (a.order) mine = a.order[mine];
+  const uint64_t rows = __ballot((unsigned)mine < (unsigned)a.M);
+  if (rows == 0) return;
+  const int other = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rows));
+  if ((unsigned)mine >= (unsigned)a.M) mine = other;
+  const auto row_of = [&](int m) { return __shfl(mine, m); };
   const E* src[NX + NA];  // this lane's chunk of its rows of x, and of A (behind the rank: the last)
   const int lr = lane / UC, lc = lane % UC;
 #pragma unroll
   for (int i = 0; i < NX; ++i)
-    src[i] = (const E*)a.x + max(row_of(lr + RPL * i), 0) * a.xs + lc * V;
+    src[i] = (const E*)a.x + row_of(lr + RPL * i) * a.xs + lc * V;
 #pragma unroll
   for (int i = 0; i < NA; ++i)
     src[NX + i] = (const E*)a.a +
@@ -203,7 +218,8 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   };
   const auto load_step = [&](Step& k, int u) {
 #pragma unroll
-    for (int i = 0; i < NX + NA; ++i) k.q[i] = load_full(src[i] + u * UNIT);
+    for (int i = 0; i < NX + NA; ++i)
+      k.q[i] = i < NX ? load_x<STREAM>(src[i] + u * UNIT) : load_full(src[i] + u * UNIT);
   };
   const auto use_step = [&](const Step& k) {
     wave_lds_order();
@@ -239,30 +255,32 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   const int bc = lane % RC * V;  // first element of this lane's chunk of a row of B
   const E* const bg = (const E*)a.b + (int64_t)t.g * a.N * a.bs;
   const int oc = lane % CPR * V;
-  int orow[NO];
+  E* out[NO];
   const E* base[NO];
 #pragma unroll
   for (int i = 0; i < NO; ++i) {
-    orow[i] = row_of(lane / CPR + RPO * i);
+    const int r = row_of(lane / CPR + RPO * i);
+    out[i] = (E*)a.out + r * a.os + oc;
     // without a base any 16 bytes of the output's row serve: nothing takes them
-    base[i] = a.base ? (const E*)a.base + max(orow[i], 0) * a.base_s + oc
-                     : (const E*)a.out + max(orow[i], 0) * a.os;
+    base[i] = a.base ? (const E*)a.base + r * a.base_s + oc : (const E*)a.out + r * a.os;
   }
   const int base_n = a.base ? -1 : 0;
-  struct Block {
-    u32x4 b[NBL];
-    Chunk<E> base[NO];
-  };
-  const auto load_block = [&](Block& k, int nb) {
+  const auto block_at = [&](int i) { return min(i, whole - 1); };
+  // two blocks of B and one of the base are under way (with the base two or four blocks ahead, a tile
+  // of 32 rows took 8 to 10 us longer)
+  u32x4 bq[2][NBL];
+  Chunk<E> bases[NO];
+  const auto load_b = [&](u32x4(&k)[NBL], int nb) {
 #pragma unroll
     for (int i = 0; i < NBL; ++i)
-      k.b[i] = load_full(bg + (nb * NB + (i * 64 + lane) / RC) * a.bs + min(bc, a.rank - V));
+      k[i] = load_full(bg + (nb * NB + (i * 64 + lane) / RC) * a.bs + min(bc, a.rank - V));
+  };
+  const auto load_base = [&](Chunk<E>(&k)[NO], int nb) {
 #pragma unroll
-    for (int i = 0; i < NO; ++i) k.base[i] = load_chunk<V>(base[i] + (nb * NB & base_n));
+    for (int i = 0; i < NO; ++i) k[i] = load_chunk<V, STREAM>(base[i] + (nb * NB & base_n));
   };
 
   const int units = a.K / UNIT, batches = units / BATCH;
-  Block blk[2];
   const int ib = blockIdx.y * AD_W + wave;
   {
     Step k[2][BATCH];  // in turn; behind the last the last is loaded again
@@ -276,7 +294,6 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
       for (int j = 0; j < BATCH; ++j) use_step(k[j]);
     };
     if (wave < batches) load_batch(k[0], wave);
-    if (ib < whole) load_block(blk[0], ib);
     for (int i = wave; i < batches; i += 2 * AD_W) {
       load_batch(k[1], i + AD_W);
       use_batch(k[0]);
@@ -295,6 +312,11 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
       for (int i = 0; i < NX + NA; ++i) k[0][0].q[i] = load_tail(src[i] + units * UNIT, n, a.K);
       use_step(k[0][0]);
     }
+  }
+  if (whole > 0) {
+    load_b(bq[0], block_at(ib));
+    load_b(bq[1], block_at(ib + step));
+    load_base(bases, block_at(ib));
   }
   wave_lds_order();
 #pragma unroll
@@ -354,22 +376,23 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
       for (int p = 0; p < PARTS; ++p)
         h[i][s][p] = *(const u32x4*)&s_h[p][16 * i + col][(s * 4 + quad) * V];
 
-  const bool cut = !short_rank && a.rank != R;
-  const auto use_block = [&](Block& k, int nb, bool all) {
+  // what counts of a lane's chunk of B: nothing behind the rank and, in its last chunk, nothing that
+  // the one before has
+  Chunk<E> count;
+  count.q = u32x4{~0u, ~0u, ~0u, ~0u};
+  if (!short_rank) {
+    const int gone = bc - min(bc, a.rank - V);
+#pragma unroll
+    for (int e = 0; e < V; ++e) count.e[e] = e < gone ? E{} : count.e[e];
+  }
+  const auto put_b = [&](u32x4(&k)[NBL]) {
     wave_lds_order();
 #pragma unroll
-    for (int i = 0; i < NBL; ++i) {
-      if (cut) {  // zeros behind the rank and, in its last chunk, where the one before has been
-        Chunk<E> c;
-        c.q = k.b[i];
-        const int gone = bc - min(bc, a.rank - V);
-#pragma unroll
-        for (int e = 0; e < V; ++e) c.e[e] = e < gone ? E{} : c.e[e];
-        k.b[i] = c.q;
-      }
-      *(u32x4*)(mem + ((i * 64 + lane) / RC * HP + bc) * (int)sizeof(E)) = k.b[i];
-    }
+    for (int i = 0; i < NBL; ++i)
+      *(u32x4*)(mem + ((i * 64 + lane) / RC * HP + bc) * (int)sizeof(E)) = k[i] & count.q;
     wave_lds_order();
+  };
+  const auto use_block = [&](const Chunk<E>(&bk)[NO], int nb, bool all) {
     u32x4 bf[NT][RK];
 #pragma unroll
     for (int c = 0; c < NT; ++c)
@@ -399,43 +422,44 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
         const float back = __is_same(E, fp16_t) ? s_back[16 * i + m] : 1.f;
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          f[e] = fmaf(f[e], back, a.base ? to_f32(k.base[at].e[e]) : 0.f);
+          f[e] = fmaf(f[e], back, a.base ? to_f32(bk[at].e[e]) : 0.f);
         const Chunk<E> v = round_chunk<E, V>(f);
-        if (orow[at] < 0) continue;
-        const int n = nb * NB + oc;
-        E* const out = (E*)a.out + orow[at] * a.os + n;
         if (all) {
-          store_chunk(out, v);
+          store_chunk<STREAM>(out[at] + nb * NB, v);
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e)
-            if (n + e < a.N) out[e] = v.e[e];
+            if (nb * NB + oc + e < a.N) out[at][nb * NB + e] = v.e[e];
         }
       }
     }
   };
-  const auto block_at = [&](int i) { return min(i, whole - 1); };
+  const auto turn = [&](u32x4(&k)[NBL], int nb) {
+    put_b(k);
+    load_b(k, block_at(nb + 2 * step));
+    use_block(bases, nb, true);
+    load_base(bases, block_at(nb + step));
+  };
   for (int nb = ib; nb < whole; nb += 2 * step) {
-    load_block(blk[1], block_at(nb + step));
-    use_block(blk[0], nb, true);
+    turn(bq[0], nb);
     if (nb + step >= whole) break;
-    load_block(blk[0], block_at(nb + 2 * step));
-    use_block(blk[1], nb + step, true);
+    turn(bq[1], nb + step);
   }
   for (int nb = ib; nb < blocks; nb += step) {
     if (nb < whole) continue;
 #pragma unroll
     for (int i = 0; i < NBL; ++i) {
       const E* const b = bg + min(nb * NB + (i * 64 + lane) / RC, a.N - 1) * a.bs;
-      blk[0].b[i] = short_rank ? load_tail(b + bc, a.rank - bc, a.rank)
-                               : load_full(b + min(bc, a.rank - V));
+      bq[0][i] = short_rank ? load_tail(b + bc, a.rank - bc, a.rank)
+                            : load_full(b + min(bc, a.rank - V));
     }
 #pragma unroll
     for (int i = 0; i < NO; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        blk[0].base[i].e[e] = a.base && nb * NB + oc + e < a.N ? base[i][nb * NB + e] : E{};
-    use_block(blk[0], nb, false);
+        bases[i].e[e] = a.base && nb * NB + oc + e < a.N ? base[i][nb * NB + e] : E{};
+    put_b(bq[0]);
+    use_block(bases, nb, false);
   }
 }
 
@@ -450,8 +474,10 @@ hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
   const int tiles = (std::min(a.M, a.M / BM + groups) + kDies - 1) / kDies * kDies;
   const int full = std::max(1, a.M / BM);
   const int shares = std::max(1, std::min((a.N + 255) / 256, 512 / full));
-  return launch_kernel(adapt_rows_kernel<E, RT, MT, UC>, dim3((unsigned)tiles, (unsigned)shares),
-                       dim3(64 * AD_W), 0, s, a);
+  const int64_t bytes = (int64_t)a.M * (a.K + (a.base ? 2 : 1) * (int64_t)a.N) * (int)sizeof(E);
+  const auto kernel = bytes > kAdaptStreamBytes ? adapt_rows_kernel<E, RT, MT, UC, true>
+                                                : adapt_rows_kernel<E, RT, MT, UC, false>;
+  return launch_kernel(kernel, dim3((unsigned)tiles, (unsigned)shares), dim3(64 * AD_W), 0, s, a);
 }
 template <class E>
 hipError_t launch_adapt(const AdaptArgs& a, hipStream_t s) {
