@@ -24,8 +24,9 @@ constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 1024;
 constexpr int AD_W = 4;  // waves
 // Calls whose x, base and out are more than this together pass the caches by: they would push out the
-// adapters (16384 rows of 2048 to 2048 of rank 64: 67 us without, 59 with).
-constexpr int64_t kAdaptStreamBytes = 128 << 20;
+// adapters (2048 to 2048 of rank 64: 16384 rows 67 us without, 59 with; 8192 rows 41 and 36; 6144 rows,
+// 75 MB, 25 both).
+constexpr int64_t kAdaptStreamBytes = 64 << 20;
 
 struct AdaptArgs {
   const void* x;
@@ -466,14 +467,16 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
 // ------------------------------------------------------------------ host side
 
 // Row tiles are counted for the worst split of the rows over the adapters; workgroups behind the last
-// tile return.  The channels are shared out until there are two workgroups for a CU.
+// tile return.  The channels of few tiles are shared out over up to 128 workgroups, each of which
+// computes the tile's h for itself (4096 rows of rank 64, 2048 to 2048, in 128 tiles: 20 us with one
+// workgroup each, 28 with four; 2048 rows in 64 tiles: 16 us with two, 20 with one).
 template <class E, int RT, int MT, int UC>
 hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
   constexpr int BM = 16 * MT;
   const int groups = a.offsets ? std::min(a.adapters, a.M) : 1;
   const int tiles = (std::min(a.M, a.M / BM + groups) + kDies - 1) / kDies * kDies;
   const int full = std::max(1, a.M / BM);
-  const int shares = std::max(1, std::min((a.N + 255) / 256, 512 / full));
+  const int shares = std::max(1, std::min((a.N + 255) / 256, 128 / full));
   const int64_t bytes = (int64_t)a.M * (a.K + (a.base ? 2 : 1) * (int64_t)a.N) * (int)sizeof(E);
   const auto kernel = bytes > kAdaptStreamBytes ? adapt_rows_kernel<E, RT, MT, UC, true>
                                                 : adapt_rows_kernel<E, RT, MT, UC, false>;
@@ -481,8 +484,9 @@ hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
 }
 template <class E>
 hipError_t launch_adapt(const AdaptArgs& a, hipStream_t s) {
-  // 32 rows a tile where the adapters have so many
-  const bool wide = a.M >= 32 * (a.offsets ? a.adapters : 1);
+  // 32 rows a tile where there are 64 such tiles and the adapters have so many rows (rank 64, 2048 to
+  // 2048: 1024 rows 12.7 us with 16 rows a tile, 13.8 with 32; 4096 rows 22.9 and 20.3)
+  const bool wide = a.M >= std::max(2048, 32 * (a.offsets ? a.adapters : 1));
   if (a.rank <= 16)
     return wide ? launch_adapt_by<E, 1, 2, 8>(a, s) : launch_adapt_by<E, 1, 1, 8>(a, s);
   if (a.rank <= 32)

@@ -1,0 +1,63 @@
+"""Cases that between them launch every kernel of the norm, routing and adapter operators.
+test_more_ops_launches.py shows that they do (without a GPU), test_gpu_more_ops.py that the results
+are right."""
+
+KINDS = ["bf16", "fp16", "fp32"]
+TYPE = {"bf16": 0, "fp16": 1, "fp32": 2}
+SIZE = {"bf16": 2, "fp16": 2, "fp32": 4}
+P = 1 << 20  # an address, where nothing is launched
+
+
+def norms(kind):
+    """M, K: few rows of every width, and of every width that is held in pieces of 16 bytes as many
+    rows as make the smallest call of both directions stream."""
+    widths = (3, 60, 500, 1001, 3000, 5001, 9000)
+    few = [(9, K) for K in widths]
+    return few + [((128 << 20) // (2 * K * SIZE[kind]) + 5, K) for K in widths[1:]]
+
+
+def norm_args(M, K, kind):
+    return dict(x=P, x_stride=K, residual=P, residual_stride=K, type=TYPE[kind], M=M, K=K, weight=P,
+                eps=1e-6, sum=P, sum_stride=K, y=P, y_stride=K, codes=P, codes_stride=K, scale=P)
+
+
+def norm_grad_args(M, K, kind):
+    return dict(dy=P, dy_stride=K, dsum=None, dsum_stride=K, sum=P, sum_stride=K, type=TYPE[kind],
+                M=M, K=K, weight=P, eps=1e-6, dx=P, dx_stride=K, dweight=P, workspace=P,
+                workspace_bytes=1 << 40)
+
+
+# T, experts, top_k, groups, group_best, top_groups: four sizes of either kernel, and one more of the
+# kernel that gives a token a wave (16 choices, groups that lanes cannot share, above 512 experts)
+ROUTES = [(70, 33, 4, 1, 1, 1), (70, 128, 8, 8, 2, 4), (70, 256, 8, 8, 2, 4), (70, 500, 6, 1, 1, 1),
+          (30, 40, 16, 1, 1, 1), (30, 100, 4, 10, 2, 3), (30, 200, 16, 1, 1, 1),
+          (30, 450, 5, 50, 1, 7), (30, 1024, 8, 32, 2, 9)]
+
+
+def route_args(T, E, k, G, best, kept, kind):
+    return dict(logits=P, logits_stride=E, type=TYPE[kind], T=T, experts=E, score=1, bias=P,
+                groups=G, group_best=best, top_groups=kept, top_k=k, renormalise=1, scale=1.0,
+                topk_idx=P, topk_w=P)
+
+
+def route_grad_args(T, E, k, kind):
+    return dict(logits=P, logits_stride=E, type=TYPE[kind], T=T, experts=E, score=0, topk_idx=P,
+                top_k=k, renormalise=0, scale=1.0, dweights=P, dlogits=P, dlogits_stride=E)
+
+
+def adapts(kind):
+    """M, K, N, rank, adapters: each range of ranks with few rows an adapter and many, below and above
+    what streams."""
+    few, out = 600 * SIZE[kind], []
+    for rank in (10, 32, 49, 100):
+        out += [(130, 90, 70, rank, 40), (2100, 70, 90, rank, 3)]
+        if rank <= 64:  # rows in tiles of 16, above 64 MiB
+            out.append((30000, 300, (1 << 26) // 30000 // few * 300 + 300, rank, 1000))
+        out.append(((1 << 26) // (300 * SIZE[kind]) + 9, 100, 100, rank, 5))
+    return out
+
+
+def adapt_args(M, K, N, rank, adapters, kind):
+    return dict(x=P, x_stride=K, type=TYPE[kind], M=M, K=K, a=P, a_stride=K, b=P, b_stride=rank, N=N,
+                rank=rank, scale=P, adapters=adapters, offsets=P, order=P, base=P, base_stride=N,
+                out=P, out_stride=N)

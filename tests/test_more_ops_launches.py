@@ -1,0 +1,79 @@
+"""What the norm, routing and adapter operators launch, and what they answer when a launch fails, seen
+without a GPU: the runtime's launches are replaced (hip_stub.py)."""
+import re
+
+import pytest
+
+import hip_stub
+import more_ops_variants as v
+
+OK, HIP = 0, -4
+
+
+@pytest.fixture(scope="module")
+def calls(tmp_path_factory):
+    lib = hip_stub.build(tmp_path_factory.mktemp("stub"))
+
+    def run(*wanted):
+        out, kernels = hip_stub.run(lib, [[w[0], w[1], w[2] if len(w) > 2 else {}]
+                                          for w in wanted])
+        run.kernels = kernels
+        return out
+    return run
+
+
+EACH = [  # a call of every operator, with its launches
+    ("moe_norm_rows", v.norm_args(5, 64, "bf16"), 1),
+    ("moe_norm_rows_grad", v.norm_grad_args(3, 2000, "bf16"), 1),  # one workgroup: no parts to join
+    ("moe_norm_rows_grad", v.norm_grad_args(500, 64, "fp16"), 2),
+    ("moe_norm_rows_grad", {**v.norm_grad_args(500, 64, "fp16"), "dweight": None}, 1),
+    ("moe_norm_rows_grad", {**v.norm_grad_args(0, 64, "fp16"), "dy": None, "sum": None}, 1),
+    ("moe_route_tokens", v.route_args(9, 64, 4, 1, 1, 1, "fp32"), 1),
+    ("moe_route_tokens_grad", v.route_grad_args(9, 64, 4, "fp32"), 1),
+    ("moe_adapt_rows", v.adapt_args(9, 64, 64, 8, 4, "bf16"), 1)]
+
+
+def test_error_of_another_call_is_neither_reported_nor_taken(calls):
+    for (name, args, n), r in zip(EACH, calls(*[(name, args, dict(error=1))
+                                                for name, args, _ in EACH])):
+        assert r["status"] == OK and len(r["launches"]) == n, (name, r)
+        assert r["error"] == 1, name
+
+
+def test_failed_launch_ends_the_call(calls):
+    """Nothing is launched after it: the parts of a gradient that was not computed are not joined."""
+    wanted = [(name, args, at) for name, args, n in EACH for at in range(1, n + 1)]
+    for (name, args, at), r in zip(wanted, calls(*[(name, args, dict(launch=at))
+                                                   for name, args, at in wanted])):
+        assert r["status"] == HIP and len(r["launches"]) == at, (name, at, r)
+        assert r["error"] == 0, name
+
+
+def test_groups_that_all_stay_are_no_groups(calls):
+    """The same kernel as without groups, whatever their size."""
+    same = calls(("moe_route_tokens", v.route_args(9, 100, 4, 1, 1, 1, "fp32")),
+                 ("moe_route_tokens", v.route_args(9, 100, 4, 10, 2, 10, "fp32")))
+    assert same[0]["launches"] == same[1]["launches"]
+
+
+def test_variants_reach_every_kernel(calls):
+    wanted = []
+    for kind in v.KINDS:
+        for M, K in v.norms(kind):
+            wanted.append(("moe_norm_rows", v.norm_args(M, K, kind)))
+            wanted.append(("moe_norm_rows_grad", v.norm_grad_args(M, K, kind)))
+        for case in v.ROUTES:
+            wanted.append(("moe_route_tokens", v.route_args(*case, kind)))
+            wanted.append(("moe_route_tokens_grad", v.route_grad_args(*case[:3], kind)))
+        for case in v.adapts(kind):
+            wanted.append(("moe_adapt_rows", v.adapt_args(*case, kind)))
+    reached = set()
+    for (name, args), r in zip(wanted, calls(*wanted)):
+        assert r["status"] == OK, (name, args)
+        for kernel, x, y, threads, lds in r["launches"]:
+            reached.add(kernel)
+            assert 0 < x * threads < 1 << 32 and 0 < y < 1 << 16 and lds <= 1 << 16
+    kernels = {k for k in calls.kernels if re.search(r"\d(norm_rows|route_tokens|adapt_rows)_", k)}
+    assert len(kernels) > 90
+    missed = sorted(kernels - reached)
+    assert not missed, (len(missed), missed)
