@@ -4,7 +4,7 @@
 // h = x + r rounded to the rows' type, q = 1 / sqrt(mean(h^2) + eps), y = q h w.  The 8-bit codes are
 // those of the unrounded y: code = 127 y / max |y| = 127 p / max |p| with p = h w, where q cancels,
 // so they are exact; scale = max |p| q / 127.  Gradient: with S = sum_k w dy h,
-// dx = dsum + q w dy - h q^3 S / K, and dw = sum over the rows of q dy h.
+// dx = dsum + q w dy - h q^3 S / K = dsum + q (w dy - (q h) (q S / K)), dw = sum over the rows of q dy h.
 //
 // A row is read once and held in registers between its sums and its outputs, so both directions
 // are bound by the bytes of the matrices.  Sums over a row are held in 64 bits, over a chunk of 16
@@ -388,7 +388,7 @@ void norm_rows_grad_kernel(NormGradArgs a) {
     }
     const double q = row_factor<G>(h, a.K, a.eps, lane, nc, s_part[0]);
     const float qf = (float)q;
-    const float cf = (float)(q * q * q * row_sum<G>(dot, s_part[1]) / a.K);
+    const float along = (float)(q * row_sum<G>(dot, s_part[1]) / a.K);  // mean of w dy (q h)
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       if (lane + i * G >= nc) continue;
@@ -398,10 +398,10 @@ void norm_rows_grad_kernel(NormGradArgs a) {
       float f[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float hf = to_f32(h[i].e[e]), gf = to_f32(g[i].e[e]);
-        dw[i][e] = fmaf(gf, hf * qf, dw[i][e]);
+        const float n = to_f32(h[i].e[e]) * qf, gf = to_f32(g[i].e[e]);
+        dw[i][e] = fmaf(gf, n, dw[i][e]);
         const float own = a.dsum ? to_f32(d[i].e[e]) : 0.f;
-        f[e] = fmaf(-hf, cf, fmaf(qf, to_f32(w[i].e[e]) * gf, own));
+        f[e] = fmaf(qf, fmaf(-n, along, to_f32(w[i].e[e]) * gf), own);
       }
       if (a.dx)
         store_chunk<STREAM>((E*)a.dx + row * a.dxs + chunk_at<V>(lane + i * G, a.K),
@@ -514,6 +514,11 @@ hipError_t launch_norm_grad(NormGradArgs& a, float* dweight, float* ws, hipStrea
                        dim3(PART_COLS * PART_SHARES), 0, s, (const float*)ws, parts, a.K, dweight);
 }
 
+// An output that is written over an input has its rows.
+bool same_rows(const void* out, int64_t out_s, const void* in, int64_t in_s) {
+  return !out || out != in || out_s == in_s;
+}
+
 bool norm_ok(int type, int M, int K, float eps) {
   return float_type(type) && M >= 0 && M <= kMaxRows && K >= 1 && K <= kMaxNormCols && eps > 0.f &&
          eps < __builtin_inff();
@@ -538,7 +543,10 @@ moe_status moe_norm_rows(const void* x, int64_t x_stride, const void* residual,
       (sum && (!residual || !rows_ok(sum, sum_stride, K, type))) ||
       (y && !rows_ok(y, y_stride, K, type)) ||
       (codes && (!rows_ok(codes, codes_stride, K, MOE_T_I8) || !scale || !aligned4(scale))) ||
-      !on_current_device(x))
+      (sum && sum == y) || !same_rows(sum, sum_stride, x, x_stride) ||
+      !same_rows(sum, sum_stride, residual, residual_stride) ||
+      !same_rows(y, y_stride, x, x_stride) ||
+      !same_rows(y, y_stride, residual, residual_stride) || !on_current_device(x))
     return MOE_E_INVALID;
   NormArgs a{x,   x_stride,   residual, residual_stride, M,     K,            weight, eps,
              sum, sum_stride, y,        y_stride,        codes, codes_stride, scale};
@@ -564,7 +572,9 @@ moe_status moe_norm_rows_grad(const void* dy, int64_t dy_stride, const void* dsu
   if (M > 0 && (!rows_ok(dy, dy_stride, K, type) || !rows_ok(sum, sum_stride, K, type) ||
                 !rows_ok(weight, K, K, type) || (!dx && !dweight) ||
                 (dsum && !rows_ok(dsum, dsum_stride, K, type)) ||
-                (dx && !rows_ok(dx, dx_stride, K, type))))
+                (dx && !rows_ok(dx, dx_stride, K, type)) ||
+                !same_rows(dx, dx_stride, dy, dy_stride) ||
+                !same_rows(dx, dx_stride, dsum, dsum_stride)))
     return MOE_E_INVALID;
   const size_t need = dweight ? moe_norm_grad_workspace_bytes(M, K) : 0;
   if (need && (!workspace || !aligned4(workspace))) return MOE_E_INVALID;

@@ -496,7 +496,7 @@ moe_status moe_product_i8(const int8_t* a, int64_t a_stride, const float* a_scal
  *     row's factor.  A row of zeros has scale 0, one with a NaN or an infinity in p scale NaN,
  *     both codes 0.
  * At least one of y and codes.  weight: [K] of `type`.  eps above 0.  sum and y may be x or residual
- * themselves (the same rows), not both the same.  The mean is held in 64 bits.
+ * themselves (then with its stride), not both the same.  The mean is held in 64 bits.
  * M 0..16777215, K 1..16384, type bf16, fp16 or fp32. */
 moe_status moe_norm_rows(const void* x, int64_t x_stride, const void* residual,
                          int64_t residual_stride, int32_t type, int32_t M, int32_t K,
@@ -512,7 +512,7 @@ size_t moe_norm_grad_workspace_bytes(int32_t M, int32_t K);
  * forward pass's sum, or x without a residual); dy: the gradient of y; dsum: what reaches h by
  * other ways (may be NULL).  With q = 1 / sqrt(mean(h^2) + eps):
  *   dx = dsum + q * weight * dy - h * q^3 * mean(weight * dy * h), the gradient of x and of residual
- *     alike; dx may be dy or dsum itself;
+ *     alike; dx may be dy or dsum itself (then with its stride);
  *   dweight [K] fp32 = sum over the rows of q * dy * h (M = 0: zeros).
  * dx or dweight may be NULL; without dweight no workspace is needed.  Sizes as moe_norm_rows.
  * MOE_E_SCRATCH when workspace_bytes is below moe_norm_grad_workspace_bytes. */

@@ -18,7 +18,7 @@ def norms(kind):
 
 def norm_args(M, K, kind):
     return dict(x=P, x_stride=K, residual=P, residual_stride=K, type=TYPE[kind], M=M, K=K, weight=P,
-                eps=1e-6, sum=P, sum_stride=K, y=P, y_stride=K, codes=P, codes_stride=K, scale=P)
+                eps=1e-6, sum=P, sum_stride=K, y=2 * P, y_stride=K, codes=P, codes_stride=K, scale=P)
 
 
 def norm_grad_args(M, K, kind):

@@ -196,7 +196,7 @@ def _grad_ref(torch, dy, dsum, h, w, eps=EPS):
     return dx, mag, n.sum(0), n.abs().sum(0)
 
 
-def _run_grad(env, dy, dsum, h, w, kind, want=("dx", "dweight"), stream=0):
+def _run_grad(env, dy, dsum, h, w, kind, want=("dx", "dweight"), stream=0, eps=EPS):
     torch, m, types, tid = env
     M, K = dy.shape
     wide, dx = _wide(torch, M, K, types[kind]) if "dx" in want else (None, None)
@@ -204,16 +204,16 @@ def _run_grad(env, dy, dsum, h, w, kind, want=("dx", "dweight"), stream=0):
     size = m.moe_norm_grad_workspace_bytes(M, K)
     ws = torch.full((size + 64,), 0x5a, dtype=torch.uint8, device="cuda")
     m.moe_norm_rows_grad(dy, dy.stride(0), dsum, 0 if dsum is None else dsum.stride(0), h,
-                         h.stride(0), tid[kind], M, K, w, EPS, dx, K + 4, dw, ws, size, stream)
+                         h.stride(0), tid[kind], M, K, w, eps, dx, K + 4, dw, ws, size, stream)
     assert bool((ws[size:] == 0x5a).all())
     return wide, dx, dw
 
 
-def _check_grad(env, dy, dsum, h, w, kind, out):
+def _check_grad(env, dy, dsum, h, w, kind, out, eps=EPS):
     torch, m, types, tid = env
     M, K = dy.shape
     u = _half_ulp(torch, types[kind])
-    dx, mag, dw, dw_mag = _grad_ref(torch, dy, dsum, h, w)
+    dx, mag, dw, dw_mag = _grad_ref(torch, dy, dsum, h, w, eps)
     wide, got, got_w = out
     if got is not None:
         # the factors, their products and sums in fp32 (six roundings on the way to any term), then
@@ -262,6 +262,19 @@ def test_norm_grad_in_place_and_repeated(env, kind, K):
         assert torch.equal(dx, ref) and torch.equal(dw, ref_w[:K])
     m.moe_norm_rows_grad(None, K, None, 0, None, K, tid[kind], 0, K, None, EPS, None, K, dw)
     assert not bool(dw.any())
+
+
+def test_norm_grad_of_far_rows(env):
+    """Rows, and an eps, so small or large that the factor's cube leaves fp32's range."""
+    torch, m, types, tid = env
+    g = _gen(torch, 12)
+    M, K = 8, 300
+    dy, h = (torch.randn(M, K, generator=g, device="cuda") for _ in "ab")
+    w = torch.rand(K, generator=g, device="cuda")
+    h *= torch.tensor([1e-19, 1e-17, 1e-10, 1e-3, 1, 1e5, 1e10, 1e15], device="cuda")[:, None]
+    for eps in (1e-37, 1e-6, 1e6):
+        _check_grad(env, dy, None, h, w, "fp32", _run_grad(env, dy, None, h, w, "fp32", eps=eps),
+                    eps)
 
 
 def test_norm_grad_against_differences(env):

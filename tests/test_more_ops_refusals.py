@@ -22,7 +22,8 @@ def _refused(name, status, **kw):
     assert e.value.status == status, (name, kw, e.value)
 
 
-NORM = v.norm_args(16, 64, "bf16")
+Q = 1 << 24  # another one
+NORM = {**v.norm_args(16, 64, "bf16"), "x": Q, "residual": 2 * Q, "y": 3 * Q}
 
 
 @pytest.mark.parametrize("bad", [
@@ -34,6 +35,19 @@ NORM = v.norm_args(16, 64, "bf16")
     dict(scale=P + 2), dict(y=None, codes=None)])
 def test_norm_refuses(bad):
     _refused("moe_norm_rows", _m().MOE_E_INVALID, **{**NORM, **bad})
+
+
+@pytest.mark.parametrize("over", [
+    dict(sum=3 * Q), dict(sum=Q, sum_stride=65), dict(sum=2 * Q, sum_stride=65),
+    dict(y=Q, y_stride=65), dict(y=2 * Q, y_stride=65)])
+def test_norm_refuses_outputs_over_each_other_or_over_other_rows(over):
+    _refused("moe_norm_rows", _m().MOE_E_INVALID, **{**NORM, **over})
+
+
+@pytest.mark.parametrize("over", [dict(dx=Q, dx_stride=65), dict(dx=2 * Q, dx_stride=65)])
+def test_norm_grad_refuses_other_rows(over):
+    _refused("moe_norm_rows_grad", _m().MOE_E_INVALID,
+             **{**GRAD, "dy": Q, "dsum": 2 * Q, "dsum_stride": 64, **over})
 
 
 GRAD = v.norm_grad_args(500, 64, "fp32")
