@@ -9,7 +9,7 @@
 // h is held in fp32.  16-bit inputs multiply it as two 16-bit parts, which keep 16 bits of bf16 and
 // 22 (of the row's largest) of fp16: its rounding stays far inside the output's.
 #include <algorithm>
-#include <type_traits>
+#include <cmath>
 
 #include "row_ops.h"
 
@@ -163,7 +163,9 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   constexpr int PARTS = SPLIT ? 2 : 1;
   constexpr int RPL = 64 / UC;                        // rows of a load of all lanes
   constexpr int NX = BM / RPL, NA = 16 * RT / RPL;    // loads of a step
-  constexpr int BATCH = NX + NA <= 4 ? 4 : NX + NA <= 8 ? 2 : 1;  // steps under way
+  // steps under way (twice as many cost the registers of a wave more a SIMD: 2000 rows of rank 8, 1024 to
+  // 8192, 23.7 us so and 21.4; 7254 rows of rank 16, 6888 to 920, 37 and 39)
+  constexpr int BATCH = NX + NA <= 4 ? 2 : 1;
   constexpr int PITCH = 16 * RT + 4;                  // of a row of h, in floats
   constexpr int R = RT == 1 && SPLIT ? 32 : 16 * RT;  // contraction of the second product, padded
   constexpr int RC = R / V, RK = RC / 4;              // its chunks, and steps
@@ -467,16 +469,26 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
 // ------------------------------------------------------------------ host side
 
 // Row tiles are counted for the worst split of the rows over the adapters; workgroups behind the last
-// tile return.  The channels of few tiles are shared out over up to 128 workgroups, each of which
-// computes the tile's h for itself (4096 rows of rank 64, 2048 to 2048, in 128 tiles: 20 us with one
-// workgroup each, 28 with four; 2048 rows in 64 tiles: 16 us with two, 20 with one).
+// tile return.  The channels of a tile are shared out over several workgroups, each of which
+// computes the tile's h for itself.  With p1 elements that h reads and p2 that the rest moves, a
+// workgroup's own time goes with p1 + p2 / shares, what all of them read with tiles (p1 shares + p2): the
+// best number is the root of p2 / (p1 tiles) times a constant, which measures 200 to 400 (1024 rows of
+// rank 64, 2048 to 2048: 15.5, 12.6 and 15.7 us with 1, 2 and 4; 664 rows, 864 to 3080: 20.5, 16.0,
+// 13.7 and 12.4 with 1, 2, 4 and 8; 4096 rows, 2048 to 2048: 20.5 and 23.4 with 1 and 2), up to four
+// workgroups for a CU (4480 rows of rank 32, 112 to 7072, in 140 tiles: 55, 48 and 51 us with 1, 8
+// and 14).
+constexpr double kShareRate = 215.0;
+int adapt_shares(const AdaptArgs& a, int tiles, int rows, int blocks) {
+  const double p1 = (double)a.K * (rows + a.rank), p2 = (double)a.N * (a.rank + 2 * rows);
+  const int best = (int)std::lround(std::sqrt(kShareRate * p2 / (p1 * tiles)));
+  return std::max(1, std::min({(blocks + AD_W - 1) / AD_W, 1024 / tiles, best}));
+}
 template <class E, int RT, int MT, int UC>
 hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
   constexpr int BM = 16 * MT;
   const int groups = a.offsets ? std::min(a.adapters, a.M) : 1;
   const int tiles = (std::min(a.M, a.M / BM + groups) + kDies - 1) / kDies * kDies;
-  const int full = std::max(1, a.M / BM);
-  const int shares = std::max(1, std::min((a.N + 255) / 256, 128 / full));
+  const int shares = adapt_shares(a, std::min(tiles, a.M / BM + 1), BM, (a.N + 63) / 64);
   const int64_t bytes = (int64_t)a.M * (a.K + (a.base ? 2 : 1) * (int64_t)a.N) * (int)sizeof(E);
   const auto kernel = bytes > kAdaptStreamBytes ? adapt_rows_kernel<E, RT, MT, UC, true>
                                                 : adapt_rows_kernel<E, RT, MT, UC, false>;
@@ -484,9 +496,9 @@ hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
 }
 template <class E>
 hipError_t launch_adapt(const AdaptArgs& a, hipStream_t s) {
-  // 32 rows a tile where there are 64 such tiles and the adapters have so many rows (rank 64, 2048 to
-  // 2048: 1024 rows 12.7 us with 16 rows a tile, 13.8 with 32; 4096 rows 22.9 and 20.3)
-  const bool wide = a.M >= std::max(2048, 32 * (a.offsets ? a.adapters : 1));
+  // 32 rows a tile where there are 128 such tiles and the adapters have so many rows (rank 64, 2048 to
+  // 2048: 1024 rows 12.6 us with 16 rows a tile, 13.5 with 32; 4096 rows 23.2 and 20.5)
+  const bool wide = a.M >= std::max(4096, 32 * (a.offsets ? a.adapters : 1));
   if (a.rank <= 16)
     return wide ? launch_adapt_by<E, 1, 2, 8>(a, s) : launch_adapt_by<E, 1, 1, 8>(a, s);
   if (a.rank <= 32)

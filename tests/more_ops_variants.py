@@ -50,7 +50,7 @@ def adapts(kind):
     what streams."""
     few, out = 600 * SIZE[kind], []
     for rank in (10, 32, 49, 100):
-        out += [(130, 90, 70, rank, 40), (2100, 70, 90, rank, 3)]
+        out += [(130, 90, 70, rank, 40), (4200, 70, 90, rank, 3)]
         if rank <= 64:  # rows in tiles of 16, above 64 MiB
             out.append((30000, 300, (1 << 26) // 30000 // few * 300 + 300, rank, 1000))
         out.append(((1 << 26) // (300 * SIZE[kind]) + 9, 100, 100, rank, 5))
