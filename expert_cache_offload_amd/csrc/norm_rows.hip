@@ -39,7 +39,7 @@ struct NormArgs {
 
 // Calls that move more bytes than this pass the caches by: what they read is not read again soon.
 constexpr int64_t kNormStreamBytes = 128 << 20;
-// A row is held by G lanes (beyond 64: by the whole workgroup).
+// A row is held by G lanes, 16, 32, 64 or (all of) a workgroup.
 constexpr int norm_threads(int G) { return G < 256 ? 256 : G; }
 
 // v joined over the lanes of a row, in all of them.
@@ -57,6 +57,22 @@ __device__ __forceinline__ T row_join(T v, T* s_part, Join&& join) {
     for (int i = 1; i < G / 64; ++i) v = join(v, s_part[i]);
   }
   return v;
+}
+// Two sums at once.
+template <int G>
+__device__ __forceinline__ void row_sums(double& u, double& v, double (*s_part)[2]) {
+  const auto add = [](double a, double b) { return a + b; };
+  u = join16(u, add), v = join16(v, add);
+#pragma unroll
+  for (int s = 16; s < (G < 64 ? G : 64); s <<= 1) u += __shfl_xor(u, s), v += __shfl_xor(v, s);
+  if constexpr (G > 64) {
+    __syncthreads();  // what an earlier join left has been read
+    if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6][0] = u, s_part[threadIdx.x >> 6][1] = v;
+    __syncthreads();
+    u = s_part[0][0], v = s_part[0][1];
+#pragma unroll
+    for (int i = 1; i < G / 64; ++i) u += s_part[i][0], v += s_part[i][1];
+  }
 }
 template <int G>
 __device__ __forceinline__ double row_sum(double v, double* s_part) {
@@ -121,26 +137,31 @@ __device__ __forceinline__ double chunk_squares_f64(const Chunk<E, V>& c) {
 // Where sums of squares and products in fp32 lose nothing to its range.
 __device__ __forceinline__ bool far_inside(double v) { return v > 0x1p-60 && v < 0x1p60; }
 
-// 1 / sqrt(mean of the squares + eps).
-template <int G, class E, int V>
-__device__ __forceinline__ double row_factor(const Chunk<E, V> (&h)[HELD], int K, float eps,
-                                             int lane, int nc, double* s_part) {
+// The lane's share of a row's sum of squares.
+template <int G, class E, int V, class Squares>
+__device__ __forceinline__ double lane_squares(const Chunk<E, V> (&h)[HELD], int K, int lane, int nc,
+                                               Squares&& squares) {
   double sq = 0.0;
 #pragma unroll
   for (int i = 0; i < HELD; ++i) {
     const int c = lane + i * G;
-    if (c < nc) sq += chunk_squares(without_first(h[i], c * V - chunk_at<V>(c, K)));
+    if (c < nc) sq += squares(without_first(h[i], c * V - chunk_at<V>(c, K)));
   }
-  sq = row_sum<G>(sq, s_part);
-  if (sizeof(E) == 2 && !far_inside(sq)) {
-    sq = 0.0;
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      const int c = lane + i * G;
-      if (c < nc) sq += chunk_squares_f64(without_first(h[i], c * V - chunk_at<V>(c, K)));
-    }
-    sq = row_sum<G>(sq, s_part);
-  }
+  return sq;
+}
+template <int G, class E, int V>
+__device__ __forceinline__ double lane_squares(const Chunk<E, V> (&h)[HELD], int K, int lane,
+                                               int nc) {
+  return lane_squares<G>(h, K, lane, nc, [](const Chunk<E, V>& c) { return chunk_squares(c); });
+}
+// 1 / sqrt(mean of the squares + eps), sq their sum.
+template <int G, class E, int V>
+__device__ __forceinline__ double row_factor(const Chunk<E, V> (&h)[HELD], double sq, int K,
+                                             float eps, int lane, int nc, double* s_part) {
+  if (sizeof(E) == 2 && !far_inside(sq))
+    sq = row_sum<G>(lane_squares<G>(h, K, lane, nc,
+                                    [](const Chunk<E, V>& c) { return chunk_squares_f64(c); }),
+                    s_part);
   return rsqrt(sq / K + (double)eps);
 }
 
@@ -272,7 +293,8 @@ void norm_rows_kernel(NormArgs a) {
         h[i] = round_chunk<E, V>(f);
       }
     }
-    const double q = row_factor<G>(h, a.K, a.eps, lane, nc, s_sum);
+    const double q = row_factor<G>(h, row_sum<G>(lane_squares<G>(h, a.K, lane, nc), s_sum), a.K, a.eps,
+                                   lane, nc, s_sum);
     const float qf = (float)q;
     // every lane has read its part of the row (it may be overwritten now)
     if (a.sum) {
@@ -338,7 +360,7 @@ template <class E, int V, int G, bool STREAM>
 __global__ __launch_bounds__(norm_threads(G), 2)
 void norm_rows_grad_kernel(NormGradArgs a) {
   constexpr int THR = norm_threads(G), ROWS = THR / G;
-  __shared__ double s_part[2][THR / 64];
+  __shared__ double s_part[THR / 64], s_both[THR / 64][2];
   constexpr bool AHEAD = THR < 1024;  // a thousand threads have no registers for it
   extern __shared__ __align__(16) float s_dw[];  // [ROWS][K], where ROWS > 1
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
@@ -386,9 +408,11 @@ void norm_rows_grad_kernel(NormGradArgs a) {
         part = fmaf(to_f32(once.e[e]), to_f32(w[i].e[e]) * to_f32(g[i].e[e]), part);
       dot += part;
     }
-    const double q = row_factor<G>(h, a.K, a.eps, lane, nc, s_part[0]);
+    double sq = lane_squares<G>(h, a.K, lane, nc);
+    row_sums<G>(sq, dot, s_both);
+    const double q = row_factor<G>(h, sq, a.K, a.eps, lane, nc, s_part);
     const float qf = (float)q;
-    const float along = (float)(q * row_sum<G>(dot, s_part[1]) / a.K);  // mean of w dy (q h)
+    const float along = (float)(q * dot / a.K);  // mean of w dy (q h)
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       if (lane + i * G >= nc) continue;
@@ -462,6 +486,7 @@ auto by_width(int K, F&& f) {
   const int nc = chunk_count<V>(K);
   if (K < V) return f(Int<1>{}, Int<16>{});
   if (nc <= 16 * HELD) return f(Int<V>{}, Int<16>{});
+  if (nc <= 32 * HELD) return f(Int<V>{}, Int<32>{});
   if (nc <= 64 * HELD) return f(Int<V>{}, Int<64>{});
   if (nc <= 256 * HELD) return f(Int<V>{}, Int<256>{});
   return f(Int<V>{}, Int<kMaxNormCols / V / HELD>{});

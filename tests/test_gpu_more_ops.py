@@ -19,11 +19,11 @@ EPS = 1e-6
 # ------------------------------------------------------------------ every kernel
 
 
-@pytest.mark.parametrize("case", range(13))
+@pytest.mark.parametrize("case", range(17))
 @pytest.mark.parametrize("kind", KINDS)
 def test_norm_kernels(env, kind, case):
     torch, m, types, tid = env
-    assert len(v.norms(kind)) == 13
+    assert len(v.norms(kind)) == 17
     M, K = v.norms(kind)[case]
     g = _gen(torch, M + K)
     x, r = (_matrix(torch, g, M, K, types[kind]) for _ in "xr")
