@@ -22,7 +22,6 @@ typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 1024;
-constexpr int AD_W = 4;  // waves
 // Calls whose x, base and out are more than this together pass the caches by: they would push out the
 // adapters (2048 to 2048 of rank 64: 16384 rows 67 us without, 59 with; 8192 rows 41 and 36; 6144 rows,
 // 75 MB, 25 both).
@@ -151,13 +150,13 @@ __device__ __forceinline__ int dealt(int chunk, int row) {
   return UC == 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
 }
 
-// A tile of 16 MT rows, ranks up to 16 RT, UC 16-byte chunks of a row's contraction at a time.
+// A tile of 16 MT rows, ranks up to 16 RT, UC 16-byte chunks of a row's contraction at a time, W waves.
 // Neighbouring lanes load neighbouring chunks (a lane per row, as the matrix instruction has them,
 // costs an access of the cache for each lane: 93 us where this took 67), which go through the
 // wave's own part of LDS into the instruction's order, and its results back the same way.  Both
 // products have the loads of their next step under way in registers.
-template <class E, int RT, int MT, int UC, bool STREAM>
-__global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
+template <class E, int RT, int MT, int UC, int W, bool STREAM>
+__global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
   constexpr int V = kChunk<E>, BM = 16 * MT, UNIT = UC * V;
   constexpr bool SPLIT = sizeof(E) == 2;
   constexpr int PARTS = SPLIT ? 2 : 1;
@@ -170,7 +169,8 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   constexpr int R = RT == 1 && SPLIT ? 32 : 16 * RT;  // contraction of the second product, padded
   constexpr int RC = R / V, RK = RC / 4;              // its chunks, and steps
   constexpr int HP = R + V;                           // pitch of its operands
-  constexpr int NT = RC <= 8 ? 4 : RC <= 16 ? 2 : 1;  // channel tiles of a block
+  // channel tiles of a block; half where LDS holds eight waves'
+  constexpr int NT = (RC <= 8 ? 4 : RC <= 16 ? 2 : 1) / (W > 4 && RC <= 16 ? 2 : 1);
   constexpr int NB = 16 * NT, CPR = NB / V;           // channels, chunks of a row of the output
   constexpr int NBL = NB * RC / 64;                   // loads of a block's B
   constexpr int RPO = 64 / CPR, NO = BM / RPO;        // rows of a load of the base; loads
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
                              ? (STEP_B > PART_B ? STEP_B : PART_B)
                              : BLOCK_B + RESULT_B;
   static_assert(WAVE_B % 16 == 0 && BLOCK_B % 16 == 0 && NX * RPL == BM && NA * RPL == 16 * RT);
-  __shared__ __align__(16) uint8_t s_wave[AD_W][WAVE_B];
+  __shared__ __align__(16) uint8_t s_wave[W][WAVE_B];
   __shared__ __align__(16) E s_h[PARTS][BM][HP];
   __shared__ float s_back[BM];  // powers of two that fp16's parts were divided by
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   };
 
   // A block of channels: its rows of B, a lane a chunk of NBL of them, and the base's chunks
-  const int blocks = (a.N + NB - 1) / NB, step = gridDim.y * AD_W;
+  const int blocks = (a.N + NB - 1) / NB, step = gridDim.y * W;
   const bool short_rank = a.rank < V;
   // whole blocks; the others (the last where N is no multiple, all where the rank is below 16
   // bytes) go element by element
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
   };
 
   const int units = a.K / UNIT, batches = units / BATCH;
-  const int ib = blockIdx.y * AD_W + wave;
+  const int ib = blockIdx.y * W + wave;
   {
     Step k[2][BATCH];  // in turn; behind the last the last is loaded again
     const auto load_batch = [&](Step(&k)[BATCH], int i) {
@@ -297,19 +297,19 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
       for (int j = 0; j < BATCH; ++j) use_step(k[j]);
     };
     if (wave < batches) load_batch(k[0], wave);
-    for (int i = wave; i < batches; i += 2 * AD_W) {
-      load_batch(k[1], i + AD_W);
+    for (int i = wave; i < batches; i += 2 * W) {
+      load_batch(k[1], i + W);
       use_batch(k[0]);
-      if (i + AD_W >= batches) break;
-      load_batch(k[0], i + 2 * AD_W);
+      if (i + W >= batches) break;
+      load_batch(k[0], i + 2 * W);
       use_batch(k[1]);
     }
-    static_assert(BATCH - 1 <= AD_W);
+    static_assert(BATCH - 1 <= W);
     if (BATCH > 1 && batches * BATCH + wave < units) {  // steps short of a batch, one each
       load_step(k[0][0], batches * BATCH + wave);
       use_step(k[0][0]);
     }
-    if (units * UNIT < a.K && wave == AD_W - 1) {
+    if (units * UNIT < a.K && wave == W - 1) {
       const int n = a.K - units * UNIT - lc * V;
 #pragma unroll
       for (int i = 0; i < NX + NA; ++i) k[0][0].q[i] = load_tail(src[i] + units * UNIT, n, a.K);
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
     constexpr int PER = 16;  // threads of a row
     const float f = a.scale ? a.scale[t.g] : 1.f;
 #pragma unroll
-    for (int m = tid / PER; m < BM; m += 64 * AD_W / PER) {
+    for (int m = tid / PER; m < BM; m += 64 * W / PER) {
       float h[R / PER], big = 0.f;
 #pragma unroll
       for (int i = 0; i < R / PER; ++i) {
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
         h[i] = 0.f;
         if (in) {
 #pragma unroll
-          for (int p = 0; p < AD_W; ++p) h[i] += ((const float*)s_wave[p])[m * PITCH + r];
+          for (int p = 0; p < W; ++p) h[i] += ((const float*)s_wave[p])[m * PITCH + r];
           h[i] *= f;
         }
         big = fmaxf(big, fabsf(h[i]));
@@ -478,34 +478,52 @@ __global__ __launch_bounds__(64 * AD_W) void adapt_rows_kernel(AdaptArgs a) {
 // workgroups for a CU (4480 rows of rank 32, 112 to 7072, in 140 tiles: 55, 48 and 51 us with 1, 8
 // and 14).
 constexpr double kShareRate = 215.0;
-int adapt_shares(const AdaptArgs& a, int tiles, int rows, int blocks) {
+int adapt_shares(const AdaptArgs& a, int tiles, int rows, int blocks, int waves) {
   const double p1 = (double)a.K * (rows + a.rank), p2 = (double)a.N * (a.rank + 2 * rows);
   const int best = (int)std::lround(std::sqrt(kShareRate * p2 / (p1 * tiles)));
-  return std::max(1, std::min({(blocks + AD_W - 1) / AD_W, 1024 / tiles, best}));
+  return std::max(1, std::min({(blocks + waves - 1) / waves, 1024 / tiles, best}));
 }
-template <class E, int RT, int MT, int UC>
+template <class E>
+bool streams(const AdaptArgs& a) {
+  return (int64_t)a.M * (a.K + (a.base ? 2 : 1) * (int64_t)a.N) * (int)sizeof(E) > kAdaptStreamBytes;
+}
+template <class E, int RT, int MT, int UC, int W>
 hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
   constexpr int BM = 16 * MT;
   const int groups = a.offsets ? std::min(a.adapters, a.M) : 1;
   const int tiles = (std::min(a.M, a.M / BM + groups) + kDies - 1) / kDies * kDies;
-  const int shares = adapt_shares(a, std::min(tiles, a.M / BM + 1), BM, (a.N + 63) / 64);
-  const int64_t bytes = (int64_t)a.M * (a.K + (a.base ? 2 : 1) * (int64_t)a.N) * (int)sizeof(E);
-  const auto kernel = bytes > kAdaptStreamBytes ? adapt_rows_kernel<E, RT, MT, UC, true>
-                                                : adapt_rows_kernel<E, RT, MT, UC, false>;
-  return launch_kernel(kernel, dim3((unsigned)tiles, (unsigned)shares), dim3(64 * AD_W), 0, s, a);
+  const int shares = adapt_shares(a, std::min(tiles, a.M / BM + 1), BM, (a.N + 63) / 64, W);
+  constexpr bool MAY = W == 4;  // the few rows of eight waves are never that much
+  const auto kernel = MAY && streams<E>(a) ? adapt_rows_kernel<E, RT, MT, UC, W, MAY>
+                                           : adapt_rows_kernel<E, RT, MT, UC, W, false>;
+  return launch_kernel(kernel, dim3((unsigned)tiles, (unsigned)shares), dim3(64 * W), 0, s, a);
 }
 template <class E>
 hipError_t launch_adapt(const AdaptArgs& a, hipStream_t s) {
   // 32 rows a tile where there are 128 such tiles and the adapters have so many rows (rank 64, 2048 to
   // 2048: 1024 rows 12.6 us with 16 rows a tile, 13.5 with 32; 4096 rows 23.2 and 20.5)
   const bool wide = a.M >= std::max(4096, 32 * (a.offsets ? a.adapters : 1));
+  // Eight waves where tiles are few and the work of each long: ranks up to 32 with long rows of x (rank 32,
+  // N = 2048: one row of 6144 10.0 us with four waves, 9.6 with eight; 256 rows of 512 5.6 and 6.0, of
+  // 4096 11.4 and 10.2; 1024 rows of 4096 15.2 and 13.3; but 4000 rows, 4096 to 4096, 35 and 45), rank 64
+  // with short ones, whose channels eight waves share (256 rows of 512 7.8 and 7.4, of 6144 19.8 and
+  // 22.8: a step holds half as much of a row there, for the LDS), or with very few
+  const int64_t row = (int64_t)a.K * (int)sizeof(E);
+  const bool few = a.M <= 1024 && !streams<E>(a);
+  const bool deep = few && (a.rank <= 32 ? row >= (a.M < 256 ? 8192 : 2048) : row <= 4096 || a.M <= 64);
   if (a.rank <= 16)
-    return wide ? launch_adapt_by<E, 1, 2, 8>(a, s) : launch_adapt_by<E, 1, 1, 8>(a, s);
+    return wide   ? launch_adapt_by<E, 1, 2, 8, 4>(a, s)
+           : deep ? launch_adapt_by<E, 1, 1, 8, 8>(a, s)
+                  : launch_adapt_by<E, 1, 1, 8, 4>(a, s);
   if (a.rank <= 32)
-    return wide ? launch_adapt_by<E, 2, 2, 8>(a, s) : launch_adapt_by<E, 2, 1, 8>(a, s);
+    return wide   ? launch_adapt_by<E, 2, 2, 8, 4>(a, s)
+           : deep ? launch_adapt_by<E, 2, 1, 8, 8>(a, s)
+                  : launch_adapt_by<E, 2, 1, 8, 4>(a, s);
   if (a.rank <= 64)
-    return wide ? launch_adapt_by<E, 4, 2, 8>(a, s) : launch_adapt_by<E, 4, 1, 8>(a, s);
-  return launch_adapt_by<E, 8, 1, 4>(a, s);
+    return wide   ? launch_adapt_by<E, 4, 2, 8, 4>(a, s)
+           : deep ? launch_adapt_by<E, 4, 1, 4, 8>(a, s)
+                  : launch_adapt_by<E, 4, 1, 8, 4>(a, s);
+  return launch_adapt_by<E, 8, 1, 4, 4>(a, s);
 }
 
 }  // namespace

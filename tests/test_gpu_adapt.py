@@ -109,7 +109,11 @@ ADAPTS = [  # M, K, N, rank, adapters, share without one, rows of a request, pad
     (33, 3, 70, 100, 2, 0.0, 33, 2, 3), (5000, 264, 96, 64, 4, 0.0, 700, 0, 0),
     (40, 64, 64, 8, 1, 0.5, 1, 0, 0), (90, 520, 1100, 32, 2, 0.0, 45, 8, 8),
     (3000, 96, 61, 12, 70, 0.3, 11, 0, 0), (50, 66, 300, 65, 6, 0.0, 10, 0, 1),
-    (20, 40, 40, 16, 4, 1.0, 5, 0, 0)]
+    (20, 40, 40, 16, 4, 1.0, 5, 0, 0),
+    # long rows, few of them: one, a tile's, one more; lengths around a step of all waves
+    (1, 6145, 100, 16, 1, 0.0, 1, 0, 0), (17, 4104, 1000, 3, 2, 0.0, 16, 8, 0),
+    (16, 4099, 66, 24, 1, 0.0, 16, 1, 1), (300, 1088, 130, 17, 5, 0.1, 40, 0, 0),
+    (70, 2049, 71, 64, 3, 0.1, 9, 0, 0), (5, 7000, 520, 40, 2, 0.0, 2, 0, 0)]
 
 
 @pytest.mark.parametrize("M,K,N,rank,adapters,none,run,pad,at", ADAPTS)

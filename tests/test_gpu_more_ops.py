@@ -45,11 +45,11 @@ def test_route_kernels(env, kind, case):
             check_route(env, z, kind, score, b, G, best, kept, k, True, 1.0)
 
 
-@pytest.mark.parametrize("case", range(15))
+@pytest.mark.parametrize("case", range(18))
 @pytest.mark.parametrize("kind", KINDS)
 def test_adapt_kernels(env, kind, case):
     torch, m, types, tid = env
-    assert len(v.adapts(kind)) == 15
+    assert len(v.adapts(kind)) == 18
     M, K, N, rank, adapters = v.adapts(kind)[case]
     x, a, b, base, scale = _operands(env, M + K, M, K, N, rank, adapters, kind)
     ids = adapter_ids(torch, M, M, adapters, 0.1, 37)
