@@ -93,8 +93,19 @@ __device__ __forceinline__ u32x4 load_tail(const E* p, int n, int len) {
 }
 
 struct Tile {
-  int g, m0, end;  // adapter, first sorted row, end of the adapter's rows
+  int g, m0, end;   // adapter, first sorted row, end of the adapter's rows
+  int part, parts;  // which part of the channels, of how many
 };
+// Tiles left over when every CU has had the same number of them are shared out over the channels, as
+// many parts as there are CUs for, of 256 channels at least; each part computes h for itself.  Whole,
+// the last ones keep a few CUs busy while the others wait (2048 to 2048, 11 requests of 16384 rows: rank
+// 64 59 us whole, 53 shared out, rank 16 50 and 47; 16032 rows, 512 tiles at most, 47 and 42; 8192 rows of
+// rank 64 36 and 30.  With 1024 channels a part at least 55, 48 and 32).
+constexpr int kCus = 256;
+__host__ __device__ constexpr int parts_of_rest(int rest, int most) {
+  return rest > 0 && kCus / rest > 1 ? (kCus / rest < most ? kCus / rest : most) : 1;
+}
+__host__ __device__ constexpr int most_parts(int N) { return N / 256 > 1 ? N / 256 : 1; }
 // The row tile (of BM rows, counted over the adapters) of workgroup column b, by every wave for itself,
 // 64 adapters at a time; g = -1 where there is none.  Workgroups go round the eight dies, so each
 // die is given a run of neighbouring tiles: its L2 then holds the one or two adapters that they
@@ -123,20 +134,32 @@ __device__ __forceinline__ Tile find_tile(const AdaptArgs& a, int b, int lane) {
   };
   int total = look(0);
   for (int g0 = 64; g0 < a.adapters; g0 += 64) total += look(g0);
-  const int per = (total + kDies - 1) / kDies;
-  int tile = b % kDies * per + b / kDies;
-  if (b / kDies >= per || tile >= total) return Tile{-1, 0, 0};
+  const int rest = gridDim.y == 1 && total > kCus ? total % kCus : 0;
+  int parts = parts_of_rest(rest, most_parts(a.N)), part = 0, tile;
+  const int whole = parts > 1 ? total - rest : total, per = (whole + kDies - 1) / kDies;
+  if (b < per * kDies) {
+    tile = b % kDies * per + b / kDies;
+    if (tile >= whole) return Tile{-1, 0, 0, 0, 1};
+    parts = gridDim.y;
+    part = blockIdx.y;
+  } else {  // the parts of a tile on one die too
+    if (parts == 1) return Tile{-1, 0, 0, 0, 1};
+    const int i = (b - whole) / kDies, left = i / parts * kDies + b % kDies;
+    if (left >= rest) return Tile{-1, 0, 0, 0, 1};
+    tile = whole + left;
+    part = i % parts;
+  }
   for (int g0 = 0; g0 < a.adapters; g0 += 64) {
     const int here = a.adapters > 64 ? look(g0) : total;
     if (tile < here) {
       const int l = __builtin_ctzll(__ballot(inc > tile));
       const int before = __builtin_amdgcn_readlane(inc - n, l);
       return Tile{g0 + l, __builtin_amdgcn_readlane(rows.x, l) + (tile - before) * BM,
-                  __builtin_amdgcn_readlane(rows.y, l)};
+                  __builtin_amdgcn_readlane(rows.y, l), part, parts};
     }
     tile -= here;
   }
-  return Tile{-1, 0, 0};
+  return Tile{-1, 0, 0, 0, 1};
 }
 
 // A wave's LDS accesses execute in order; this keeps the compiler, which sees one lane's only, from
@@ -175,13 +198,11 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
   constexpr int NBL = NB * RC / 64;                   // loads of a block's B
   constexpr int RPO = 64 / CPR, NO = BM / RPO;        // rows of a load of the base; loads
   constexpr int OP = NB + 4;                          // pitch of the results
-  // the wave's LDS: a step's operands, or its part of h, or a block's B and results
+  // the wave's LDS: a step's operands, or its part of h, or a block's B, then its results
   constexpr int STEP_B = (BM + 16 * RT) * UC * 16, PART_B = BM * PITCH * 4;
   constexpr int BLOCK_B = NB * HP * (int)sizeof(E), RESULT_B = 16 * OP * 4;
-  constexpr int WAVE_B = (STEP_B > PART_B ? STEP_B : PART_B) > BLOCK_B + RESULT_B
-                             ? (STEP_B > PART_B ? STEP_B : PART_B)
-                             : BLOCK_B + RESULT_B;
-  static_assert(WAVE_B % 16 == 0 && BLOCK_B % 16 == 0 && NX * RPL == BM && NA * RPL == 16 * RT);
+  constexpr int WAVE_B = std::max({STEP_B, PART_B, BLOCK_B, RESULT_B});
+  static_assert(WAVE_B % 16 == 0 && NX * RPL == BM && NA * RPL == 16 * RT);
   __shared__ __align__(16) uint8_t s_wave[W][WAVE_B];
   __shared__ __align__(16) E s_h[PARTS][BM][HP];
   __shared__ float s_back[BM];  // powers of two that fp16's parts were divided by
@@ -250,7 +271,7 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
   };
 
   // A block of channels: its rows of B, a lane a chunk of NBL of them, and the base's chunks
-  const int blocks = (a.N + NB - 1) / NB, step = gridDim.y * W;
+  const int blocks = (a.N + NB - 1) / NB, step = t.parts * W;
   const bool short_rank = a.rank < V;
   // whole blocks; the others (the last where N is no multiple, all where the rank is below 16
   // bytes) go element by element
@@ -284,7 +305,7 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
   };
 
   const int units = a.K / UNIT, batches = units / BATCH;
-  const int ib = blockIdx.y * W + wave;
+  const int ib = t.part * W + wave;
   {
     Step k[2][BATCH];  // in turn; behind the last the last is loaded again
     const auto load_batch = [&](Step(&k)[BATCH], int i) {
@@ -402,7 +423,7 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
 #pragma unroll
       for (int s = 0; s < RK; ++s)
         bf[c][s] = *(const u32x4*)(mem + ((16 * c + col) * HP + (s * 4 + quad) * V) * (int)sizeof(E));
-    float* const res = (float*)(mem + BLOCK_B);
+    float* const res = (float*)mem;  // where B was, which is in registers
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       wave_lds_order();
@@ -491,8 +512,14 @@ template <class E, int RT, int MT, int UC, int W>
 hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
   constexpr int BM = 16 * MT;
   const int groups = a.offsets ? std::min(a.adapters, a.M) : 1;
-  const int tiles = (std::min(a.M, a.M / BM + groups) + kDies - 1) / kDies * kDies;
+  const int most = std::min(a.M, a.M / BM + groups);
+  int tiles = (most + kDies - 1) / kDies * kDies;
   const int shares = adapt_shares(a, std::min(tiles, a.M / BM + 1), BM, (a.N + 63) / 64, W);
+  if (shares == 1 && most > kCus) {  // enough for every number of tiles that there may be
+    const int p = most_parts(a.N), even = most / kCus * kCus;
+    tiles = std::max(tiles, (even + std::min(kCus, most % kCus * p) + (kDies - 1) * p + kDies - 1) /
+                                kDies * kDies);
+  }
   constexpr bool MAY = W == 4;  // the few rows of eight waves are never that much
   const auto kernel = MAY && streams<E>(a) ? adapt_rows_kernel<E, RT, MT, UC, W, MAY>
                                            : adapt_rows_kernel<E, RT, MT, UC, W, false>;

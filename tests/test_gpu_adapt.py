@@ -113,7 +113,10 @@ ADAPTS = [  # M, K, N, rank, adapters, share without one, rows of a request, pad
     # long rows, few of them: one, a tile's, one more; lengths around a step of all waves
     (1, 6145, 100, 16, 1, 0.0, 1, 0, 0), (17, 4104, 1000, 3, 2, 0.0, 16, 8, 0),
     (16, 4099, 66, 24, 1, 0.0, 16, 1, 1), (300, 1088, 130, 17, 5, 0.1, 40, 0, 0),
-    (70, 2049, 71, 64, 3, 0.1, 9, 0, 0), (5, 7000, 520, 40, 2, 0.0, 2, 0, 0)]
+    (70, 2049, 71, 64, 3, 0.1, 9, 0, 0), (5, 7000, 520, 40, 2, 0.0, 2, 0, 0),
+    # a few more tiles than one or two for each CU, whose channels are shared out
+    (8300, 40, 1100, 16, 3, 0.0, 900, 0, 0), (4000, 24, 2100, 40, 100, 0.1, 35, 3, 1),
+    (16500, 16, 530, 64, 9, 0.0, 1700, 0, 0), (4112, 9, 777, 128, 1, 0.0, 4112, 0, 0)]
 
 
 @pytest.mark.parametrize("M,K,N,rank,adapters,none,run,pad,at", ADAPTS)
