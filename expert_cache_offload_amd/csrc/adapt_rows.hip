@@ -23,9 +23,11 @@ typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 1024;
 // Calls whose x, base and out are more than this together pass the caches by: they would push out the
-// adapters (2048 to 2048 of rank 64: 16384 rows 67 us without, 59 with; 8192 rows 41 and 36; 6144 rows,
-// 75 MB, 25 both).
-constexpr int64_t kAdaptStreamBytes = 64 << 20;
+// adapters (2048 to 2048 of rank 64: 16384 rows, 201 MB, 57.7 us without, 52.3 with; 8192 rows 33.3 and
+// 29.5; 6144 rows, 75 MB, 21.1 and 24.4).  Only where rows of out start with a half line: a store that
+// passes the caches by is not joined with its neighbour's part of the line (16384 rows, 1024 to 3000
+// of rank 32, 100 us with and 69 without; 1024 to 2976 equal).
+constexpr int64_t kAdaptStreamBytes = 80 << 20;
 
 struct AdaptArgs {
   const void* x;
@@ -273,8 +275,8 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
   // A block of channels: its rows of B, a lane a chunk of NBL of them, and the base's chunks
   const int blocks = (a.N + NB - 1) / NB, step = t.parts * W;
   const bool short_rank = a.rank < V;
-  // whole blocks; the others (the last where N is no multiple, all where the rank is below 16
-  // bytes) go element by element
+  // whole blocks; of the others (the last where N is no multiple, all where the rank is below 16
+  // bytes) a lane's chunk may be short
   const int whole = short_rank ? 0 : a.N / NB;
   const int bc = lane % RC * V;  // first element of this lane's chunk of a row of B
   const E* const bg = (const E*)a.b + (int64_t)t.g * a.N * a.bs;
@@ -448,12 +450,13 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
         for (int e = 0; e < V; ++e)
           f[e] = fmaf(f[e], back, a.base ? to_f32(bk[at].e[e]) : 0.f);
         const Chunk<E> v = round_chunk<E, V>(f);
-        if (all) {
+        const int n = a.N - nb * NB - oc;
+        if (all || n >= V) {
           store_chunk<STREAM>(out[at] + nb * NB, v);
         } else {
 #pragma unroll
-          for (int e = 0; e < V; ++e)
-            if (nb * NB + oc + e < a.N) out[at][nb * NB + e] = v.e[e];
+          for (int e = 0; e < V - 1; ++e)
+            if (e < n) out[at][nb * NB + e] = v.e[e];
         }
       }
     }
@@ -478,10 +481,17 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
                             : load_full(b + min(bc, a.rank - V));
     }
 #pragma unroll
-    for (int i = 0; i < NO; ++i)
+    for (int i = 0; i < NO; ++i) {
+      bases[i].q = u32x4{0, 0, 0, 0};
+      const int n = a.base ? a.N - nb * NB - oc : 0;
+      if (n >= V) {
+        bases[i] = load_chunk<V, STREAM>(base[i] + nb * NB);
+      } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        bases[i].e[e] = a.base && nb * NB + oc + e < a.N ? base[i][nb * NB + e] : E{};
+        for (int e = 0; e < V - 1; ++e)
+          if (e < n) bases[i].e[e] = base[i][nb * NB + e];
+      }
+    }
     put_b(bq[0]);
     use_block(bases, nb, false);
   }
@@ -506,7 +516,9 @@ int adapt_shares(const AdaptArgs& a, int tiles, int rows, int blocks, int waves)
 }
 template <class E>
 bool streams(const AdaptArgs& a) {
-  return (int64_t)a.M * (a.K + (a.base ? 2 : 1) * (int64_t)a.N) * (int)sizeof(E) > kAdaptStreamBytes;
+  return (int64_t)a.M * (a.K + (a.base ? 2 : 1) * (int64_t)a.N) * (int)sizeof(E) >
+             kAdaptStreamBytes &&
+         (uintptr_t)a.out % 64 == 0 && a.os * (int64_t)sizeof(E) % 64 == 0;
 }
 template <class E, int RT, int MT, int UC, int W>
 hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
@@ -527,9 +539,12 @@ hipError_t launch_adapt_by(const AdaptArgs& a, hipStream_t s) {
 }
 template <class E>
 hipError_t launch_adapt(const AdaptArgs& a, hipStream_t s) {
-  // 32 rows a tile where there are 128 such tiles and the adapters have so many rows (rank 64, 2048 to
-  // 2048: 1024 rows 12.6 us with 16 rows a tile, 13.5 with 32; 4096 rows 23.2 and 20.5)
-  const bool wide = a.M >= std::max(4096, 32 * (a.offsets ? a.adapters : 1));
+  // 32 rows a tile read A and B half as often, but leave a CU half as many waves: taken for many rows of a
+  // high rank (rank 64, 2048 to 2048: 4096 rows 19.4 us with 16 rows a tile, 20.2 with 32, 6144 rows
+  // 23.6 and 21.1, 16384 60.9 and 51.5; rank 32: 8192 rows, 2048 to 4096, 41.9 and 47.0, 20000 rows,
+  // 2048 to 2048, 55.0 and 51.3; rank 16: 16384 rows 41.0 and 45.4), where an adapter has so many
+  const bool wide = (int64_t)a.M * (a.rank <= 32 ? 32 : 64) >= 6144 * 64 &&
+                    a.M >= 32 * (a.offsets ? a.adapters : 1);
   // Eight waves where tiles are few and the work of each long: ranks up to 32 with long rows of x (rank 32,
   // N = 2048: one row of 6144 10.0 us with four waves, 9.6 with eight; 256 rows of 512 5.6 and 6.0, of
   // 4096 11.4 and 10.2; 1024 rows of 4096 15.2 and 13.3; but 4000 rows, 4096 to 4096, 35 and 45), rank 64
@@ -539,9 +554,7 @@ hipError_t launch_adapt(const AdaptArgs& a, hipStream_t s) {
   const bool few = a.M <= 1024 && !streams<E>(a);
   const bool deep = few && (a.rank <= 32 ? row >= (a.M < 256 ? 8192 : 2048) : row <= 4096 || a.M <= 64);
   if (a.rank <= 16)
-    return wide   ? launch_adapt_by<E, 1, 2, 8, 4>(a, s)
-           : deep ? launch_adapt_by<E, 1, 1, 8, 8>(a, s)
-                  : launch_adapt_by<E, 1, 1, 8, 4>(a, s);
+    return deep ? launch_adapt_by<E, 1, 1, 8, 8>(a, s) : launch_adapt_by<E, 1, 1, 8, 4>(a, s);
   if (a.rank <= 32)
     return wide   ? launch_adapt_by<E, 2, 2, 8, 4>(a, s)
            : deep ? launch_adapt_by<E, 2, 1, 8, 8>(a, s)

@@ -48,14 +48,13 @@ def route_grad_args(T, E, k, kind):
 def adapts(kind):
     """M, K, N, rank, adapters: each range of ranks with few rows an adapter and many, short rows and
     long, below and above what streams."""
-    few, out = 600 * SIZE[kind], []
+    out = []
     for rank in (10, 32, 49, 100):
-        out += [(130, 90, 70, rank, 40), (4200, 70, 90, rank, 3)]
+        out += [(130, 90, 70, rank, 40), (12300, 70, 90, rank, 3)]
         if rank <= 64:
-            out.append((300, 2100, 130, rank, 40))
-            # rows in tiles of 16, above 64 MiB
-            out.append((30000, 300, (1 << 26) // 30000 // few * 300 + 300, rank, 1000))
-        out.append(((1 << 26) // (300 * SIZE[kind]) + 9, 100, 100, rank, 5))
+            # rows in tiles of 16, above 80 MiB in whole half lines
+            out += [(300, 2100, 130, rank, 40), (30000, 300, 640, rank, 1000)]
+        out.append(((80 << 20) // (292 * SIZE[kind]) + 9, 100, 96, rank, 5))
     return out
 
 
