@@ -11,7 +11,7 @@ P = 1 << 20  # an address, where nothing is launched
 def norms(kind):
     """M, K: few rows of every width, and of every width that is held in pieces of 16 bytes as many
     rows as make the smallest call of both directions stream."""
-    widths = (3, 60, 300, 500, 1001, 2000, 3000, 5001, 9000)
+    widths = (3, 64, 300, 448, 960, 2000, 3000, 5001, 9000)
     few = [(9, K) for K in widths]
     return few + [((128 << 20) // (2 * K * SIZE[kind]) + 5, K) for K in widths[1:]]
 
