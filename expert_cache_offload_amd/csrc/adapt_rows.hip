@@ -107,7 +107,9 @@ constexpr int kCus = 256;
 __host__ __device__ constexpr int parts_of_rest(int rest, int most) {
   return rest > 0 && kCus / rest > 1 ? (kCus / rest < most ? kCus / rest : most) : 1;
 }
-__host__ __device__ constexpr int most_parts(int N) { return N / 256 > 1 ? N / 256 : 1; }
+__host__ __device__ constexpr int most_parts(int N) {
+  return N / 256 > kCus ? kCus : N / 256 > 1 ? N / 256 : 1;
+}
 // The row tile (of BM rows, counted over the adapters) of workgroup column b, by every wave for itself,
 // 64 adapters at a time; g = -1 where there is none.  Workgroups go round the eight dies, so each
 // die is given a run of neighbouring tiles: its L2 then holds the one or two adapters that they
@@ -507,7 +509,7 @@ __global__ __launch_bounds__(64 * W) void adapt_rows_kernel(AdaptArgs a) {
 // rank 64, 2048 to 2048: 15.5, 12.6 and 15.7 us with 1, 2 and 4; 664 rows, 864 to 3080: 20.5, 16.0,
 // 13.7 and 12.4 with 1, 2, 4 and 8; 4096 rows, 2048 to 2048: 20.5 and 23.4 with 1 and 2), up to four
 // workgroups for a CU (4480 rows of rank 32, 112 to 7072, in 140 tiles: 55, 48 and 51 us with 1, 8
-// and 14).
+// and 14); all by four waves.
 constexpr double kShareRate = 215.0;
 int adapt_shares(const AdaptArgs& a, int tiles, int rows, int blocks, int waves) {
   const double p1 = (double)a.K * (rows + a.rank), p2 = (double)a.N * (a.rank + 2 * rows);
