@@ -218,6 +218,22 @@ def test_route_grad(env, T, E, k, G, kept, pad, masked, kind, score):
             bool((wide[:, 1 + E:] == 77).all())
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("T,E,scale", [(1, 1, 1.0), (31, 8, 1.0), (612, 60, 16.0), (1749, 64, 2.5)])
+def test_route_grad_of_one_renormalised_choice(env, T, E, scale, kind, score):
+    """A single score divided by itself is one whatever the logits are: the gradient is zero, exactly,
+    and it is written."""
+    torch, m, types, tid = env
+    g = _gen(torch, T)
+    z = _logits(torch, g, T, E, types[kind])
+    idx = torch.randint(0, E, (T, 1), generator=g, device="cuda").to(torch.int32)
+    dw = torch.randn(T, 1, generator=g, device="cuda")
+    dz = torch.full((T, E), 77.0, dtype=types[kind], device="cuda")
+    m.moe_route_tokens_grad(z, E, tid[kind], T, E, score, idx, 1, True, scale, dw, dz, E)
+    assert not bool(dz.any())
+
+
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_route_grad_against_differences(env, score, renorm):
