@@ -8,7 +8,7 @@
 //
 // A row is read once and held in registers between its sums and its outputs, so both directions
 // are bound by the bytes of the matrices.  Sums over a row are held in 64 bits, over a chunk of 16
-// bytes in fp32.
+// bytes in fp32, but where a row's squares or products leave its range.
 #include <algorithm>
 #include <type_traits>
 
@@ -158,15 +158,33 @@ __device__ __forceinline__ double lane_squares(const Chunk<E, V> (&h)[HELD], int
                                                int nc) {
   return lane_squares<G>(h, K, lane, nc, [](const Chunk<E, V>& c) { return chunk_squares(c); });
 }
-// 1 / sqrt(mean of the squares + eps), sq their sum.
+// 1 / sqrt(mean of the squares + eps), sq their sum (summed again where fp32 may have lost some).
 template <int G, class E, int V>
-__device__ __forceinline__ double row_factor(const Chunk<E, V> (&h)[HELD], double sq, int K,
+__device__ __forceinline__ double row_factor(const Chunk<E, V> (&h)[HELD], double& sq, int K,
                                              float eps, int lane, int nc, double* s_part) {
   if (sizeof(E) == 2 && !far_inside(sq))
     sq = row_sum<G>(lane_squares<G>(h, K, lane, nc,
                                     [](const Chunk<E, V>& c) { return chunk_squares_f64(c); }),
                     s_part);
   return rsqrt(sq / K + (double)eps);
+}
+
+// A number's exponent, from 0 (zero) to 2047; 1023 from one to two.
+__device__ __forceinline__ uint32_t exponent(double v) {
+  return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 52) & 0x7ff;
+}
+// Whether a row's dot in fp32 has lost something that dx would show (fp16's never has).  Beside 2^-100
+// terms below fp32's normal numbers are nothing; below 2^100 no term left the range (the dot would be
+// infinite or NaN), nor does n mean(w dy n), n up to 128.  Where all terms are lost, below 2^-150, dx is
+// off by up to 128 q^2 2^-150: nothing beside its normal numbers up to q = 2^8, nor in a row of zeros.
+template <class E>
+__device__ __forceinline__ bool dot_lost(double dot, double sq, double q) {
+  if (__is_same(E, fp16_t) || exponent(dot) - (1023 - 100) < 200u) return false;
+  return dot != 0.0 || (q >= 0x1p8 && sq > 0.0);
+}
+// 2^e, or the power of two of fp32's normal numbers that is nearest to it.
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
 }
 
 // The exact code of p beside the row's largest magnitude m: p and m are products of two numbers of 24
@@ -297,8 +315,8 @@ void norm_rows_kernel(NormArgs a) {
         h[i] = round_chunk<E, V>(f);
       }
     }
-    const double q = row_factor<G>(h, row_sum<G>(lane_squares<G>(h, a.K, lane, nc), s_sum), a.K, a.eps,
-                                   lane, nc, s_sum);
+    double sq = row_sum<G>(lane_squares<G>(h, a.K, lane, nc), s_sum);
+    const double q = row_factor<G>(h, sq, a.K, a.eps, lane, nc, s_sum);
     const float qf = (float)q;
     // every lane has read its part of the row (it may be overwritten now)
     if (a.sum) {
@@ -365,6 +383,7 @@ __global__ __launch_bounds__(norm_threads(G), 2)
 void norm_rows_grad_kernel(NormGradArgs a) {
   constexpr int THR = norm_threads(G), ROWS = THR / G;
   __shared__ double s_part[THR / 64], s_both[THR / 64][2];
+  __shared__ float s_big[THR / 64];
   constexpr bool AHEAD = THR < 1024;  // a thousand threads have no registers for it
   extern __shared__ __align__(16) float s_dw[];  // [ROWS][K], where ROWS > 1
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
@@ -416,6 +435,32 @@ void norm_rows_grad_kernel(NormGradArgs a) {
     row_sums<G>(sq, dot, s_both);
     const double q = row_factor<G>(h, sq, a.K, a.eps, lane, nc, s_part);
     const float qf = (float)q;
+    float by = 1.f, qb = qf;  // a power of two that brings w dy into fp32's range, and q / by
+    const bool far = dot_lost<E>(dot, sq, q);
+    if (far) {
+      dot = 0.0;
+      int big = 0;
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) {
+        const int c = lane + i * G;
+        if (c >= nc) continue;
+        forget_derived(h[i]);
+        forget_derived(g[i]);
+        forget_derived(w[i]);
+        const int had = c * V - chunk_at<V>(c, a.K);  // elements that the chunk before has
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const double wg = (double)to_f32(w[i].e[e]) * (double)to_f32(g[i].e[e]);
+          dot = fma((double)to_f32(h[i].e[e]), e < had ? 0.0 : wg, dot);
+          big = max(big, (int)exponent(wg));
+        }
+      }
+      dot = row_sum<G>(dot, s_part);
+      big = (int)row_max<G>((float)big, s_big);
+      by = big > 0 ? power_of_two(1023 - big) : 1.f;
+      qb = (float)(q / by);
+      dot *= by;
+    }
     const float along = (float)(q * dot / a.K);  // mean of w dy (q h)
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
@@ -424,12 +469,20 @@ void norm_rows_grad_kernel(NormGradArgs a) {
       forget_derived(g[i]);
       forget_derived(w[i]);
       float f[V];
+      if (far) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          f[e] = (float)((double)to_f32(w[i].e[e]) * (double)to_f32(g[i].e[e]) * (double)by);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = to_f32(w[i].e[e]) * to_f32(g[i].e[e]);
+      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float n = to_f32(h[i].e[e]) * qf, gf = to_f32(g[i].e[e]);
-        dw[i][e] = fmaf(gf, n, dw[i][e]);
+        const float n = to_f32(h[i].e[e]) * qf;
+        dw[i][e] = fmaf(to_f32(g[i].e[e]), n, dw[i][e]);
         const float own = a.dsum ? to_f32(d[i].e[e]) : 0.f;
-        f[e] = fmaf(qf, fmaf(-n, along, to_f32(w[i].e[e]) * gf), own);
+        f[e] = fmaf(qb, fmaf(-n, along, f[e]), own);
       }
       if (a.dx)
         store_chunk<STREAM>((E*)a.dx + row * a.dxs + chunk_at<V>(lane + i * G, a.K),

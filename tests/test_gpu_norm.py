@@ -277,6 +277,38 @@ def test_norm_grad_of_far_rows(env):
                     eps)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [3, 300, 700, 2000, 4097, 16384])
+def test_norm_grad_of_far_products(env, kind, K):
+    """Rows, gradients and weights whose products leave fp32's range though dx does not: too large, too
+    small, all of them lost, some of a row's; and a row without a gradient, which has none."""
+    torch, m, types, tid = env
+    g = _gen(torch, K)
+    #        h     dy
+    rows = [(1e20, 1e20), (1e25, 1e14), (1e30, 1e30), (1e-20, 1e-25), (1e-25, 1e-20), (1e-30, 1e-10),
+            (1e-12, 1e-33), (1e37, 1e37), (1, 1e-37), (1e-12, 1e-25), (1, 1), (1e-3, 0), (1e5, 0)]
+    M = len(rows)
+    h, dy = (torch.randn(M, K, generator=g, device="cuda").double() for _ in "ab")
+    size = torch.tensor(rows, dtype=torch.float64, device="cuda")
+    h, dy = h * size[:, :1], dy * size[:, 1:]
+    h[10, 0], dy[10, 0] = 1e20, 1e20  # one term of a row alone
+    dsum = torch.randn(M, K, generator=g, device="cuda").to(types[kind])
+    h, dy = h.to(types[kind]), dy.to(types[kind])
+    for scale in (1.0, 1e12, 1e-20):
+        w = (scale * (0.5 + torch.rand(K, generator=g, device="cuda"))).to(types[kind])
+        for eps in (1e-6, 1e-37):
+            # rows whose dx is a number of the type
+            ref = _grad_ref(torch, dy, None, h, w, eps)[0]
+            keep = torch.nonzero(ref.abs().amax(1) < torch.finfo(types[kind]).max / 4)[:, 0]
+            assert keep.numel() > 6
+            args = [t[keep].contiguous() for t in (dy, dsum, h)]
+            _check_grad(env, *args, w, kind, _run_grad(env, *args, w, kind, eps=eps), eps)
+            args[1] = None
+            out = _run_grad(env, *args, w, kind, eps=eps)
+            _check_grad(env, *args, w, kind, out, eps)
+            assert not bool(out[1][(args[0] == 0).all(1)].any())
+
+
 def test_norm_grad_against_differences(env):
     """fp32: the directional derivative of a weighted sum of y, and of the sum's own way."""
     torch, m, types, tid = env
