@@ -586,7 +586,8 @@ extern "C" moe_status moe_adapt_rows(const void* x, int64_t x_stride, int32_t ty
   if (M == 0) return MOE_OK;  // before the pointers: empty buffers have none
   if (!rows_ok(x, x_stride, K, type) || !rows_ok(a, a_stride, K, type) ||
       !rows_ok(b, b_stride, rank, type) || !rows_ok(out, out_stride, N, type) ||
-      (base && !rows_ok(base, base_stride, N, type)) || !aligned4(scale) || !aligned4(offsets) ||
+      (base && !rows_ok(base, base_stride, N, type)) ||
+      !same_rows(out, out_stride, base, base_stride) || !aligned4(scale) || !aligned4(offsets) ||
       !aligned4(order) || !on_current_device(out))
     return MOE_E_INVALID;
   AdaptArgs p{x, x_stride, M, K, a, a_stride, b, b_stride, N, rank, scale, adapters,

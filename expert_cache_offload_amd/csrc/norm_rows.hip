@@ -596,11 +596,6 @@ hipError_t launch_norm_grad(NormGradArgs& a, float* dweight, float* ws, hipStrea
                        dim3(PART_COLS * PART_SHARES), 0, s, (const float*)ws, parts, a.K, dweight);
 }
 
-// An output that is written over an input has its rows.
-bool same_rows(const void* out, int64_t out_s, const void* in, int64_t in_s) {
-  return !out || out != in || out_s == in_s;
-}
-
 bool norm_ok(int type, int M, int K, float eps) {
   return float_type(type) && M >= 0 && M <= kMaxRows && K >= 1 && K <= kMaxNormCols && eps > 0.f &&
          eps < __builtin_inff();

@@ -282,6 +282,11 @@ inline bool rows_ok(const void* p, int64_t stride, int64_t cols, int type) {
   return p && stride >= cols && stride <= ((int64_t)1 << 40) &&
          (uintptr_t)p % elem_bytes(type) == 0;
 }
+// An output that is written over an input has its rows: with another stride a row's output lies over
+// other rows' inputs, which may not have been read yet.
+inline bool same_rows(const void* out, int64_t out_s, const void* in, int64_t in_s) {
+  return !out || out != in || out_s == in_s;
+}
 
 // The buffers' device has to be the current one: kernels are launched there.  Looked up only
 // where there is more than one device.

@@ -565,9 +565,11 @@ moe_status moe_route_tokens_grad(const void* logits, int64_t logits_stride, int3
  * = 1) for all M rows.  order: the row of x, base and out of each sorted row (distinct; what lies
  * outside [0, M) is left out); NULL: the rows lie sorted.  Both as moe_sort_tokens writes them with
  * top_k = 1 from a row's adapter, an id outside [0, adapters) for none.
- * base: [M][N], out itself, or NULL (nothing is added to).  Rows without an adapter are left as they
- * were.  All matrices are of `type` (bf16, fp16 or fp32); x A^T is held in fp32 (16-bit types: 16 bits
- * of it at least enter the second product).
+ * base: [M][N], out itself (then with its stride), or NULL (nothing is added to).  out is not x: a row
+ * of x may be read after parts of it are written.  Rows of out without an adapter are left as they
+ * were, also where base is another matrix: they do not receive its rows.  All matrices are of `type`
+ * (bf16, fp16 or fp32); x A^T is held in fp32 (16-bit types: 16 bits of it at least enter the second
+ * product).
  * M 0..16777215, K and N 1..1048576, rank 1..128, adapters 1..1024. */
 moe_status moe_adapt_rows(const void* x, int64_t x_stride, int32_t type, int32_t M, int32_t K,
                           const void* a, int64_t a_stride, const void* b, int64_t b_stride,

@@ -113,6 +113,12 @@ def test_adapt_refuses(bad):
     _refused("moe_adapt_rows", _m().MOE_E_INVALID, **{**ADAPT, **bad})
 
 
+def test_adapt_refuses_base_over_other_rows_of_out():
+    over = dict(base=2 * Q, out=2 * Q)
+    for strides in (dict(out_stride=49), dict(base_stride=49), dict(base_stride=96, out_stride=48)):
+        _refused("moe_adapt_rows", _m().MOE_E_INVALID, **{**ADAPT, **over, **strides})
+
+
 def test_no_rows_with_empty_buffers():
     m = _m()
     m.moe_norm_rows(None, 64, None, 64, BF16, 0, 64, None, 1e-6, None, 64, None, 64)
