@@ -789,7 +789,8 @@ moe_status moe_route_tokens_grad(const void* logits, int64_t logits_stride, int3
   if (T == 0) return MOE_OK;  // before the pointers: empty buffers have none
   if (!rows_ok(logits, logits_stride, experts, type) || !topk_idx || !dweights ||
       !aligned4(topk_idx) || !aligned4(dweights) ||
-      !rows_ok(dlogits, dlogits_stride, experts, type) || !on_current_device(dlogits))
+      !rows_ok(dlogits, dlogits_stride, experts, type) ||
+      !same_rows(dlogits, dlogits_stride, logits, logits_stride) || !on_current_device(dlogits))
     return MOE_E_INVALID;
   RouteGradArgs a{logits, logits_stride, T, experts, score, topk_idx, top_k,
                   renormalise, scale, dweights, dlogits, dlogits_stride};

@@ -548,7 +548,8 @@ moe_status moe_route_tokens(const void* logits, int64_t logits_stride, int32_t t
 /* Gradient of moe_route_tokens' weights for the logits, dlogits [T][experts] of `type` (the choice
  * itself has none): the logits and options of the forward call and the experts it chose; an id
  * outside [0, experts) has no part, and a token's others have to be distinct.  With renormalise or
- * sigmoid scores only the chosen logits have a gradient, the others get zeros. */
+ * sigmoid scores only the chosen logits have a gradient, the others get zeros.  dlogits may be logits
+ * itself (then with its stride). */
 moe_status moe_route_tokens_grad(const void* logits, int64_t logits_stride, int32_t type,
                                  int32_t T, int32_t experts, int32_t score,
                                  const int32_t* topk_idx, int32_t top_k, int32_t renormalise,

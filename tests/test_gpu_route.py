@@ -220,6 +220,24 @@ def test_route_grad(env, T, E, k, G, kept, pad, masked, kind, score):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("T,E,k", [(1, 5, 2), (33, 64, 8), (700, 257, 4), (50, 1024, 16)])
+def test_route_grad_in_place(env, T, E, k, kind, score):
+    """The gradient over the logits themselves."""
+    torch, m, types, tid = env
+    g = _gen(torch, T)
+    z = _logits(torch, g, T, E, types[kind])
+    idx = torch.rand(T, E, generator=g, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    for renorm in (True, False):
+        args = (tid[kind], T, E, score, idx, k, renorm, 2.5, dw)
+        dz, own = torch.full((T, E), 77.0, dtype=types[kind], device="cuda"), z.clone()
+        m.moe_route_tokens_grad(z, E, *args, dz, E)
+        m.moe_route_tokens_grad(own, E, *args, own, E)
+        assert torch.equal(own, dz)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
 @pytest.mark.parametrize("T,E,scale", [(1, 1, 1.0), (31, 8, 1.0), (612, 60, 16.0), (1749, 64, 2.5)])
 def test_route_grad_of_one_renormalised_choice(env, T, E, scale, kind, score):
     """A single score divided by itself is one whatever the logits are: the gradient is zero, exactly,

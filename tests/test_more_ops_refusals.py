@@ -99,6 +99,12 @@ def test_route_grad_refuses(bad):
     _refused("moe_route_tokens_grad", _m().MOE_E_INVALID, **{**ROUTE_GRAD, **bad})
 
 
+@pytest.mark.parametrize("over", [dict(dlogits_stride=65), dict(logits_stride=65)])
+def test_route_grad_refuses_other_rows(over):
+    _refused("moe_route_tokens_grad", _m().MOE_E_INVALID,
+             **{**ROUTE_GRAD, "logits": Q, "dlogits": Q, **over})
+
+
 ADAPT = v.adapt_args(16, 64, 48, 8, 4, "fp16")
 
 
