@@ -369,7 +369,7 @@ struct NormGradArgs {
   int M, K;
   const void* w;
   float eps;
-  void* dx;  // may be null, dy or dsum
+  void* dx;  // may be null, dy, dsum or h
   int64_t dxs;
   float* part;  // [workgroups][K] sums of q dy h over a workgroup's rows; null: no dweight
 };
@@ -651,7 +651,8 @@ moe_status moe_norm_rows_grad(const void* dy, int64_t dy_stride, const void* dsu
                 (dsum && !rows_ok(dsum, dsum_stride, K, type)) ||
                 (dx && !rows_ok(dx, dx_stride, K, type)) ||
                 !same_rows(dx, dx_stride, dy, dy_stride) ||
-                !same_rows(dx, dx_stride, dsum, dsum_stride)))
+                !same_rows(dx, dx_stride, dsum, dsum_stride) ||
+                !same_rows(dx, dx_stride, sum, sum_stride)))
     return MOE_E_INVALID;
   const size_t need = dweight ? moe_norm_grad_workspace_bytes(M, K) : 0;
   if (need && (!workspace || !aligned4(workspace))) return MOE_E_INVALID;

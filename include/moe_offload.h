@@ -512,7 +512,7 @@ size_t moe_norm_grad_workspace_bytes(int32_t M, int32_t K);
  * forward pass's sum, or x without a residual); dy: the gradient of y; dsum: what reaches h by
  * other ways (may be NULL).  With q = 1 / sqrt(mean(h^2) + eps):
  *   dx = dsum + q * weight * dy - h * q^3 * mean(weight * dy * h), the gradient of x and of residual
- *     alike; dx may be dy or dsum itself (then with its stride);
+ *     alike; dx may be dy, dsum or sum itself (then with its stride);
  *   dweight [K] fp32 = sum over the rows of q * dy * h (M = 0: zeros).
  * dx or dweight may be NULL; without dweight no workspace is needed.  Sizes as moe_norm_rows.
  * MOE_E_SCRATCH when workspace_bytes is below moe_norm_grad_workspace_bytes. */

@@ -264,6 +264,22 @@ def test_norm_grad_in_place_and_repeated(env, kind, K):
     assert not bool(dw.any())
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,K", [(1, 3), (300, 5), (5000, 72), (3000, 700), (2500, 2001), (900, 9001),
+                                 (600, 16384)])
+def test_norm_grad_over_the_sum(env, kind, M, K):
+    """dx over the rows that were normalised."""
+    torch, m, types, tid = env
+    g = _gen(torch, K + M)
+    dy, dsum, h = (torch.randn(M, K, generator=g, device="cuda").to(types[kind]) for _ in "abc")
+    w = torch.rand(K, generator=g, device="cuda").to(types[kind])
+    _, ref, ref_w = _run_grad(env, dy, dsum, h, w, kind)
+    size = m.moe_norm_grad_workspace_bytes(M, K)
+    ws, dw = torch.empty(size + 16, dtype=torch.uint8, device="cuda"), torch.empty(K, device="cuda")
+    m.moe_norm_rows_grad(dy, K, dsum, K, h, K, tid[kind], M, K, w, EPS, h, K, dw, ws, size)
+    assert torch.equal(h, ref) and torch.equal(dw, ref_w[:K])
+
+
 def test_norm_grad_of_far_rows(env):
     """Rows, and an eps, so small or large that the factor's cube leaves fp32's range."""
     torch, m, types, tid = env

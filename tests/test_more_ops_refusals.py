@@ -99,6 +99,12 @@ def test_route_grad_refuses(bad):
     _refused("moe_route_tokens_grad", _m().MOE_E_INVALID, **{**ROUTE_GRAD, **bad})
 
 
+@pytest.mark.parametrize("over", [dict(dx_stride=65), dict(sum_stride=65)])
+def test_norm_grad_refuses_other_rows_of_the_sum(over):
+    _refused("moe_norm_rows_grad", _m().MOE_E_INVALID,
+             **{**GRAD, "dy": Q, "sum": 2 * Q, "dx": 2 * Q, **over})
+
+
 @pytest.mark.parametrize("over", [dict(dlogits_stride=65), dict(logits_stride=65)])
 def test_route_grad_refuses_other_rows(over):
     _refused("moe_route_tokens_grad", _m().MOE_E_INVALID,
