@@ -566,13 +566,15 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   });
 }
 
-// Parts of dw (workgroups of the gradient's launch).
-constexpr int kMaxParts = 512;
+// Parts of dw (workgroups of the gradient's launch): as many as the CUs hold at once, and so many that a
+// lane adds up no more than kPartRows rows in fp32.
+constexpr int kMaxParts = 512, kPartRows = 256;
 template <class E>
 int grad_parts(int M, int K) {
   return by_width<E>(K, [&](auto, auto g) {
-    constexpr int G = decltype(g)::value;
-    return norm_grid(M, norm_threads(G) / G, G > 256 ? 256 : kMaxParts);
+    constexpr int G = decltype(g)::value, ROWS = norm_threads(G) / G;
+    const int few = (M + ROWS * kPartRows - 1) / (ROWS * kPartRows);
+    return norm_grid(M, ROWS, std::max(few, G > 256 ? 256 : kMaxParts));
   });
 }
 

@@ -513,7 +513,8 @@ size_t moe_norm_grad_workspace_bytes(int32_t M, int32_t K);
  * other ways (may be NULL).  With q = 1 / sqrt(mean(h^2) + eps):
  *   dx = dsum + q * weight * dy - h * q^3 * mean(weight * dy * h), the gradient of x and of residual
  *     alike; dx may be dy, dsum or sum itself (then with its stride);
- *   dweight [K] fp32 = sum over the rows of q * dy * h (M = 0: zeros).
+ *   dweight [K] fp32 = sum over the rows of q * dy * h (M = 0: zeros), in fp32 over 4096 rows at most
+ *     (256 one after the other, 16 such sums), in 64 bits over these.
  * dx or dweight may be NULL; without dweight no workspace is needed.  Sizes as moe_norm_rows.
  * MOE_E_SCRATCH when workspace_bytes is below moe_norm_grad_workspace_bytes. */
 moe_status moe_norm_rows_grad(const void* dy, int64_t dy_stride, const void* dsum,

@@ -280,6 +280,23 @@ def test_norm_grad_over_the_sum(env, kind, M, K):
     assert torch.equal(h, ref) and torch.equal(dw, ref_w[:K])
 
 
+def test_norm_grad_of_the_most_rows(env):
+    """The weight's gradient is as exact over many rows as over few: 2^24 - 1 equal terms, which an
+    addition in fp32 rounds to the same side each time once some hundreds are summed.  The
+    roundings of 256 additions one after the other, those of 16 such sums, the term's own three and
+    the result's, however many rows there are."""
+    torch, m, types, tid = env
+    M, K = (1 << 24) - 1, 3
+    term = 1 + 2.0 ** -14 - 2.0 ** -20
+    dy, h = torch.full((M, K), term, device="cuda"), torch.ones(M, K, device="cuda")
+    w = torch.ones(K, device="cuda")
+    size = m.moe_norm_grad_workspace_bytes(M, K)
+    ws, dw = torch.empty(size, dtype=torch.uint8, device="cuda"), torch.zeros(K, device="cuda")
+    m.moe_norm_rows_grad(dy, K, None, 0, h, K, tid["fp32"], M, K, w, 1e-30, None, K, dw, ws, size)
+    off = (dw.double() / (M * term) - 1).abs()
+    assert bool((off <= U32 * (256 + 16 + 3 + 1)).all()), off
+
+
 def test_norm_grad_of_far_rows(env):
     """Rows, and an eps, so small or large that the factor's cube leaves fp32's range."""
     torch, m, types, tid = env

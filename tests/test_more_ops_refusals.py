@@ -73,6 +73,14 @@ def test_norm_grad_workspace():
              **{**GRAD, "type": BF16, "workspace_bytes": need - 1})
 
 
+@pytest.mark.parametrize("K,rows", [(3, 16), (64, 16), (300, 8), (1000, 4), (2000, 1), (16384, 1)])
+def test_norm_grad_workspace_of_many_rows(K, rows):
+    """A part of the weight's gradient holds 256 rows of each of a workgroup's row groups at most."""
+    m = _m()
+    for M in (1, 500, 1 << 17, (1 << 24) - 1):
+        assert m.moe_norm_grad_workspace_bytes(M, K) >= 4 * K * (-(-M // (256 * rows)) if M > 1 else 0)
+
+
 ROUTE = v.route_args(16, 64, 8, 8, 2, 4, "fp32")
 
 
