@@ -38,10 +38,14 @@ struct NormArgs {
 };
 
 // Calls that move more bytes than this pass the caches by: what they read is not read again soon (32768
-// rows of 2048 bf16 113 us so, 120 otherwise; the gradient 95 and 106).  Short rows, which share an
-// access's lines with their neighbours, only where they start with a half line: stores that pass the
-// caches by are not joined (100000 rows of 1000 bf16 230 us so, 190 otherwise; of 2431, 32768 rows, 174
-// and 175).
+// rows of 2048 bf16 111 us so, 120 otherwise; the gradient 93 and 106).  Stores that pass the caches by
+// are not joined, so where a row's ends lie inside lines that neighbouring rows share, the lines are
+// written in parts: rows that 32 lanes or fewer hold stream only where sum and y start with a half line
+// (65536 rows of 1024 bf16 with codes 111 us streamed and 120 not, sum and y at a stride of 1027 143 and
+// 130; of 1000 149 and 127, at a stride of 1024 120 and 135; of 512, at a stride of 515 177 and 139), those
+// of 16 lanes only where the codes do too (sum and codes of 500, the codes at their own stride 109 and
+// 101, at 512 93 and 108; of 1000 95 and 97).  Longer rows stream wherever they start (of 2051 131 and 129,
+// of 4099 146 and 152), and so do the gradient's (of 1027 106 and 111, of 515 118 and 116).
 constexpr int64_t kNormStreamBytes = 128 << 20;
 // A row is held by G lanes, 16, 32, 64 or (all of) a workgroup.
 constexpr int norm_threads(int G) { return G < 256 ? 256 : G; }
@@ -552,12 +556,20 @@ auto by_width(int K, F&& f) {
 // Workgroups of a launch over M rows, `rows` at a time each.
 int norm_grid(int M, int rows, int most) { return std::min((M + rows - 1) / rows, most); }
 
+// Every row of an output (if there is one) starts with half a line.
+bool starts_half_line(const void* out, int64_t row_bytes) {
+  return !out || ((uintptr_t)out % 64 == 0 && row_bytes % 64 == 0);
+}
+
 template <class E>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return by_width<E>(a.K, [&](auto v, auto g) {
     constexpr int V = decltype(v)::value, G = decltype(g)::value, THR = norm_threads(G);
     const int64_t row = (int64_t)sizeof(E) * (1 + !!a.res + !!a.sum + !!a.y) + !!a.codes;
-    const bool stream = row * a.K * a.M > kNormStreamBytes && (G > 32 || a.K % 64 == 0);
+    const bool starts = starts_half_line(a.sum, a.sum_s * (int64_t)sizeof(E)) &&
+                        starts_half_line(a.y, a.ys * (int64_t)sizeof(E)) &&
+                        (G > 16 || starts_half_line(a.codes, a.cs));
+    const bool stream = row * a.K * a.M > kNormStreamBytes && (G > 32 || starts);
     // rows below 16 bytes are never streamed: their kernel is bound by their number
     const auto kernel = V > 1 && stream ? norm_rows_kernel<E, V, G, V != 1>
                                         : norm_rows_kernel<E, V, G, false>;

@@ -49,6 +49,26 @@ def test_failed_launch_ends_the_call(calls):
         assert r["error"] == 0, name
 
 
+def test_short_rows_stream_where_their_outputs_start_with_half_a_line(calls):
+    """By the addresses and strides of what is written, not by the rows' length."""
+    streams = "Lb1E"  # the kernels' last template argument
+    codes = {"codes": None, "scale": None}
+    at = dict(sum_stride=1024, y_stride=1024, codes_stride=1024)
+    wanted = []
+    for K in (512, 500, 1000, 1024):
+        base = {**v.norm_args(1 << 18, K, "bf16"), "x": 3 * v.P, "x_stride": K + 3,
+                "residual": 3 * v.P, "residual_stride": K + 3, **at}
+        wanted += [(base, True), ({**base, "y_stride": 1027}, False),
+                   ({**base, "sum_stride": 1027}, False),
+                   ({**base, "y_stride": 1056}, True),  # 33 half lines
+                   ({**base, "sum": v.P + 32}, False), ({**base, "codes_stride": 1027}, K > 512),
+                   ({**base, "codes_stride": 1027, **codes}, True),
+                   ({**base, "y": None, "y_stride": 1027}, True)]
+    for (args, yes), r in zip(wanted, calls(*[("moe_norm_rows", args) for args, _ in wanted])):
+        (kernel, *_), = r["launches"]
+        assert (streams in kernel) == yes, (args, kernel)
+
+
 def test_groups_that_all_stay_are_no_groups(calls):
     """The same kernel as without groups, whatever their size."""
     same = calls(("moe_route_tokens", v.route_args(9, 100, 4, 1, 1, 1, "fp32")),
