@@ -58,6 +58,20 @@ def adapts(kind):
     return out
 
 
+# Rows to a tile, rows of each adapter, rows without one, K, N, rank: the tiles (each adapter's rounded up)
+# are a few more than a multiple of the 256 CUs, and K is long enough beside N that the channels of a
+# tile are not shared out otherwise.  Every kernel, and more than 64 adapters
+ADAPT_RESTS = [
+    (16, [1500, 1300, 1400], 7, 700, 1100, 10), (16, [43] * 100, 40, 500, 800, 16),
+    (16, [2] * 300, 100, 2600, 600, 16),
+    (16, [700, 900, 1, 1100, 1480], 5, 400, 600, 24), (16, [2] * 300, 100, 2600, 600, 32),
+    (32, [3000, 17, 2500, 4000, 3500, 33, 3450], 0, 200, 600, 32),
+    (16, [1100, 1000, 900, 1200], 0, 300, 600, 49), (16, [3] * 300, 120, 1000, 520, 64),
+    (32, [1000, 900, 1100, 700, 800, 1200, 850, 950, 800], 30, 330, 600, 64),
+    (32, [1840] * 9, 80, 1000, 1024, 64),  # above 80 MiB
+    (16, [1100, 1000, 900, 1200], 11, 300, 600, 128), (16, [15, 16, 17, 18] * 45, 60, 500, 600, 100)]
+
+
 def adapt_args(M, K, N, rank, adapters, kind):
     return dict(x=P, x_stride=K, type=TYPE[kind], M=M, K=K, a=P, a_stride=K, b=P, b_stride=rank, N=N,
                 rank=rank, scale=P, adapters=adapters, offsets=P, order=P, base=P, base_stride=N,

@@ -5,6 +5,7 @@ parts that x A^T is split into (bf16: 2^-17 relative to each; fp16: 2^-22 of the
 eps_t / 2 for the output's own rounding."""
 import pytest
 
+import more_ops_variants as v
 from test_gpu_ops import KINDS, U32, _gen, _half_ulp, _matrix, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -205,3 +206,56 @@ def test_values(env, kind):
     big = ref.abs() > 0.999 * torch.finfo(types[kind]).max  # of fp16: rounded to infinity
     got, ref = torch.where(big, 0.0, got.double()), torch.where(big, 0.0, ref)
     _check(env, None, got, ref, tol, has & ~bad, kind)
+
+
+def _whole(env, seed, M, K, N, rank, adapters, kind, pad=0):
+    """Operands of small whole numbers, whose products and sums are exact in fp32 (and x A^T in the parts
+    that it is split into, 16 bits at least): only the output is rounded."""
+    torch, m, types, tid = env
+    g = _gen(torch, seed)
+
+    def matrix(rows, cols, most):
+        wide = torch.randint(-most, most + 1, (rows, cols + pad), generator=g, device="cuda")
+        return wide.to(types[kind])[:, :cols]
+    scale = 2.0 ** torch.randint(-1, 2, (adapters,), generator=g, device="cuda")
+    return (matrix(M, K, 2), matrix(adapters * rank, K, 1), matrix(adapters * N, rank, 1),
+            matrix(M, N, 9), scale.float())
+
+
+def _check_whole(env, x, a, b, base, scale, ids, adapters, rank, kind):
+    torch, m, types, tid = env
+    ref, _, has = _ref(torch, x, a, b, base, scale, ids, adapters, rank, kind)
+    plan = _plan(env, ids, adapters)
+    _, out = _run(env, x, a, b, base, scale, plan, adapters, rank, kind)
+    want = torch.where(has[:, None], ref.to(types[kind]), 77.0)
+    assert torch.equal(out, want), torch.nonzero(out != want)[:4].tolist()
+    own = base.clone()
+    _run(env, x, a, b, own, scale, plan, adapters, rank, kind, out=own)
+    assert torch.equal(own, torch.where(has[:, None], ref.to(types[kind]), base))
+
+
+@pytest.mark.parametrize("rank", [1, 7, 8, 16, 17, 24, 32, 40, 64, 65, 127, 128])
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_element_counts(env, kind, rank):
+    """Whole numbers, bit for bit: of rows around the steps that a wave or all of them take at a time, no
+    element may be left out or taken twice."""
+    torch = env[0]
+    for K in (1, 7, 9, 31, 33, 64, 65, 127, 255, 257, 520, 1023, 2049, 4099, 6145, 7000):
+        M, N, adapters = 19, 133, 2
+        ids = _ids(torch, K, M, adapters, 0.1, 4)
+        _check_whole(env, *_whole(env, K + rank, M, K, N, rank, adapters, kind, K % 3), ids, adapters,
+                     rank, kind)
+
+
+@pytest.mark.parametrize("tile,rows,none,K,N,rank", v.ADAPT_RESTS)
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_left_over(env, kind, tile, rows, none, K, N, rank):
+    """Tiles beyond a multiple of the CUs, whose channels are shared out: whole numbers, bit for bit."""
+    torch = env[0]
+    adapters = len(rows)
+    counts = torch.tensor(rows + [none], device="cuda")
+    ids = torch.repeat_interleave(torch.arange(adapters + 1, device="cuda"), counts)
+    ids = ids[torch.randperm(ids.numel(), generator=_gen(torch, K), device="cuda")]
+    ids = torch.where(ids == adapters, -1, ids).to(torch.int32)
+    M = ids.numel()
+    _check_whole(env, *_whole(env, M, M, K, N, rank, adapters, kind), ids, adapters, rank, kind)

@@ -97,3 +97,27 @@ def test_variants_reach_every_kernel(calls):
     assert len(kernels) > 90
     missed = sorted(kernels - reached)
     assert not missed, (len(missed), missed)
+
+
+def test_adapters_tiles_left_over(calls):
+    """Those cases have one workgroup for all channels of a tile, tiles left over beside those that every
+    CU has had, and workgroups for the parts that they are shared out into."""
+    wanted = []
+    for kind in v.KINDS:
+        for tile, rows, none, K, N, rank in v.ADAPT_RESTS:
+            M = sum(rows) + none
+            wanted.append((tile, rows, M, N, v.adapt_args(M, K, N, rank, len(rows), kind)))
+    reached = set()
+    for (tile, rows, M, N, args), r in zip(wanted, calls(*[("moe_adapt_rows", w[4])
+                                                           for w in wanted])):
+        (kernel, x, y, threads, _), = r["launches"]
+        RT, MT, UC, W = map(int, re.search(r"Li(\d)ELi(\d)ELi(\d)ELi(\d)E", kernel).groups())
+        reached.add((RT, MT, W))
+        total = sum(-(-n // tile) for n in rows)
+        rest = total % 256
+        assert tile == 16 * MT and y == 1 and total > 256 and 1 <= rest <= 128 and N >= 512, args
+        parts = min(256 // rest, N // 256)
+        # eight dies: whole rounds of them, and every part of a tile on one of them
+        assert parts > 1 and x >= total - rest + -(-rest // 8) * 8 * parts, args
+    assert reached == {(1, 1, 4), (1, 1, 8), (2, 1, 4), (2, 1, 8), (2, 2, 4), (4, 1, 4), (4, 1, 8),
+                       (4, 2, 4), (8, 1, 4)}
