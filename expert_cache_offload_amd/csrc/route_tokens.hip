@@ -6,9 +6,13 @@
 // of their experts the k largest c are chosen, ties to the lower id.  Weights: s of the chosen,
 // divided by their sum or not, times a factor.
 //
-// A wave takes a token; a lane holds NPL neighbouring experts, so that among equal values the first
-// lane of a ballot has the lowest id.  One read of the logits, k rounds of a wave-wide maximum:
-// bound by instructions, not by bytes.
+// A lane holds neighbouring experts.  Up to 512 experts and 15 choices four tokens share a wave, 16
+// lanes each: one read of the logits, k + 2 rounds of a maximum over the lanes on keys that hold the
+// expert's id.  Other sizes, and tokens that these keys cannot decide, take a wave each, in which the
+// first lane of a ballot has the lowest id among equal values.  Both are bound by instructions, not by
+// bytes: 16384 tokens of 128 bf16 logits and 8 choices 6.9 us (560 vector instructions for four tokens, 3.7
+// us of the SIMDs' time, behind the launch and the read), of 256 fp32 logits with a bias 14 in groups;
+// a wave to a token, of 256 with 16 choices 34, of 1024 with 8 choices 89.
 #include <algorithm>
 
 #include "row_ops.h"
@@ -16,7 +20,7 @@
 namespace moe {
 namespace {
 
-constexpr int RT_T = 256;  // threads, a wave per token
+constexpr int RT_T = 256;  // threads of a workgroup
 constexpr int kMaxChoices = 16;
 constexpr int kMaxRouted = 1024;
 constexpr int kMaxRouteGroups = 64;
@@ -251,7 +255,7 @@ __device__ __forceinline__ void load_logits(float (&z)[NPL], const E* row, int l
     if (lane * NPL + i < n) z[i] = to_f32(row[lane * NPL + i]);
 }
 
-// Logit of choice e; 64-bit score arithmetic on the few chosen.
+// Sigmoid of a logit in 64 bits: for the chosen, which are few.
 template <class E>
 __device__ __forceinline__ double sigmoid_f64(E z) {
   return 1.0 / (1.0 + exp(-(double)z));
@@ -606,7 +610,9 @@ struct RouteGradArgs {
 // dz_j = f s_j (1 - s_j) dw_j; softmax dz_e = f p_e (dw_e - sum_j p_j dw_j) for every expert (dw_e = 0
 // where e was not chosen), otherwise 0.  The chosen are few: 64 bits, four tokens to a wave, 16 lanes
 // each.  A token's row is put together in LDS (the logits of the others are read where softmax needs
-// them, their exponentials held there in fp32) and written in 16-byte pieces.
+// them, their exponentials held there in fp32) and written in 16-byte pieces.  16384 tokens of 256 fp32
+// logits: 6.8 us, softmax that is not renormalised 14.5 (its 64-bit exponentials of every expert; bytes
+// at a copy's rate 6.3).
 template <class E>
 __global__ __launch_bounds__(RT_T) void route_tokens_grad_kernel(RouteGradArgs a, int pitch) {
   constexpr int V = kChunk<E>;
